@@ -36,6 +36,8 @@
  *    the ranks' gradient slices, the copy-and-norm pass, the combine of the
  *    ranks' scalars, and the step on host cores (whose worker threads start
  *    on first use and live until the process ends);
+ *  - the step with its moments in 8 bits (zero_shard_adam8_step*,
+ *    zero_moments8_*), and the step over a list of tensors (zero_multi_*);
  *  - physically contiguous memory (zero_device_alloc_contiguous, zero_pool_*),
  *    whose purpose is to allocate, and the measurement copies
  *    (zero_copy_reference, zero_copy_widen_reference on the device,
@@ -556,6 +558,165 @@ int zero_shard_grad_sum_norm_dev(float* acc, const void* const* slices, int32_t 
                                  int64_t n, int32_t add_to_acc, const zero_adam_hyper* hp,
                                  zero_step_state* d_state, double* d_sqnorm, int32_t* d_overflow, void* d_coef,
                                  void* d_workspace, size_t workspace_bytes, void* hip_stream);
+
+/* ---------------------------------------------------------------------------
+ * Extra: the step with its moments in 8 bits (2.06 bytes a parameter instead
+ * of 8).  The explainer's "16 Bytes per Parameter Audit" counts two fp32 Adam
+ * moments per parameter; this form holds them in a block-scaled 8-bit format.
+ *
+ * Format.  Elements form blocks of 32 (the last may be partial).  exp_avg and
+ * the square root s of exp_avg_sq are each stored as an 8-bit OCP e4m3 code
+ * times 2^k, one k per block and moment:
+ *     k = max(floor(log2(largest magnitude of the block)) - 7, -126)
+ * (-126 for a block of zeros).  Positive s below 2^(k-9) is taken as 2^(k-9),
+ * the smallest code.
+ *  moments8  device, zero_moments8_bytes(n) = 8 ceil(n/4) bytes: for each four
+ *            consecutive elements, four codes of exp_avg then four of s (zero
+ *            codes where there is no element)
+ *  scales8   device, zero_scales8_bytes(n) = 2 ceil(n/32) bytes: for each
+ *            block the byte k + 127 of exp_avg, then that of s
+ * All bytes zero is a valid state: both moments zero.
+ *
+ * The update is the one of zero_shard_adam_step, in the same float32
+ * operation order, with m = code * 2^k, s0 = code * 2^k and
+ *     v = fma(B2, s0 * s0, (O2*g)*g);  s = sqrt(v);  d = fma(s, RB, E);
+ * m and s are then stored: rounded stochastically, so that changes smaller
+ * than half a code survive on average.  A value x becomes
+ *     q * floor(|x| / q + u / 2^20), with the sign of x,
+ * where q is the code spacing at x (2^(k-9) times max(1, the power of two
+ * that spaces the codes there)) and u are the upper 20 bits of a 32-bit word.
+ * With a = the step's key, e the element's index and all arithmetic modulo
+ * 2^32 the word is x5 for exp_avg and x5 rotated by 16 bits for s, where
+ *     a  = key + tensor * 0x3C6EF373 + (e >> 32) * 0xA54FF53B  (tensor 0 here)
+ *     x1 = (e & 0xFFFFFFFF) ^ a;  x2 = (x1 ^ (x1 >> 16)) * 0x9E3779B9;
+ *     x4 = (x2 ^ (x2 >> 13)) * 0xBB67AE85;  x5 = x4 ^ (x4 >> 16)
+ * and, modulo 2^64, key is the lower half of K2 ^ (K2 >> 32), with
+ *     K0 = seed * 0x9E3779B97F4A7C15 + t * 0xBB67AE8584CAA73B,
+ *     K2 = (K0 ^ (K0 >> 32)) * 0x6A09E667F3BCC909.
+ * A step is thus reproducible bit for bit from its inputs, seed and t.
+ * A moment that becomes inf or NaN is stored as NaN, and its block's scale and
+ * other codes are then unspecified; with d_global_overflow given such a step
+ * is skipped.
+ *
+ * zero_shard_adam8_step: as zero_shard_adam_step (pointers 16-byte aligned,
+ *   the same skip, clip and aliasing rules); t = hp->step keys the rounding.
+ * zero_shard_adam8_step_coef: as zero_shard_adam_step_coef; t is read from
+ *   d_step (device int64, 8-byte aligned) when the kernel runs, for instance
+ *   &d_state->applied after the step's decision, which then equals t.
+ *   d_coef, d_step, the norm and the flag must not lie in a written buffer.
+ * zero_moments8_pack: codes from fp32 moments, each rounded to nearest even
+ *   (exp_avg_sq >= 0; its root is formed in float32).
+ * zero_moments8_unpack: fp32 moments from codes: exp_avg = code * 2^k, exact,
+ *   and exp_avg_sq = (code * 2^k)^2, rounded once.
+ * Streams 16.125 bytes per element with 16-bit gradient and copy (18.125 with
+ * an fp32 gradient, 2 less without a copy); pack and unpack 10.06.
+ * Errors: ZERO_EINVAL, ZERO_EALIGN, ZERO_ERANGE, ZERO_EHIP.
+ * ------------------------------------------------------------------------- */
+size_t zero_moments8_bytes(int64_t n);
+size_t zero_scales8_bytes(int64_t n);
+int zero_shard_adam8_step(float* master, void* moments8, void* scales8, const void* grad, int32_t grad_dtype,
+                          void* param_out, int32_t param_dtype, int64_t n, const zero_adam_params* hp, uint64_t seed,
+                          const double* d_global_sqnorm, const int32_t* d_global_overflow, void* hip_stream);
+int zero_shard_adam8_step_coef(float* master, void* moments8, void* scales8, const void* grad, int32_t grad_dtype,
+                               void* param_out, int32_t param_dtype, int64_t n, const void* d_coef, uint64_t seed,
+                               const int64_t* d_step, const double* d_global_sqnorm, const int32_t* d_global_overflow,
+                               void* hip_stream);
+int zero_moments8_pack(void* moments8, void* scales8, const float* exp_avg, const float* exp_avg_sq, int64_t n,
+                       void* hip_stream);
+int zero_moments8_unpack(float* exp_avg, float* exp_avg_sq, const void* moments8, const void* scales8, int64_t n,
+                         void* hip_stream);
+
+/* ---------------------------------------------------------------------------
+ * Extra: the step over a list of tensors, each with its own buffers, element
+ * types and hyperparameter group: a model's parameters as they were allocated,
+ * or the fragments of a rank's shard (zero_rank_fragments) where norms and
+ * biases take no weight decay.  One launch updates the whole list.
+ *
+ * zero_tensor, one per tensor:
+ *  master      device, [numel] float32, updated in place
+ *  exp_avg, exp_avg_sq  with state_bits 32: device, [numel] float32; with
+ *              state_bits 8: the tensor's own moments8 and scales8 (blocks
+ *              count from the tensor's first element)
+ *  grad        device, [numel] of grad_dtype, read only
+ *  param_out   device, [numel] of param_dtype, or NULL (no copy)
+ *  group       index into the step's hyperparameters, [0, ZERO_MAX_GROUPS)
+ * Pointers need only be aligned to their elements (moments8: 8 bytes).  A
+ * tensor may be empty.  Gradients may share memory with one another; no
+ * written buffer may overlap another buffer of the list.
+ *
+ * zero_multi_table_build (host only) writes the table of the list to host
+ * memory at `table`, which the caller keeps as long as it steps the list, and
+ * sets *bytes (size of the table) and *device_bytes.  The caller copies the
+ * first *device_bytes bytes to device memory, 16-byte aligned, and passes both
+ * to the calls below.  With table NULL or capacity below *bytes it writes
+ * only the sizes and returns ZERO_ENOSPC.  state_bits is 32, 8, or 0 for a
+ * table of gradients only (the norm pass; other fields ignored).  About 8
+ * bytes per 8192 elements and 80 per tensor.  A list whose buffers move needs
+ * a new table (the device copy must not change under a step in flight).
+ *
+ * zero_multi_unscale_norm_overflow: as zero_shard_unscale_norm_overflow over
+ *   all gradients of the list.  d_tensor_sqnorm (device, [n_tensors] double,
+ *   or NULL) receives each tensor's own sum of squares (unscaled; 0 for an
+ *   empty tensor).  The sums are taken in float64 in a fixed order that
+ *   depends only on the sizes.
+ *   Workspace: zero_multi_norm_workspace_bytes(table) bytes (0 if table is
+ *   not a table).
+ * zero_multi_adam_step: as zero_shard_adam_step (state_bits 32) or
+ *   zero_shard_adam8_step (state_bits 8) on every tensor, with hp[group] of
+ *   n_groups hyperparameter sets; the random bits of tensor i are those of
+ *   `tensor` = i above, keyed by hp[group].step.  Element by element the
+ *   results equal the shard calls' bit for bit (8 bits: for tensor 0).  seed
+ *   is unused with 32 bits.
+ * zero_multi_adam_step_coef: coefficients from device memory, an array of
+ *   n_groups blocks of zero_adam_coef_bytes() bytes; d_global_sqnorm is
+ *   required, and d_step with 8-bit moments (see zero_shard_adam8_step_coef).
+ * zero_multi_decide_dev: as zero_step_decide_dev for n_groups sets (their
+ *   blocks to d_coefs, in order).  unscaled nonzero: the gradients are already
+ *   unscaled (inv_loss_scale 1), whatever their type; zero: all of them are
+ *   multiplied by 1/scale, fp32 ones too.
+ * zero_multi_unscale_norm_overflow_dev: the norm pass with 1/scale from
+ *   d_state.  zero_multi_norm_decide_dev: that and the decision of a single
+ *   rank, as zero_shard_norm_decide_dev.
+ * An empty list is valid: the norm is 0, the update does nothing, the decision
+ * is made.
+ * Errors: ZERO_EINVAL, ZERO_EALIGN, ZERO_ERANGE, ZERO_ENOSPC, ZERO_EHIP.
+ * ------------------------------------------------------------------------- */
+#define ZERO_MAX_GROUPS 16
+
+typedef struct {
+    float* master;
+    void* exp_avg;
+    void* exp_avg_sq;
+    const void* grad;
+    void* param_out;
+    int64_t numel;
+    int32_t grad_dtype, param_dtype;
+    int32_t group;
+    int32_t reserved;       /* 0 */
+} zero_tensor;
+
+int zero_multi_table_build(const zero_tensor* tensors, int32_t n_tensors, int32_t state_bits, void* table,
+                           size_t capacity, size_t* bytes, size_t* device_bytes);
+size_t zero_multi_norm_workspace_bytes(const void* table);
+int zero_multi_unscale_norm_overflow(const void* table, const void* d_table, double inv_loss_scale, double* d_sqnorm,
+                                     int32_t* d_overflow, double* d_tensor_sqnorm, void* d_workspace,
+                                     size_t workspace_bytes, void* hip_stream);
+int zero_multi_unscale_norm_overflow_dev(const void* table, const void* d_table, int32_t unscaled,
+                                         const zero_step_state* d_state, double* d_sqnorm, int32_t* d_overflow,
+                                         double* d_tensor_sqnorm, void* d_workspace, size_t workspace_bytes,
+                                         void* hip_stream);
+int zero_multi_norm_decide_dev(const void* table, const void* d_table, int32_t unscaled, const zero_adam_hyper* hp,
+                               int32_t n_groups, zero_step_state* d_state, double* d_sqnorm, int32_t* d_overflow,
+                               double* d_tensor_sqnorm, void* d_coefs, void* d_workspace, size_t workspace_bytes,
+                               void* hip_stream);
+int zero_multi_decide_dev(const zero_adam_hyper* hp, int32_t n_groups, int32_t unscaled, zero_step_state* d_state,
+                          const int32_t* d_global_overflow, void* d_coefs, void* hip_stream);
+int zero_multi_adam_step(const void* table, const void* d_table, const zero_adam_params* hp, int32_t n_groups,
+                         uint64_t seed, const double* d_global_sqnorm, const int32_t* d_global_overflow,
+                         void* hip_stream);
+int zero_multi_adam_step_coef(const void* table, const void* d_table, const void* d_coefs, int32_t n_groups,
+                              uint64_t seed, const int64_t* d_step, const double* d_global_sqnorm,
+                              const int32_t* d_global_overflow, void* hip_stream);
 
 /* ---------------------------------------------------------------------------
  * Extra, a measurement aid (not a step of the method): a plain device copy, one

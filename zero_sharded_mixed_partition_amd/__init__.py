@@ -16,6 +16,9 @@ in the library's kernels.
     zero_cpu_shard_unscale_norm_overflow(grad, inv_loss_scale) -> (sq, overflow)      host memory
     zero_cpu_shard_adam_step(master, exp_avg, exp_avg_sq, grad, param_out, hp, sq, overflow)  host memory
     zero_loss_scaler_update(scaler, overflow) -> skip
+
+moments8.py adds the shard's step with 8-bit moments, multi.py the step over a
+list of tensors.
 """
 import ctypes
 from typing import List, Optional, Sequence, Tuple
@@ -37,7 +40,11 @@ __all__ = ["zero_partition_plan", "zero_rank_fragments", "zero_norm_workspace_by
            "zero_shard_grad_accumulate_dev", "zero_shard_grad_reduce_dev", "zero_step_decide_dev",
            "zero_shard_norm_decide_dev", "StepGraphDev", "zero_sum_norm_workspace_bytes", "zero_shard_grad_sum_norm",
            "zero_shard_grad_sum_norm_dev", "zero_device_alloc_contiguous", "zero_device_free",
-           "zero_pool_counts", "contiguous_pool"]
+           "zero_pool_counts", "contiguous_pool", "zero_moments8_bytes", "zero_scales8_bytes", "zero_moments8_pack",
+           "zero_moments8_unpack", "zero_shard_adam8_step", "zero_shard_adam8_step_coef", "TensorTable", "MAX_GROUPS",
+           "zero_multi_norm_workspace_bytes", "zero_multi_unscale_norm_overflow",
+           "zero_multi_unscale_norm_overflow_dev", "zero_multi_norm_decide_dev", "zero_multi_decide_dev",
+           "zero_multi_adam_step", "zero_multi_adam_step_coef"]
 
 
 def zero_abi_version() -> int:
@@ -628,6 +635,11 @@ def zero_loss_scaler_update(scaler: LossScaler, overflow: bool) -> bool:
     return bool(skip.value)
 
 
+from .moments8 import (zero_moments8_bytes, zero_moments8_pack, zero_moments8_unpack,  # noqa: E402
+                       zero_scales8_bytes, zero_shard_adam8_step, zero_shard_adam8_step_coef)
+from .multi import (MAX_GROUPS, TensorTable, zero_multi_adam_step, zero_multi_adam_step_coef,  # noqa: E402
+                    zero_multi_decide_dev, zero_multi_norm_decide_dev, zero_multi_norm_workspace_bytes,
+                    zero_multi_unscale_norm_overflow, zero_multi_unscale_norm_overflow_dev)
 from .shard import ShardAdam  # noqa: E402
 from .offload import OffloadShardAdam  # noqa: E402
 from . import checkpoint  # noqa: E402,F401

@@ -43,6 +43,14 @@ class zero_step_state(ctypes.Structure):
                 ("reserved", c_i32)]
 
 
+class zero_tensor(ctypes.Structure):
+    _fields_ = [("master", c_vp), ("exp_avg", c_vp), ("exp_avg_sq", c_vp), ("grad", c_vp), ("param_out", c_vp),
+                ("numel", c_i64), ("grad_dtype", c_i32), ("param_dtype", c_i32), ("group", c_i32), ("reserved", c_i32)]
+
+
+c_u64 = ctypes.c_uint64
+P_sz = ctypes.POINTER(c_sz)
+
 # name -> (restype, argtypes); every symbol the header declares
 SIGNATURES = {
     "zero_abi_version": (c_i32, []),
@@ -94,6 +102,23 @@ SIGNATURES = {
                                          ctypes.POINTER(zero_adam_hyper), c_vp, c_vp, c_vp, c_vp, c_vp]),
     "zero_shard_grad_accumulate_dev": (c_i32, [c_vp, c_vp, c_i32, c_i64, c_vp, c_i32, c_vp, c_vp]),
     "zero_shard_grad_reduce_dev": (c_i32, [c_vp, ctypes.POINTER(c_vp), c_i32, c_i32, c_i64, c_vp, c_vp, c_vp]),
+    "zero_moments8_bytes": (c_sz, [c_i64]),
+    "zero_scales8_bytes": (c_sz, [c_i64]),
+    "zero_shard_adam8_step": (c_i32, [c_vp, c_vp, c_vp, c_vp, c_i32, c_vp, c_i32, c_i64,
+                                      ctypes.POINTER(zero_adam_params), c_u64, c_vp, c_vp, c_vp]),
+    "zero_shard_adam8_step_coef": (c_i32, [c_vp, c_vp, c_vp, c_vp, c_i32, c_vp, c_i32, c_i64, c_vp, c_u64, c_vp, c_vp,
+                                           c_vp, c_vp]),
+    "zero_moments8_pack": (c_i32, [c_vp, c_vp, c_vp, c_vp, c_i64, c_vp]),
+    "zero_moments8_unpack": (c_i32, [c_vp, c_vp, c_vp, c_vp, c_i64, c_vp]),
+    "zero_multi_table_build": (c_i32, [ctypes.POINTER(zero_tensor), c_i32, c_i32, c_vp, c_sz, P_sz, P_sz]),
+    "zero_multi_norm_workspace_bytes": (c_sz, [c_vp]),
+    "zero_multi_unscale_norm_overflow": (c_i32, [c_vp, c_vp, c_dbl, c_vp, c_vp, c_vp, c_vp, c_sz, c_vp]),
+    "zero_multi_unscale_norm_overflow_dev": (c_i32, [c_vp, c_vp, c_i32, c_vp, c_vp, c_vp, c_vp, c_vp, c_sz, c_vp]),
+    "zero_multi_norm_decide_dev": (c_i32, [c_vp, c_vp, c_i32, ctypes.POINTER(zero_adam_hyper), c_i32, c_vp, c_vp,
+                                           c_vp, c_vp, c_vp, c_vp, c_sz, c_vp]),
+    "zero_multi_decide_dev": (c_i32, [ctypes.POINTER(zero_adam_hyper), c_i32, c_i32, c_vp, c_vp, c_vp, c_vp]),
+    "zero_multi_adam_step": (c_i32, [c_vp, c_vp, ctypes.POINTER(zero_adam_params), c_i32, c_u64, c_vp, c_vp, c_vp]),
+    "zero_multi_adam_step_coef": (c_i32, [c_vp, c_vp, c_vp, c_i32, c_u64, c_vp, c_vp, c_vp, c_vp]),
     "zero_status_string": (ctypes.c_char_p, [c_i32]),
     "zero_last_error": (ctypes.c_char_p, []),
 }

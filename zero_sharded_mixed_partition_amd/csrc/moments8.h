@@ -1,0 +1,291 @@
+// AdamW moments held in 8 bits: the number format and the device code that
+// reads and writes it (gfx950).
+//
+// A tensor's elements form blocks of 32.  exp_avg (m) and the square root of
+// exp_avg_sq (s) are each stored as an OCP e4m3 code times a power of two per
+// block, value = code * 2^k, with k = floor(log2(largest magnitude of the
+// block)) - 7: the largest value lands in [128, 256), below e4m3's 448, so
+// rounding up never overflows, and the smallest code stands for 2^-16 to
+// 2^-17 of it.  Power-of-two scales make decoding exact, and gfx950 converts
+// two values with their scale in one instruction.  s instead of its square:
+// the update needs s itself, and the format's range of 2^17 below the block's
+// maximum then covers 2^34 of the second moment.  A positive s is stored as
+// at least the smallest code, so that m / (s + eps) cannot grow without bound
+// once s has become small beside its block.
+//
+// Rounding in the step is stochastic.  With beta2 = 0.999 the second moment
+// moves by about 0.1% a step and e4m3 codes are 6-12% apart, so rounding to
+// nearest would drop nearly every change (simulated on normal gradients over
+// 4,000 steps: s then settles at 0.38 of its true value; with stochastic
+// rounding at 1.01 of it, with a spread of 15% between elements).  The random
+// bits are a function of (seed, step, tensor, element) alone, so a step is
+// reproducible bit for bit.
+//
+// Layout: codes in quads of 8 bytes, four of m then four of s, and the two
+// exponent bytes (k + 127) of a block side by side.  A lane that owns four
+// consecutive elements reads and writes one 8-byte word of codes, and eight
+// lanes share a block.
+#pragma once
+#include "stream.h"
+
+namespace zero_shard {
+namespace {
+
+constexpr int kBlock8 = 32;                      // elements per scale
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef short s16x2 __attribute__((ext_vector_type(2)));
+
+// Pointers read from a table are generic ones to the compiler; naming the
+// address space keeps the accesses global (flat ones count against the LDS
+// too), and the table's own reads scalar.
+#define ZS_GLOBAL __attribute__((address_space(1)))
+#define ZS_CONSTANT __attribute__((address_space(4)))
+
+template <typename T>
+__device__ __forceinline__ ZS_GLOBAL T* global(T* p) {
+    return (ZS_GLOBAL T*)p;
+}
+
+// fp32 and 16-bit vectors at the alignment of their element: tensors of a list
+// may start anywhere.  The hardware takes 8- and 16-byte accesses at any
+// address, so an aligned tensor costs nothing extra.
+typedef f32x4 f32x4_any __attribute__((aligned(4)));
+typedef u32x2 u32x2_any __attribute__((aligned(2)));
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+
+__device__ __forceinline__ f32x4 ld_any(const float* p) {
+    return __builtin_nontemporal_load((const ZS_GLOBAL f32x4_any*)p);
+}
+__device__ __forceinline__ u32x2 ld_any(const uint16_t* p) {
+    return __builtin_nontemporal_load((const ZS_GLOBAL u32x2_any*)p);
+}
+__device__ __forceinline__ u32x4 ld16_any(const void* p) {
+    return __builtin_nontemporal_load((const ZS_GLOBAL u32x4_any*)p);
+}
+__device__ __forceinline__ u32x2 ld_codes(const u32x2* p) {
+    return __builtin_nontemporal_load((const ZS_GLOBAL u32x2*)p);
+}
+__device__ __forceinline__ void st_any(f32x4 v, float* p) {
+    __builtin_nontemporal_store(v, (ZS_GLOBAL f32x4_any*)p);
+}
+__device__ __forceinline__ void st_any(u32x2 v, uint16_t* p) {
+    __builtin_nontemporal_store(v, (ZS_GLOBAL u32x2_any*)p);
+}
+__device__ __forceinline__ void st_codes(u32x2 v, u32x2* p) { __builtin_nontemporal_store(v, (ZS_GLOBAL u32x2*)p); }
+
+// One gradient value, and four consecutive ones as loaded and as values.
+template <int DT>
+__device__ __forceinline__ float ld_grad1(const void* G, int64_t e) {
+    if constexpr (DT == ZERO_F32) {
+        return global(static_cast<const float*>(G))[e];
+    } else {
+        const uint32_t h = global(static_cast<const uint16_t*>(G))[e];
+        return DT == ZERO_F16 ? f16_to_f32(h) : bf16_to_f32(h);
+    }
+}
+
+template <int DT>
+struct Grad4 {
+    u32x2 w;
+    __device__ __forceinline__ void load(const void* G, int64_t e) { w = ld_any(static_cast<const uint16_t*>(G) + e); }
+    __device__ __forceinline__ void values(float g[4]) const {
+        unpack2<DT>(w[0], g[0], g[1]);
+        unpack2<DT>(w[1], g[2], g[3]);
+    }
+};
+template <>
+struct Grad4<ZERO_F32> {
+    f32x4 w;
+    __device__ __forceinline__ void load(const void* G, int64_t e) { w = ld_any(static_cast<const float*>(G) + e); }
+    __device__ __forceinline__ void values(float g[4]) const {
+        for (int j = 0; j < 4; ++j) g[j] = w[j];
+    }
+};
+
+template <int DT>
+__device__ __forceinline__ u32x2 pack4_16(const float p[4]) {
+    u32x2 o;
+    o[0] = to16<DT>(p[0]) | (to16<DT>(p[1]) << 16);
+    o[1] = to16<DT>(p[2]) | (to16<DT>(p[3]) << 16);
+    return o;
+}
+
+// ---------------------------------------------------------------- random bits
+
+// 32-bit key of one step: the seed and the step mixed by multiplication and
+// shifts, modulo 2^64.  Host and device form it alike.
+ZS_HD inline uint32_t dither_key(uint64_t seed, uint64_t step) {
+    uint64_t k = seed * 0x9E3779B97F4A7C15ull + step * 0xBB67AE8584CAA73Bull;
+    k ^= k >> 32;
+    k *= 0x6A09E667F3BCC909ull;
+    return (uint32_t)(k ^ (k >> 32));
+}
+
+// the key of one tensor of a list (0 for a shard) and the upper half of the element index
+__device__ __forceinline__ uint32_t dither_tensor(uint32_t key, uint32_t tensor, int64_t e) {
+    return key + tensor * 0x3C6EF373u + (uint32_t)(e >> 32) * 0xA54FF53Bu;
+}
+
+// 32 random bits of the element whose index has the lower half e: two rounds
+// of multiply and shift (every input bit flips every output bit with
+// probability 0.5 +- 0.01).  m takes the upper 20 bits of them, s those of the
+// word rotated by half.
+__device__ __forceinline__ uint32_t dither_bits(uint32_t e, uint32_t key) {
+    uint32_t x = e ^ key;
+    x ^= x >> 16;
+    x *= 0x9E3779B9u;
+    x ^= x >> 13;
+    x *= 0xBB67AE85u;
+    return x ^ (x >> 16);
+}
+
+__device__ __forceinline__ uint32_t rotate16(uint32_t x) { return (x << 16) | (x >> 16); }
+
+// ---------------------------------------------------------------- codes
+
+// The largest of 8 lanes' values (the lanes of one block), in all of them.
+__device__ __forceinline__ uint32_t max_of_block(uint32_t x) {
+    const auto other = [](uint32_t v, auto ctrl) {
+        return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, decltype(ctrl)::value, 0xF, 0xF, true);
+    };
+    uint32_t y = other(x, std::integral_constant<int, 0xB1>{});      // lane ^ 1
+    x = x > y ? x : y;
+    y = other(x, std::integral_constant<int, 0x4E>{});               // lane ^ 2
+    x = x > y ? x : y;
+    y = other(x, std::integral_constant<int, 0x141>{});              // 7 - lane, within each 8
+    return x > y ? x : y;
+}
+
+// Exponent byte (k + 127) of a block whose largest magnitude has these bits.
+__device__ __forceinline__ uint32_t scale_byte(uint32_t top_bits) {
+    const uint32_t e = top_bits >> 23;
+    return (e > 8u ? e : 8u) - 7u;
+}
+
+__device__ __forceinline__ float scale_of(uint32_t byte) { return __uint_as_float(byte << 23); }
+
+// four codes to float32, times the scale (exact)
+__device__ __forceinline__ void decode4(uint32_t codes, float scale, float x[4]) {
+    const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8((int)codes, scale, false);
+    const f32x2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8((int)codes, scale, true);
+    x[0] = a[0];
+    x[1] = a[1];
+    x[2] = b[0];
+    x[3] = b[1];
+}
+
+__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
+
+__device__ __forceinline__ uint32_t top_of4(const float x[4]) {
+    uint32_t t = abs_bits(x[0]);
+    for (int j = 1; j < 4; ++j) t = t > abs_bits(x[j]) ? t : abs_bits(x[j]);
+    return max_of_block(t);
+}
+
+// a positive root is at least the smallest code
+__device__ __forceinline__ float floor_root(float s, float smallest) {
+    return (s > 0.0f && s < smallest) ? smallest : s;
+}
+
+// Four values to codes.  The conversion with random bits adds the upper 20 of
+// them below the last place of the code (of the smallest code's place for
+// values below the normal range) and truncates: checked on every exponent
+// against that definition.
+__device__ __forceinline__ uint32_t encode4_random(const float x[4], float scale, const uint32_t r[4]) {
+    uint32_t w = __builtin_amdgcn_cvt_scalef32_sr_fp8_f32(0, x[0], r[0], scale, 0);
+    w = __builtin_amdgcn_cvt_scalef32_sr_fp8_f32(w, x[1], r[1], scale, 1);
+    w = __builtin_amdgcn_cvt_scalef32_sr_fp8_f32(w, x[2], r[2], scale, 2);
+    return __builtin_amdgcn_cvt_scalef32_sr_fp8_f32(w, x[3], r[3], scale, 3);
+}
+
+__device__ __forceinline__ uint32_t encode4_nearest(const float x[4], float scale) {
+    s16x2 w = {0, 0};
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, x[0], x[1], scale, false);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, x[2], x[3], scale, true);
+    return __builtin_bit_cast(uint32_t, w);
+}
+
+// ---------------------------------------------------------------- one task of the step
+
+// One AdamW element on a decoded second-moment root: as adam_elem, and the
+// new root is what the denominator needs anyway.
+__device__ __forceinline__ void adam8_elem(const StepCoef& c, float gscale, float graw, float& p, float& m, float& s) {
+    const float g = graw * gscale;
+    m = fmaf(c.beta1, m, c.omb1 * g);
+    s = sqrtf(fmaf(c.beta2, s * s, (c.omb2 * g) * g));
+    const float denom = fmaf(s, c.rsqrt_bc2, c.eps);
+    p = fmaf(p, c.decay, -(c.step_size * m) / denom);
+}
+
+// Elements [base, base + 256) of one tensor, base a multiple of 256, by one
+// wave; lane l owns four consecutive elements.  WHOLE: all of them lie below
+// n; else the lanes past the end take part in the block maxima with zeros.
+// key: dither_tensor.  PDT 0: no 16-bit copy.
+template <int GDT, int PDT, bool WHOLE>
+__device__ __forceinline__ void adam8_quads(float* P, u32x2* C, uint16_t* S, const void* G, uint16_t* Pout, int64_t n,
+                                            int64_t base, const StepCoef& c, float gscale, uint32_t key) {
+    const int lane = threadIdx.x;
+    const int64_t e0 = base + 4 * lane;
+    const int here = WHOLE ? 4 : e0 >= n ? 0 : n - e0 < 4 ? (int)(n - e0) : 4;
+    float p[4] = {}, g[4] = {}, m[4], s[4];
+    u32x2 codes = {0, 0};
+    uint32_t scales = 0;
+    if constexpr (WHOLE) {
+        const f32x4 v = ld_any(P + e0);
+        codes = ld_codes(C + (e0 >> 2));
+        Grad4<GDT> gq;
+        gq.load(G, e0);
+        scales = global(S)[e0 >> 5];
+        gq.values(g);
+        for (int j = 0; j < 4; ++j) p[j] = v[j];
+    } else if (here > 0) {
+        codes = ld_codes(C + (e0 >> 2));
+        scales = global(S)[e0 >> 5];
+        for (int j = 0; j < 4; ++j) {
+            if (j < here) {
+                p[j] = global(P)[e0 + j];
+                g[j] = ld_grad1<GDT>(G, e0 + j);
+            }
+        }
+    }
+    decode4(codes[0], scale_of(scales & 0xFFu), m);
+    decode4(codes[1], scale_of(scales >> 8), s);
+    uint32_t r[4], q[4];
+    for (int j = 0; j < 4; ++j) {
+        if (j < here) adam8_elem(c, gscale, g[j], p[j], m[j], s[j]);
+        else m[j] = s[j] = 0.0f;
+        r[j] = dither_bits((uint32_t)(e0 + j), key);
+        q[j] = rotate16(r[j]);
+    }
+    const uint32_t mb = scale_byte(top_of4(m)), sb = scale_byte(top_of4(s));
+    const float smallest = __builtin_ldexpf(scale_of(sb), -9);
+    for (int j = 0; j < 4; ++j) s[j] = floor_root(s[j], smallest);
+    codes[0] = encode4_random(m, scale_of(mb), r);
+    codes[1] = encode4_random(s, scale_of(sb), q);
+    if constexpr (WHOLE) {
+        f32x4 v;
+        for (int j = 0; j < 4; ++j) v[j] = p[j];
+        st_any(v, P + e0);
+        st_codes(codes, C + (e0 >> 2));
+        if constexpr (PDT != 0) st_any(pack4_16<PDT>(p), Pout + e0);
+    } else if (here > 0) {
+        st_codes(codes, C + (e0 >> 2));
+        for (int j = 0; j < 4; ++j) {
+            if (j < here) {
+                global(P)[e0 + j] = p[j];
+                if constexpr (PDT != 0) global(Pout)[e0 + j] = (uint16_t)to16<PDT>(p[j]);
+            }
+        }
+    }
+    if ((lane & 7) == 0 && here > 0) global(S)[e0 >> 5] = (uint16_t)(mb | (sb << 8));
+}
+
+template <int GDT, int PDT>
+__device__ __forceinline__ void adam8_task(float* P, u32x2* C, uint16_t* S, const void* G, uint16_t* Pout, int64_t n,
+                                           int64_t base, const StepCoef& c, float gscale, uint32_t key) {
+    if (base + kTask <= n) adam8_quads<GDT, PDT, true>(P, C, S, G, Pout, n, base, c, gscale, key);
+    else adam8_quads<GDT, PDT, false>(P, C, S, G, Pout, n, base, c, gscale, key);
+}
+
+}  // namespace
+}  // namespace zero_shard
