@@ -19,6 +19,17 @@ namespace {
 
 constexpr int64_t kMaxGrid = (int64_t(1) << 26) - 1;
 
+// LDS that a workgroup reserves and never uses, to cap how many (one wave
+// each) are resident on a CU of 160 KiB, as for the fp32 update: with fewer
+// waves in competition HBM sustains more.  Measured on MI355X, 251M elements
+// with fp16 gradient and copy: 7 KiB (21 resident) 6.44 TB/s, 6 KiB 6.39, none
+// 6.32, 8.5 KiB 6.36, 10 KiB 6.13.  One task per wave: two reach 6.37 (at
+// 10 KiB), four 6.32 (14 KiB).
+constexpr size_t kLds8 = 7 * 1024;
+// pack8: 6 KiB (25 resident) 6.78 TB/s, 7 KiB 6.71, none 6.35; unpack8: 6.48,
+// 6.28 and 6.30 (251M elements).
+constexpr size_t kLdsConvert = 6 * 1024;
+
 dim3 task_grid(int64_t n) {
     const int64_t t = (n + kTask - 1) / kTask;
     return dim3((unsigned)(t < kMaxGrid ? t : kMaxGrid));
@@ -40,10 +51,9 @@ __global__ __launch_bounds__(kTaskThreads) void adam8_update(float* __restrict__
         c = *pc;
         key = dither_key(seed, (uint64_t)*d_step);
     }
-    const float gscale = clipped_scale(c, d_sq);
     const int64_t ntasks = (n + kTask - 1) / kTask;
     for (int64_t t = blockIdx.x; t < ntasks; t += gridDim.x)
-        adam8_task<GDT, PDT>(P, C, S, G, Pout, n, t * kTask, c, gscale, dither_tensor(key, 0, t * kTask));
+        adam8_task<GDT, PDT>(P, C, S, G, Pout, n, t * kTask, c, d_sq, dither_tensor(key, 0, t * kTask));
 }
 
 __global__ __launch_bounds__(kTaskThreads) void pack8(u32x2* __restrict__ C, uint16_t* __restrict__ S,
@@ -68,7 +78,7 @@ __global__ __launch_bounds__(kTaskThreads) void pack8(u32x2* __restrict__ C, uin
                 }
             }
         }
-        const uint32_t mb = scale_byte(top_of4(m)), sb = scale_byte(top_of4(s));
+        const uint32_t mb = scale_byte(top_of_block(m)), sb = scale_byte(top_of_block(s));
         const float smallest = __builtin_ldexpf(scale_of(sb), -9);
         for (int j = 0; j < 4; ++j) s[j] = floor_root(s[j], smallest);
         if (e0 < n) {
@@ -151,11 +161,11 @@ void launch8(hipStream_t st, float* P, void* C, void* S, const void* G, void* Po
              uint32_t key, uint64_t seed, const StepCoef* pc, const int64_t* d_step, const double* d_sq,
              const int32_t* d_ovf) {
     if (pc == nullptr)
-        hipLaunchKernelGGL((adam8_update<GDT, PDT, false>), task_grid(n), dim3(kTaskThreads), 0, st, P,
+        hipLaunchKernelGGL((adam8_update<GDT, PDT, false>), task_grid(n), dim3(kTaskThreads), kLds8, st, P,
                            static_cast<u32x2*>(C), static_cast<uint16_t*>(S), G, static_cast<uint16_t*>(Pout), n, c,
                            key, seed, pc, d_step, d_sq, d_ovf);
     else
-        hipLaunchKernelGGL((adam8_update<GDT, PDT, true>), task_grid(n), dim3(kTaskThreads), 0, st, P,
+        hipLaunchKernelGGL((adam8_update<GDT, PDT, true>), task_grid(n), dim3(kTaskThreads), kLds8, st, P,
                            static_cast<u32x2*>(C), static_cast<uint16_t*>(S), G, static_cast<uint16_t*>(Pout), n, c,
                            key, seed, pc, d_step, d_sq, d_ovf);
 }
@@ -246,7 +256,7 @@ int zero_moments8_pack(void* moments8, void* scales8, const float* exp_avg, cons
     clear_error();
     const int st = check_convert(exp_avg, exp_avg_sq, moments8, scales8, n);
     if (st != ZERO_OK || n == 0) return st;
-    hipLaunchKernelGGL(pack8, task_grid(n), dim3(kTaskThreads), 0, static_cast<hipStream_t>(hip_stream),
+    hipLaunchKernelGGL(pack8, task_grid(n), dim3(kTaskThreads), kLdsConvert, static_cast<hipStream_t>(hip_stream),
                        static_cast<u32x2*>(moments8), static_cast<uint16_t*>(scales8), exp_avg, exp_avg_sq, n);
     return launch_status("pack8");
 }
@@ -256,7 +266,7 @@ int zero_moments8_unpack(float* exp_avg, float* exp_avg_sq, const void* moments8
     clear_error();
     const int st = check_convert(exp_avg, exp_avg_sq, moments8, scales8, n);
     if (st != ZERO_OK || n == 0) return st;
-    hipLaunchKernelGGL(unpack8, task_grid(n), dim3(kTaskThreads), 0, static_cast<hipStream_t>(hip_stream), exp_avg,
+    hipLaunchKernelGGL(unpack8, task_grid(n), dim3(kTaskThreads), kLdsConvert, static_cast<hipStream_t>(hip_stream), exp_avg,
                        exp_avg_sq, static_cast<const u32x2*>(moments8), static_cast<const uint16_t*>(scales8), n);
     return launch_status("unpack8");
 }

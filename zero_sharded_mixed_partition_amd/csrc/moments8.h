@@ -176,12 +176,6 @@ __device__ __forceinline__ void decode4(uint32_t codes, float scale, float x[4])
 
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
 
-__device__ __forceinline__ uint32_t top_of4(const float x[4]) {
-    uint32_t t = abs_bits(x[0]);
-    for (int j = 1; j < 4; ++j) t = t > abs_bits(x[j]) ? t : abs_bits(x[j]);
-    return max_of_block(t);
-}
-
 // a positive root is at least the smallest code
 __device__ __forceinline__ float floor_root(float s, float smallest) {
     return (s > 0.0f && s < smallest) ? smallest : s;
@@ -207,84 +201,163 @@ __device__ __forceinline__ uint32_t encode4_nearest(const float x[4], float scal
 
 // ---------------------------------------------------------------- one task of the step
 
-// One AdamW element on a decoded second-moment root: as adam_elem, and the
-// new root is what the denominator needs anyway.
-__device__ __forceinline__ void adam8_elem(const StepCoef& c, float gscale, float graw, float& p, float& m, float& s) {
-    const float g = graw * gscale;
-    m = fmaf(c.beta1, m, c.omb1 * g);
-    s = sqrtf(fmaf(c.beta2, s * s, (c.omb2 * g) * g));
-    const float denom = fmaf(s, c.rsqrt_bc2, c.eps);
-    p = fmaf(p, c.decay, -(c.step_size * m) / denom);
+// Root and quotient, correctly rounded as sqrtf and / give them, without their
+// scaling and special cases: root_normal for every v in [2^-96, FLT_MAX]
+// (all 1.9e9 of them compared), quotient_normal where no step under- or
+// overflows (2.6e10 random pairs compared).
+__device__ __forceinline__ float root_normal(float v) {
+    const float y = __builtin_amdgcn_rsqf(v);
+    const float s = v * y;
+    return fmaf(fmaf(-s, s, v), 0.5f * y, s);
+}
+
+__device__ __forceinline__ float quotient_normal(float a, float d) {
+    float y = __builtin_amdgcn_rcpf(d);
+    y = fmaf(fmaf(-d, y, 1.0f), y, y);
+    const float q = a * y;
+    return fmaf(fmaf(-d, q, a), y, q);
+}
+
+__device__ __forceinline__ uint32_t min_of4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    const uint32_t x = a < b ? a : b, y = c < d ? c : d;
+    return x < y ? x : y;
+}
+
+__device__ __forceinline__ uint32_t max_of4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    const uint32_t x = a > b ? a : b, y = c > d ? c : d;
+    return x > y ? x : y;
+}
+
+// The block's largest magnitude (its bits) from each lane's four values.
+__device__ __forceinline__ uint32_t top_of_block(const float x[4]) {
+    return max_of_block(max_of4(abs_bits(x[0]), abs_bits(x[1]), abs_bits(x[2]), abs_bits(x[3])));
+}
+
+// Whether the float with these bits (sign clear) lies in [2^LO, 2^HI).
+template <int LO, int HI>
+__device__ __forceinline__ bool in_powers(uint32_t bits) {
+    return bits - ((uint32_t)(LO + 127) << 23) < (uint32_t)(HI - LO) << 23;
+}
+
+// Whether a step's coefficients allow root_normal and quotient_normal for
+// values in the ranges that adam8_four asks of its moments: then
+// d = s * RB + eps lies in [2^-48, 2^46], the numerator in [2^-74, 2^50] and
+// the quotient in [2^-120, 2^98], and its residuals are exact.
+__device__ __forceinline__ bool usual_coefficients(const StepCoef& c) {
+    return in_powers<-24, 10>(__float_as_uint(c.step_size)) && in_powers<0, 12>(__float_as_uint(c.rsqrt_bc2)) &&
+           __float_as_uint(c.eps) < (127u + 20u) << 23;
+}
+
+// What a lane reads of its four consecutive elements.
+template <int GDT>
+struct Quad8 {
+    f32x4 p;
+    u32x2 codes;
+    Grad4<GDT> g;
+    uint32_t scales;
+    __device__ __forceinline__ void load(const float* P, const u32x2* C, const uint16_t* S, const void* G, int64_t e) {
+        p = ld_any(P + e);
+        codes = ld_codes(C + (e >> 2));
+        g.load(G, e);
+        scales = global(S)[e >> 5];
+    }
+};
+
+// The step of four elements from e on, of which `here` exist (4 everywhere but
+// at the tensor's end; the block's lanes all take part in its maxima).  The
+// arithmetic of adam_elem on a decoded root; the new root, which the
+// denominator needs, is what is stored.  A correctly rounded root and quotient
+// are about a third of the instructions, and with 16 bytes an element the
+// kernel is bound by those as much as by memory: a wave whose moments all lie
+// in the usual range takes the short forms of both (same results).
+__device__ __forceinline__ void adam8_four(const StepCoef& c, bool usual, float gscale, uint32_t key, int64_t e, int here,
+                                           const float g[4], float p[4], u32x2& codes, uint32_t& scales) {
+    float m[4], s[4], v[4];
+    decode4(codes[0], scale_of(scales & 0xFFu), m);
+    decode4(codes[1], scale_of(scales >> 8), s);
+    uint32_t mb[4], r[4], q[4];
+    for (int j = 0; j < 4; ++j) {
+        const float gj = g[j] * gscale;
+        m[j] = fmaf(c.beta1, m[j], c.omb1 * gj);
+        v[j] = fmaf(c.beta2, s[j] * s[j], (c.omb2 * gj) * gj);
+        if (j >= here) m[j] = v[j] = 0.0f;
+        mb[j] = abs_bits(m[j]);
+        r[j] = dither_bits((uint32_t)(e + j), key);
+        q[j] = rotate16(r[j]);
+    }
+    const uint32_t m_top = max_of4(mb[0], mb[1], mb[2], mb[3]);
+    const uint32_t v0 = __float_as_uint(v[0]), v1 = __float_as_uint(v[1]), v2 = __float_as_uint(v[2]),
+                   v3 = __float_as_uint(v[3]);
+    // below the sign bit the order of the bits is the order of the values; a NaN is above them all
+    usual = usual && in_powers<-50, 40>(min_of4(mb[0], mb[1], mb[2], mb[3])) && in_powers<-50, 40>(m_top) &&
+            in_powers<-96, 64>(min_of4(v0, v1, v2, v3)) && in_powers<-96, 64>(max_of4(v0, v1, v2, v3));
+    if (__all(usual)) {
+        for (int j = 0; j < 4; ++j) {
+            s[j] = root_normal(v[j]);
+            p[j] = fmaf(p[j], c.decay, quotient_normal(-(c.step_size * m[j]), fmaf(s[j], c.rsqrt_bc2, c.eps)));
+        }
+    } else {
+        for (int j = 0; j < 4; ++j) {
+            s[j] = sqrtf(v[j]);
+            p[j] = fmaf(p[j], c.decay, -(c.step_size * m[j]) / fmaf(s[j], c.rsqrt_bc2, c.eps));
+        }
+    }
+    const uint32_t m_byte = scale_byte(max_of_block(m_top));
+    const uint32_t s_byte = scale_byte(top_of_block(s));
+    const float smallest = __builtin_ldexpf(scale_of(s_byte), -9);
+    for (int j = 0; j < 4; ++j) s[j] = floor_root(s[j], smallest);
+    codes[0] = encode4_random(m, scale_of(m_byte), r);
+    codes[1] = encode4_random(s, scale_of(s_byte), q);
+    scales = m_byte | (s_byte << 8);
 }
 
 // Elements [base, base + 256) of one tensor, base a multiple of 256, by one
-// wave; lane l owns four consecutive elements.  WHOLE: all of them lie below
-// n; else the lanes past the end take part in the block maxima with zeros.
-// key: dither_tensor.  PDT 0: no 16-bit copy.
-template <int GDT, int PDT, bool WHOLE>
-__device__ __forceinline__ void adam8_quads(float* P, u32x2* C, uint16_t* S, const void* G, uint16_t* Pout, int64_t n,
-                                            int64_t base, const StepCoef& c, float gscale, uint32_t key) {
-    const int lane = threadIdx.x;
-    const int64_t e0 = base + 4 * lane;
-    const int here = WHOLE ? 4 : e0 >= n ? 0 : n - e0 < 4 ? (int)(n - e0) : 4;
-    float p[4] = {}, g[4] = {}, m[4], s[4];
-    u32x2 codes = {0, 0};
-    uint32_t scales = 0;
-    if constexpr (WHOLE) {
-        const f32x4 v = ld_any(P + e0);
-        codes = ld_codes(C + (e0 >> 2));
-        Grad4<GDT> gq;
-        gq.load(G, e0);
-        scales = global(S)[e0 >> 5];
-        gq.values(g);
-        for (int j = 0; j < 4; ++j) p[j] = v[j];
-    } else if (here > 0) {
-        codes = ld_codes(C + (e0 >> 2));
-        scales = global(S)[e0 >> 5];
-        for (int j = 0; j < 4; ++j) {
-            if (j < here) {
-                p[j] = global(P)[e0 + j];
-                g[j] = ld_grad1<GDT>(G, e0 + j);
-            }
-        }
-    }
-    decode4(codes[0], scale_of(scales & 0xFFu), m);
-    decode4(codes[1], scale_of(scales >> 8), s);
-    uint32_t r[4], q[4];
-    for (int j = 0; j < 4; ++j) {
-        if (j < here) adam8_elem(c, gscale, g[j], p[j], m[j], s[j]);
-        else m[j] = s[j] = 0.0f;
-        r[j] = dither_bits((uint32_t)(e0 + j), key);
-        q[j] = rotate16(r[j]);
-    }
-    const uint32_t mb = scale_byte(top_of4(m)), sb = scale_byte(top_of4(s));
-    const float smallest = __builtin_ldexpf(scale_of(sb), -9);
-    for (int j = 0; j < 4; ++j) s[j] = floor_root(s[j], smallest);
-    codes[0] = encode4_random(m, scale_of(mb), r);
-    codes[1] = encode4_random(s, scale_of(sb), q);
-    if constexpr (WHOLE) {
-        f32x4 v;
-        for (int j = 0; j < 4; ++j) v[j] = p[j];
-        st_any(v, P + e0);
-        st_codes(codes, C + (e0 >> 2));
-        if constexpr (PDT != 0) st_any(pack4_16<PDT>(p), Pout + e0);
-    } else if (here > 0) {
-        st_codes(codes, C + (e0 >> 2));
-        for (int j = 0; j < 4; ++j) {
-            if (j < here) {
-                global(P)[e0 + j] = p[j];
-                if constexpr (PDT != 0) global(Pout)[e0 + j] = (uint16_t)to16<PDT>(p[j]);
-            }
-        }
-    }
-    if ((lane & 7) == 0 && here > 0) global(S)[e0 >> 5] = (uint16_t)(mb | (sb << 8));
-}
-
+// wave; lane l owns four consecutive elements.  The clip coefficient's float64
+// arithmetic (about 30 dependent instructions) runs while the loads are on
+// their way.  key: dither_tensor.  PDT 0: no 16-bit copy.
 template <int GDT, int PDT>
 __device__ __forceinline__ void adam8_task(float* P, u32x2* C, uint16_t* S, const void* G, uint16_t* Pout, int64_t n,
-                                           int64_t base, const StepCoef& c, float gscale, uint32_t key) {
-    if (base + kTask <= n) adam8_quads<GDT, PDT, true>(P, C, S, G, Pout, n, base, c, gscale, key);
-    else adam8_quads<GDT, PDT, false>(P, C, S, G, Pout, n, base, c, gscale, key);
+                                           int64_t base, const StepCoef& c, const double* d_sq, uint32_t key) {
+    const int lane = threadIdx.x;
+    const int64_t e = base + 4 * lane;
+    const bool usual = usual_coefficients(c);
+    float p[4] = {}, g[4] = {};
+    if (base + kTask <= n) {
+        Quad8<GDT> quad;
+        quad.load(P, C, S, G, e);
+        const float gscale = clipped_scale(c, d_sq);
+        quad.g.values(g);
+        for (int j = 0; j < 4; ++j) p[j] = quad.p[j];
+        adam8_four(c, usual, gscale, key, e, 4, g, p, quad.codes, quad.scales);
+        const f32x4 v = {p[0], p[1], p[2], p[3]};
+        st_any(v, P + e);
+        st_codes(quad.codes, C + (e >> 2));
+        if constexpr (PDT != 0) st_any(pack4_16<PDT>(p), Pout + e);
+        if ((lane & 7) == 0) global(S)[e >> 5] = (uint16_t)quad.scales;
+        return;
+    }
+    const int here = e >= n ? 0 : n - e < 4 ? (int)(n - e) : 4;
+    u32x2 codes = {0, 0};
+    uint32_t scales = 0;
+    if (here > 0) {
+        codes = ld_codes(C + (e >> 2));
+        scales = global(S)[e >> 5];
+    }
+    for (int j = 0; j < 4; ++j) {
+        if (j >= here) continue;
+        p[j] = global(P)[e + j];
+        g[j] = ld_grad1<GDT>(G, e + j);
+    }
+    adam8_four(c, usual, clipped_scale(c, d_sq), key, e, here, g, p, codes, scales);
+    if (here > 0) {
+        st_codes(codes, C + (e >> 2));
+        if ((lane & 7) == 0) global(S)[e >> 5] = (uint16_t)scales;
+    }
+    for (int j = 0; j < 4; ++j) {
+        if (j >= here) continue;
+        global(P)[e + j] = p[j];
+        if constexpr (PDT != 0) global(Pout)[e + j] = (uint16_t)to16<PDT>(p[j]);
+    }
 }
 
 }  // namespace
