@@ -137,7 +137,8 @@ def test_workspace():
     assert lib.zero_multi_norm_workspace_bytes(ctypes.create_string_buffer(256)) == 0
     small, large = table_of(5), table_of(5, 8192 * 5000, bits=0)      # gradients only: nothing overlaps
     assert lib.zero_multi_norm_workspace_bytes(small) == 256
-    assert lib.zero_multi_norm_workspace_bytes(large) >= (1024 + 2 + 1) * 8 + 1024 * 4
+    # 512 blocks and 2 tensors: a partial each, the scale's factor, and a flag per block
+    assert lib.zero_multi_norm_workspace_bytes(large) == -(-((512 + 2 + 1) * 8 + 512 * 4) // 256) * 256
 
 
 D = AL + (1 << 39)                  # where the scalars and the table's device copy lie
@@ -356,19 +357,43 @@ def test_binding_checks_list_calls():
         Z.zero_multi_adam_step(t, hps, FakeDev(1, F32), ov, stream=0)
 
 
-def test_tensors_on_another_device_are_refused():
-    class Elsewhere(FakeDev):
-        device = torch.device("cuda", 0)
+class Placed(FakeDev):
+    """A stand-in that knows its device."""
 
+    def __init__(self, numel, dtype, addr=1 << 40, index=0):
+        super().__init__(numel, dtype, addr)
+        self.device = torch.device("cuda", index)
+
+    def get_device(self):
+        return self.device.index
+
+
+def test_tensors_on_another_device_are_refused(monkeypatch):
+    from zero_sharded_mixed_partition_amd import moments8 as M8
+    from zero_sharded_mixed_partition_amd import multi as MU
+    cols = [[Placed(t.numel(), t.dtype, t.data_ptr()) for t in col] for col in fake_list([100, 7])]
+    for col in range(5):
+        bad = [list(c) for c in cols]
+        t = bad[col][1]
+        bad[col][1] = Placed(t.numel(), t.dtype, t.data_ptr(), index=1)
+        with pytest.raises(ValueError, match="cuda:1"):
+            Z.TensorTable(*bad)
+    for module in (M8, MU):
+        monkeypatch.setattr(module, "_current_device", lambda: 1)
+    n = 100
+    for k in range(5):
+        args = [FakeDev(n, F32), FakeDev(200, U8), FakeDev(8, U8), FakeDev(n, BF16), FakeDev(n, BF16)]
+        for i, t in enumerate(args):                        # all on the current device but one
+            args[i] = Placed(t.numel(), t.dtype, t.data_ptr(), index=0 if i == k else 1)
+        with pytest.raises(ValueError, match="current device is cuda:1"):
+            Z.zero_shard_adam8_step(*args, Z.AdamHyper(), stream=0)
     m, a, b, g, p = fake_list([100, 7])
-    g[1].device, m[1].device = torch.device("cuda", 1), torch.device("cuda", 0)
-    with pytest.raises(ValueError, match="cuda"):
-        Z.TensorTable(m, a, b, g, p)
-    x = Elsewhere(100, F32)
-    y = Elsewhere(100, BF16)
-    y.device = torch.device("cuda", 1)
-    with pytest.raises(ValueError, match="different devices"):
-        Z.zero_shard_adam8_step(x, FakeDev(200, U8), FakeDev(8, U8), y, None, Z.AdamHyper(), stream=0)
+    t = Z.TensorTable(m, a, b, g, p)
+    t._index = 0
+    with pytest.raises(ValueError, match="current device is cuda:1"):
+        Z.zero_multi_adam_step(t, [Z.AdamHyper()], FakeDev(1, F64), stream=0)
+    with pytest.raises(ValueError, match="current device is cuda:1"):
+        Z.zero_multi_unscale_norm_overflow(t, 1.0, FakeDev(1, F64), FakeDev(1, I32), FakeDev(256, U8), stream=0)
 
 
 def test_np_seed_range():

