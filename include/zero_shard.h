@@ -607,7 +607,8 @@ int zero_shard_grad_sum_norm_dev(float* acc, const void* const* slices, int32_t 
  * zero_moments8_pack: codes from fp32 moments, each rounded to nearest even
  *   (exp_avg_sq >= 0; its root is formed in float32).
  * zero_moments8_unpack: fp32 moments from codes: exp_avg = code * 2^k, exact,
- *   and exp_avg_sq = (code * 2^k)^2, rounded once.
+ *   and exp_avg_sq = (code * 2^k)^2, rounded once.  Both take fp32 moments at
+ *   any 4-byte, moments8 at any 8-byte and scales8 at any 2-byte address.
  * Streams 16.125 bytes per element with 16-bit gradient and copy (18.125 with
  * an fp32 gradient, 2 less without a copy); pack and unpack 10.06.
  * Errors: ZERO_EINVAL, ZERO_EALIGN, ZERO_ERANGE, ZERO_EHIP.

@@ -250,7 +250,7 @@ def test_shard8_refusals():
             a = [AL, AL + M, AL + 2 * M, AL + 3 * M]
             a[k] = None
             assert f(*a, 100) == L.ZERO_EINVAL
-            a[k] = AL + 5 * M + 8
+            a[k] = AL + 5 * M + (2, 2, 4, 1)[k]
             assert f(*a, 100) == L.ZERO_EALIGN
             a[k] = a[k - 1]
             assert f(*a, 100) == L.ZERO_EINVAL
@@ -400,3 +400,19 @@ def test_np_seed_range():
     """Any integer seeds the rounding: it is taken modulo 2^64."""
     from zero_sharded_mixed_partition_amd.moments8 import _seed
     assert _seed(-1) == 2 ** 64 - 1 and _seed(2 ** 64 + 5) == 5 and _seed(np.int64(3)) == 3
+
+
+def test_multi_adam_refuses_bad_lists():
+    g = [FakeDev(5, BF16)]
+    for kw in (dict(state_bits=16), dict(hyper=[]), dict(hyper=[{}] * 17), dict(hyper=[dict(lr=1.0, momentum=0.9)]),
+               dict(groups=[1]), dict(groups=[-1])):
+        with pytest.raises(ValueError):
+            Z.MultiAdam([FakeDev(5, F32)], g, **kw)
+    with pytest.raises(ValueError, match="empty"):
+        Z.MultiAdam([], [])
+    with pytest.raises(ValueError, match="fp32"):
+        Z.ShardAdam8(FakeDev(5, BF16))
+    with pytest.raises(ValueError, match="together"):
+        Z.ShardAdam8(FakeDev(5, F32), moments8=FakeDev(16, U8))
+    with pytest.raises(ValueError, match="uint8"):
+        Z.ShardAdam8(FakeDev(5, F32), moments8=FakeDev(15, U8), scales8=FakeDev(2, U8))

@@ -18,7 +18,7 @@ in the library's kernels.
     zero_loss_scaler_update(scaler, overflow) -> skip
 
 moments8.py adds the shard's step with 8-bit moments, multi.py the step over a
-list of tensors.
+list of tensors; ShardAdam, ShardAdam8 and MultiAdam run whole steps.
 """
 import ctypes
 from typing import List, Optional, Sequence, Tuple
@@ -44,7 +44,7 @@ __all__ = ["zero_partition_plan", "zero_rank_fragments", "zero_norm_workspace_by
            "zero_moments8_unpack", "zero_shard_adam8_step", "zero_shard_adam8_step_coef", "TensorTable", "MAX_GROUPS",
            "zero_multi_norm_workspace_bytes", "zero_multi_unscale_norm_overflow",
            "zero_multi_unscale_norm_overflow_dev", "zero_multi_norm_decide_dev", "zero_multi_decide_dev",
-           "zero_multi_adam_step", "zero_multi_adam_step_coef"]
+           "zero_multi_adam_step", "zero_multi_adam_step_coef", "ShardAdam8", "MultiAdam"]
 
 
 def zero_abi_version() -> int:
@@ -451,6 +451,11 @@ class StepState:
     def ptr(self) -> int:
         return self.tensor.data_ptr()
 
+    def applied(self):
+        """The count of applied steps, as an int64 [1] view of the device state."""
+        import torch
+        return self.tensor.view(torch.int64)[zero_step_state.applied.offset // 8:][:1]
+
     def read(self) -> zero_step_state:
         """Copy the state to the host (synchronises with its stream)."""
         raw = bytes(self.tensor.cpu().numpy().tobytes())
@@ -649,6 +654,8 @@ from .multi import (MAX_GROUPS, TensorTable, zero_multi_adam_step, zero_multi_ad
                     zero_multi_decide_dev, zero_multi_norm_decide_dev, zero_multi_norm_workspace_bytes,
                     zero_multi_unscale_norm_overflow, zero_multi_unscale_norm_overflow_dev)
 from .shard import ShardAdam  # noqa: E402
+from .shard8 import ShardAdam8  # noqa: E402
+from .multi_adam import MultiAdam  # noqa: E402
 from .offload import OffloadShardAdam  # noqa: E402
 from . import checkpoint  # noqa: E402,F401
 

@@ -64,8 +64,7 @@ __global__ __launch_bounds__(kTaskThreads) void pack8(u32x2* __restrict__ C, uin
         const int64_t e0 = t * kTask + 4 * threadIdx.x;
         float m[4] = {}, s[4] = {};
         if (e0 + 4 <= n) {
-            const f32x4 a = ld_stream(reinterpret_cast<const f32x4*>(M + e0));
-            const f32x4 b = ld_stream(reinterpret_cast<const f32x4*>(V + e0));
+            const f32x4 a = ld_any(M + e0), b = ld_any(V + e0);
             for (int j = 0; j < 4; ++j) {
                 m[j] = a[j];
                 s[j] = sqrtf(b[j]);
@@ -107,8 +106,8 @@ __global__ __launch_bounds__(kTaskThreads) void unpack8(float* __restrict__ M, f
                 a[j] = m[j];
                 b[j] = s[j] * s[j];
             }
-            st_stream(a, reinterpret_cast<f32x4*>(M + e0));
-            st_stream(b, reinterpret_cast<f32x4*>(V + e0));
+            st_any(a, M + e0);
+            st_any(b, V + e0);
         } else {
             for (int j = 0; j < 4; ++j) {
                 if (e0 + j < n) {
@@ -189,8 +188,8 @@ int check_convert(const void* exp_avg, const void* exp_avg_sq, const void* momen
     if (n == 0) return ZERO_OK;
     if (n > INT64_MAX / 8) return fail(ZERO_ERANGE, "n too large");
     if (!exp_avg || !exp_avg_sq || !moments8 || !scales8) return fail(ZERO_EINVAL, "NULL pointer");
-    if (!aligned16(exp_avg) || !aligned16(exp_avg_sq) || !aligned16(moments8) || !aligned16(scales8))
-        return fail(ZERO_EALIGN, "pointers must be 16-byte aligned");
+    if ((((uintptr_t)exp_avg | (uintptr_t)exp_avg_sq) & 3u) || ((uintptr_t)moments8 & 7u) || ((uintptr_t)scales8 & 1u))
+        return fail(ZERO_EALIGN, "fp32 moments must be 4-byte, moments8 8-byte and scales8 2-byte aligned");
     const Range r[] = {{exp_avg, n * 4},
                        {exp_avg_sq, n * 4},
                        {moments8, (int64_t)zero_moments8_bytes(n)},

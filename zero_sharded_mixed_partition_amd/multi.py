@@ -73,13 +73,12 @@ class TensorTable:
                 old[1].record_stream(torch.cuda.current_stream())    # a step there may still read it
 
     def _build(self, grads) -> None:
-        self.grads = list(grads)
-        self._grad_key = tuple((g.data_ptr(), g.dtype, g.numel()) for g in self.grads)
+        grads = list(grads)
         arr = (_L.zero_tensor * max(1, self.n_tensors))()
         bits, index = self.state_bits, -1
         if self.n_tensors:
-            index = self.grads[0].get_device() if hasattr(self.grads[0], "get_device") else -1
-        for i, g in enumerate(self.grads):
+            index = grads[0].get_device() if hasattr(grads[0], "get_device") else -1
+        for i, g in enumerate(grads):
             n, t = g.numel(), arr[i]
             t.grad, t.numel, t.grad_dtype = _buf(g, None, 0, f"grads[{i}]", index), n, dtype_code(g)
             if not bits:
@@ -103,10 +102,12 @@ class TensorTable:
             raise RuntimeError("a table cannot be built while its stream records a graph")
         # pinned: the copy to the device needs no wait, and torch's host allocator
         # hands the memory out again only after the copy has run
-        self.host = torch.empty(size.value, dtype=torch.uint8, pin_memory=on_gpu)
-        _L.check(build(arr, self.n_tensors, bits, self.host.data_ptr(), size.value, ctypes.byref(size),
+        host = torch.empty(size.value, dtype=torch.uint8, pin_memory=on_gpu)
+        _L.check(build(arr, self.n_tensors, bits, host.data_ptr(), size.value, ctypes.byref(size),
                        ctypes.byref(dev_size)), "zero_multi_table_build")
-        self.device = self.host[:dev_size.value].to(torch.device("cuda", index), non_blocking=True) if on_gpu else None
+        self.grads, self.host = grads, host
+        self._grad_key = tuple((g.data_ptr(), g.dtype, g.numel()) for g in grads)
+        self.device = host[:dev_size.value].to(torch.device("cuda", index), non_blocking=True) if on_gpu else None
         self._index, self._captured = index, False
         self._addresses = self.host.data_ptr(), None if self.device is None else self.device.data_ptr()
 

@@ -36,12 +36,21 @@ class ShardAdam:
         for t in (master, exp_avg, exp_avg_sq):
             if t.dtype != torch.float32 or not t.is_cuda or t.numel() != n or not t.is_contiguous():
                 raise ValueError("master / exp_avg / exp_avg_sq must be contiguous fp32 device tensors of equal size")
-        self.master, self.exp_avg, self.exp_avg_sq, self.n = master, exp_avg, exp_avg_sq, n
-        self.hyper = dict(lr=lr, beta1=beta1, beta2=beta2, eps=eps, weight_decay=weight_decay,
-                          max_grad_norm=max_grad_norm)
+        self.master, self.exp_avg, self.exp_avg_sq = master, exp_avg, exp_avg_sq
+        self._init_step(n, dict(lr=lr, beta1=beta1, beta2=beta2, eps=eps, weight_decay=weight_decay,
+                                max_grad_norm=max_grad_norm), scaler, applied_steps, graph, device_state)
+
+    def checkpoint_arrays(self) -> dict:
+        """The device tensors that a checkpoint holds, by name."""
+        return {"master": self.master, "exp_avg": self.exp_avg, "exp_avg_sq": self.exp_avg_sq}
+
+    def _init_step(self, n: int, hyper: dict, scaler: Optional[LossScaler], applied_steps: int, graph: bool,
+                   device_state: bool) -> None:
+        """Everything a step needs besides the shard's streams."""
+        self.n, self.hyper = n, hyper
         self.scaler = scaler if scaler is not None else LossScaler.static(1.0)
         self.t = applied_steps
-        dev = master.device
+        dev = self.master.device
         self.workspace = torch.empty(zero_norm_workspace_bytes(n), dtype=torch.uint8, device=dev)
         self.sqnorm = torch.empty(1, dtype=torch.float64, device=dev)
         self.overflow = torch.empty(1, dtype=torch.int32, device=dev)
