@@ -68,10 +68,10 @@ def test_table_contents():
     assert refs == [(k, c) for k, i in enumerate(live) for c in range(chunks[i])]
     first = 0
     for k, i in enumerate(live):
-        f = struct.unpack_from("<QQQQQqiiiIII", raw, desc_at + k * 72)
+        f = struct.unpack_from("<QQQQQqiiiIIIii", raw, desc_at + k * 80)
         t = tensors[i]
         assert f == (t.master, t.exp_avg, t.exp_avg_sq, t.grad, t.param_out, sizes[i], t.grad_dtype, t.param_dtype,
-                     t.group, i, first, chunks[i])
+                     t.group, i, first, chunks[i], 0, 0)
         first += chunks[i]
     assert [struct.unpack_from("<I", raw, empty_at + 4 * j)[0] for j in range(2)] == [1, 4]
     ranges = [struct.unpack_from("<QQ", raw, ranges_at + 16 * j) for j in range(n_ranges)]
@@ -416,3 +416,15 @@ def test_multi_adam_refuses_bad_lists():
         Z.ShardAdam8(FakeDev(5, F32), moments8=FakeDev(16, U8))
     with pytest.raises(ValueError, match="uint8"):
         Z.ShardAdam8(FakeDev(5, F32), moments8=FakeDev(15, U8), scales8=FakeDev(2, U8))
+
+
+def test_table_phases():
+    """32-bit tensors whose master starts off a 256-byte boundary: the update's
+    tasks start before the tensor, and take one chunk more where that spills."""
+    for off, n, bits, want in ((1, 8192, 32, (2, 1)), (63, 8130, 32, (2, 63)), (63, 8129, 32, (1, 63)), (64, 8192, 32, (1, 0)),
+                               (1, 8192, 8, (1, 0)), (5, 1, 32, (1, 5))):
+        st, buf, _ = build([tensor(AL, n, master=AL + 4 * off)], bits)
+        assert st == L.ZERO_OK
+        hdr = struct.unpack_from(HDR, buf.raw)
+        f = struct.unpack_from("<QQQQQqiiiIIIii", buf.raw, hdr[7])
+        assert (f[11], f[12]) == want == (hdr[6], f[12]), (off, n, bits)
