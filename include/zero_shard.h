@@ -646,7 +646,8 @@ int zero_moments8_unpack(float* exp_avg, float* exp_avg_sq, const void* moments8
  * written buffer may overlap another buffer of the list.
  *
  * zero_multi_table_build (host only) writes the table of the list to host
- * memory at `table`, which the caller keeps as long as it steps the list, and
+ * memory at `table` (8-byte aligned), which the caller keeps as long as it
+ * steps the list (and does not move to another program or library), and
  * sets *bytes (size of the table) and *device_bytes.  The caller copies the
  * first *device_bytes bytes to device memory, 16-byte aligned, and passes both
  * to the calls below.  With table NULL or capacity below *bytes it writes

@@ -15,7 +15,7 @@ from zero_sharded_mixed_partition_amd import _lib as L  # noqa: E402
 from test_binding_checks import FakeDev, FakeState  # noqa: E402
 
 AL = 1 << 40                        # a plausible, 16-byte aligned device address
-HDR = "<Iiiiiiqqqqqqqq"
+HDR = "<Iiiiiiqqqqqqqqqq"
 
 
 def tensor(base, n, gdt=L.ZERO_BF16, pdt=L.ZERO_BF16, group=0, bits=32, **over):
@@ -59,7 +59,7 @@ def test_table_contents():
     assert st == L.ZERO_OK
     raw = buf.raw
     (_, bits, n_groups, n_user, n_tensors, n_empty, n_chunks, desc_at, map_at, empty_at, device_bytes, ranges_at,
-     n_ranges, size) = struct.unpack_from(HDR, raw)
+     n_ranges, grads_at, n_grads, size) = struct.unpack_from(HDR, raw)
     assert (bits, n_groups, n_user, n_tensors, n_empty) == (32, 3, 6, 4, 2)
     chunks = [-(-n // 8192) for n in sizes]
     assert n_chunks == sum(chunks) and device_bytes == dev <= size
@@ -79,6 +79,8 @@ def test_table_contents():
                   ((tensors[i].master, 4 * sizes[i]), (tensors[i].exp_avg, 4 * sizes[i]),
                    (tensors[i].exp_avg_sq, 4 * sizes[i]), (tensors[i].param_out, 2 * sizes[i])))
     assert ranges == want
+    grads = [struct.unpack_from("<QQ", raw, grads_at + 16 * j) for j in range(n_grads)]
+    assert grads == [(tensors[i].grad, tensors[i].grad + 2 * sizes[i]) for i in live]
 
 
 def test_table_joins_written_ranges():
@@ -112,6 +114,9 @@ def test_table_refusals():
     assert lib.zero_multi_table_build(None, 1, 32, None, 0, ctypes.byref(s), ctypes.byref(s)) == L.ZERO_EINVAL
     assert lib.zero_multi_table_build(None, -1, 32, None, 0, ctypes.byref(s), ctypes.byref(s)) == L.ZERO_EINVAL
     assert lib.zero_multi_table_build(None, 0, 32, None, 0, None, ctypes.byref(s)) == L.ZERO_EINVAL
+    odd = ctypes.addressof(ctypes.create_string_buffer(4096)) // 8 * 8 + 4
+    assert lib.zero_multi_table_build(None, 0, 32, odd, 4096, ctypes.byref(s), ctypes.byref(s)) == L.ZERO_EALIGN
+    assert lib.zero_multi_adam_step(odd, None, None, 1, 0, None, None, None) in (L.ZERO_EALIGN, L.ZERO_EINVAL)
 
 
 def test_table_refuses_overlaps():
@@ -128,7 +133,8 @@ def test_table_refuses_overlaps():
     assert build([tensor(AL, 33, exp_avg_sq=AL + (1 << 20) + 70)], 8)[0] == L.ZERO_EINVAL
     assert build([tensor(AL, 33, exp_avg_sq=AL + (1 << 20) + 72)], 8)[0] == L.ZERO_OK
     # a table of gradients looks at nothing else
-    assert build([L.zero_tensor(None, None, None, AL, None, 100, L.ZERO_F16, 0, 0, 0)] * 2, 0)[0] == L.ZERO_OK
+    st, buf, _ = build([L.zero_tensor(None, None, None, AL, None, 100, L.ZERO_F16, 0, 0, 0)] * 2, 0)
+    assert st == L.ZERO_OK and struct.unpack_from(HDR, buf.raw)[14] == 1     # gradients that overlap are one range
 
 
 def test_workspace():

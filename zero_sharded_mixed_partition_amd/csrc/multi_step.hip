@@ -75,14 +75,16 @@ struct ChunkRef {
 // At the start of the table.  The device image is [0, device_bytes): this
 // header, the descriptors of the tensors that hold elements, the chunk map and
 // the caller's indices of the empty ones.  The host part behind it holds the
-// written address ranges, merged and sorted.
+// address ranges that the update writes and those of the gradients, each merged
+// and sorted, so that a call checks a pointer against the whole list at once.
 struct TableHeader {
     uint32_t magic;
     int32_t state_bits, n_groups;
     int32_t n_user, n_tensors, n_empty;
     int64_t n_chunks;
     int64_t desc_at, map_at, empty_at, device_bytes;
-    int64_t ranges_at, n_ranges, bytes;
+    int64_t ranges_at, n_ranges;
+    int64_t grads_at, n_grads, bytes;
 };
 
 struct AddressRange {
@@ -398,6 +400,7 @@ size_t norm_workspace(const TableHeader& h) {
 
 int read_table(const void* table, const void* d_table, TableHeader* h) {
     if (table == nullptr) return fail(ZERO_EINVAL, "table is NULL");
+    if ((uintptr_t)table & 7u) return fail(ZERO_EALIGN, "table must be 8-byte aligned");
     std::memcpy(h, table, sizeof(*h));
     if (h->magic != kTableMagic) return fail(ZERO_EINVAL, "not a table of zero_multi_table_build");
     if (h->n_user > 0) {
@@ -412,13 +415,17 @@ TableRef table_ref(const TableHeader& h, const void* d_table) {
                     at<uint32_t>(d_table, h.empty_at), h.n_chunks, h.n_tensors, h.n_empty};
 }
 
-// whether [p, p + bytes) meets an address range that the update writes
-bool written(const void* table, const TableHeader& h, const void* p, int64_t bytes) {
-    if (p == nullptr) return false;
-    const AddressRange* r = at<AddressRange>(table, h.ranges_at);
+// Whether [p, p + bytes) meets one of n sorted, disjoint address ranges.
+bool meets(const AddressRange* r, int64_t n, const void* p, int64_t bytes) {
+    if (p == nullptr || bytes == 0) return false;
     const uintptr_t lo = reinterpret_cast<uintptr_t>(p), hi = lo + (uintptr_t)bytes;
-    const AddressRange* f = std::upper_bound(r, r + h.n_ranges, lo, [](uintptr_t x, const AddressRange& a) { return x < a.hi; });
-    return f != r + h.n_ranges && f->lo < hi;
+    const AddressRange* f = std::upper_bound(r, r + n, lo, [](uintptr_t x, const AddressRange& a) { return x < a.hi; });
+    return f != r + n && f->lo < hi;
+}
+
+// ... one that the update writes
+bool written(const void* table, const TableHeader& h, const void* p, int64_t bytes) {
+    return meets(at<AddressRange>(table, h.ranges_at), h.n_ranges, p, bytes);
 }
 
 int check_groups(const TableHeader& h, int32_t n_groups) {
@@ -481,11 +488,9 @@ int multi_norm(const void* table, const void* d_table, double inv2, const double
         for (int j = 0; j < i; ++j)
             if (out[i].bytes && out[j].bytes && overlaps(out[i].p, out[i].bytes, out[j].p, out[j].bytes))
                 return fail(ZERO_EINVAL, "the norm pass's outputs, workspace and table must not overlap");
-    const TensorDesc* d = at<TensorDesc>(table, h.desc_at);
-    for (int i = 0; i < h.n_tensors; ++i)
-        for (int j = 0; j < 6; ++j)
-            if (out[j].bytes && overlaps(d[i].grad, d[i].numel * grad_bytes(d[i].gdt), out[j].p, out[j].bytes))
-                return fail(ZERO_EINVAL, "an output of the norm pass lies in gradient %u", d[i].user);
+    for (int j = 0; j < 6; ++j)
+        if (meets(at<AddressRange>(table, h.grads_at), h.n_grads, out[j].p, out[j].bytes))
+            return fail(ZERO_EINVAL, "an output of the norm pass lies in a gradient");
     const int nb = norm_grid(h.n_chunks);
     double* slots = static_cast<double*>(d_workspace);
     uint32_t* flags = reinterpret_cast<uint32_t*>(slots + nb + h.n_tensors + 1);
@@ -588,12 +593,16 @@ int build_table(const zero_tensor* tensors, int32_t n_tensors, int32_t state_bit
     // no written range may meet another range; gradients may be shared
     std::sort(regions.begin(), regions.end(), [](const Region& a, const Region& b) { return a.lo < b.lo; });
     uintptr_t any_hi = 0, write_hi = 0;
-    std::vector<AddressRange> ranges;
+    std::vector<AddressRange> ranges, grads;
     for (const Region& r : regions) {
         if (r.lo < (r.write ? any_hi : write_hi))
             return fail(ZERO_EINVAL, "tensor %d: a buffer the update writes overlaps another of the list", r.tensor);
         any_hi = std::max(any_hi, r.hi);
-        if (!r.write) continue;
+        if (!r.write) {
+            if (!grads.empty() && grads.back().hi >= r.lo) grads.back().hi = std::max(grads.back().hi, r.hi);
+            else grads.push_back({r.lo, r.hi});
+            continue;
+        }
         write_hi = std::max(write_hi, r.hi);
         if (!ranges.empty() && ranges.back().hi == r.lo) ranges.back().hi = r.hi;
         else ranges.push_back({r.lo, r.hi});
@@ -604,9 +613,12 @@ int build_table(const zero_tensor* tensors, int32_t n_tensors, int32_t state_bit
     h.device_bytes = pad16(h.empty_at + h.n_empty * (int64_t)sizeof(uint32_t));
     h.ranges_at = h.device_bytes;
     h.n_ranges = (int64_t)ranges.size();
-    h.bytes = pad16(h.ranges_at + h.n_ranges * (int64_t)sizeof(AddressRange));
+    h.grads_at = pad16(h.ranges_at + h.n_ranges * (int64_t)sizeof(AddressRange));
+    h.n_grads = (int64_t)grads.size();
+    h.bytes = pad16(h.grads_at + h.n_grads * (int64_t)sizeof(AddressRange));
     *bytes = (size_t)h.bytes;
     *device_bytes = (size_t)h.device_bytes;
+    if ((uintptr_t)table & 7u) return fail(ZERO_EALIGN, "table must be 8-byte aligned");
     if (table == nullptr || capacity < *bytes) return fail(ZERO_ENOSPC, "table %zu bytes, need %zu", capacity, *bytes);
     char* out = static_cast<char*>(table);
     std::memset(out, 0, (size_t)h.bytes);
@@ -644,6 +656,7 @@ int build_table(const zero_tensor* tensors, int32_t n_tensors, int32_t state_bit
         ++tensor;
     }
     if (!ranges.empty()) std::memcpy(out + h.ranges_at, ranges.data(), ranges.size() * sizeof(AddressRange));
+    if (!grads.empty()) std::memcpy(out + h.grads_at, grads.data(), grads.size() * sizeof(AddressRange));
     return ZERO_OK;
 }
 

@@ -45,8 +45,9 @@ class TensorTable:
         if state_bits not in (0, 8, 32):
             raise ValueError(f"state_bits must be 32 or 8, got {state_bits}")
         self.state_bits, self.n_tensors = state_bits, n
-        self.masters, self.exp_avgs, self.exp_avg_sqs = masters, exp_avgs, exp_avg_sqs
-        self.params_out, self.groups = params_out, None if groups is None else list(groups)
+        own = lambda x: None if x is None else list(x)  # noqa: E731
+        self.masters, self.exp_avgs, self.exp_avg_sqs = own(masters), own(exp_avgs), own(exp_avg_sqs)
+        self.params_out, self.groups = own(params_out), own(groups)
         self.n_groups = 1 + max(self.groups) if self.groups else 1
         self._kept = []                        # descriptions that recorded graphs read
         self._build(grads)
