@@ -1,11 +1,13 @@
-// Device and launch helpers shared by the HIP translation units: vector types
-// and streaming accesses, the gradient formats, the block reduction, the
-// step's decision and the AdamW element, and the host side's pointer checks.
+// Device and launch helpers of the list and 8-bit sources: vector types and
+// streaming accesses, the gradient formats, the block reduction, the step's
+// decision and the AdamW element, and the host side's pointer checks.
+// shard_step.hip has its own forms of these: the committed counter summaries
+// of its kernels hold for its text (bench.py compares a hash), so what it is
+// made of stays in it.  The two give the same bits, and are tested to.
 #pragma once
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
-#include <utility>
 
 #include "common.h"
 #include "zero_shard.h"
@@ -33,19 +35,16 @@ struct GradFmt;
 template <>
 struct GradFmt<ZERO_F16> {
     static constexpr int per_vec = 8;
-    static constexpr int norm_unroll = 4;
     static constexpr uint32_t mask = 0x7C007C00u, carry = 0x04000400u;
 };
 template <>
 struct GradFmt<ZERO_BF16> {
     static constexpr int per_vec = 8;
-    static constexpr int norm_unroll = 4;
     static constexpr uint32_t mask = 0x7F807F80u, carry = 0x00800080u;
 };
 template <>
 struct GradFmt<ZERO_F32> {
     static constexpr int per_vec = 4;
-    static constexpr int norm_unroll = 8;
     static constexpr uint32_t mask = 0x7F800000u, carry = 0x00800000u;
 };
 constexpr uint32_t kNonfiniteBits = 0x80008000u;
@@ -88,42 +87,6 @@ template <typename T>
 __device__ __forceinline__ T ld_stream(const T* p) { return __builtin_nontemporal_load(p); }
 template <typename T>
 __device__ __forceinline__ void st_stream(T v, T* p) { __builtin_nontemporal_store(v, p); }
-
-// f(integral_constant<int, 0>), ..., f(integral_constant<int, N-1>), as straight-line code
-template <typename F, int... I>
-__device__ __forceinline__ void static_for_impl(F& f, std::integer_sequence<int, I...>) {
-    (f(std::integral_constant<int, I>{}), ...);
-}
-template <int N, typename F>
-__device__ __forceinline__ void static_for(F&& f) {
-    static_for_impl(f, std::make_integer_sequence<int, N>{});
-}
-
-// the 4 gradient values of element group q (elements 4q .. 4q+3)
-template <int DT>
-__device__ __forceinline__ void load_grad4(const void* G, int64_t q, float g[4]) {
-    if constexpr (DT == ZERO_F32) {
-        const f32x4 v = ld_stream(static_cast<const f32x4*>(G) + q);
-        g[0] = v[0];
-        g[1] = v[1];
-        g[2] = v[2];
-        g[3] = v[3];
-    } else {
-        const u32x2 w = ld_stream(static_cast<const u32x2*>(G) + q);
-        unpack2<DT>(w[0], g[0], g[1]);
-        unpack2<DT>(w[1], g[2], g[3]);
-    }
-}
-
-template <int DT>
-__device__ __forceinline__ float load_grad1(const void* G, int64_t e) {
-    if constexpr (DT == ZERO_F32) {
-        return static_cast<const float*>(G)[e];
-    } else {
-        const uint32_t h = static_cast<const uint16_t*>(G)[e];
-        return DT == ZERO_F16 ? f16_to_f32(h) : bf16_to_f32(h);
-    }
-}
 
 // ---------------------------------------------------------------- block reduction
 
@@ -203,12 +166,6 @@ __device__ inline void decide_advance(zero_step_state* __restrict__ st, int32_t 
     }
     st->scaler = s;
     st->last_overflow = ovf;
-}
-
-__device__ inline void decide_step(zero_step_state* __restrict__ st, int32_t ovf, const HyperArgs& h, int unscaled_grad,
-                                   StepCoef* __restrict__ coef) {
-    decide_coef(st, h, unscaled_grad, coef);
-    decide_advance(st, ovf);
 }
 
 // ---------------------------------------------------------------- AdamW element
