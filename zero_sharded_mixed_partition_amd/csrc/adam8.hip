@@ -7,6 +7,12 @@
 //  pack8 / unpack8: 10.06 B/element (8 B of fp32 moments, 2 B of codes).
 // Both are elementwise streams in the lane layout of the fp32 update: one
 // wave64 per workgroup, four consecutive elements per lane.
+// Measured on MI355X at 251M elements, where a plain copy runs at 6.43 TB/s:
+// the update 0.630 ms (6.42 TB/s; a skipped step 0.21 ms), pack8 0.365 ms (6.91)
+// and unpack8 0.387 ms (6.51).  HBM counters: the update reads 5% more than its
+// bytes, because the 128-byte lines of the scale bytes hold eight waves' scales
+// and eight XCDs fetch each; giving an XCD 2, 4 or 8 consecutive tasks removes
+// that and is slower all the same (0.631, 0.633 and 0.634 ms).
 #include <hip/hip_runtime.h>
 
 #include <cmath>

@@ -269,7 +269,9 @@ struct Quad8 {
 // denominator needs, is what is stored.  A correctly rounded root and quotient
 // are about a third of the instructions, and with 16 bytes an element the
 // kernel is bound by those as much as by memory: a wave whose moments all lie
-// in the usual range takes the short forms of both (same results).
+// in the usual range takes the short forms of both (same results).  251M
+// elements, fp16: 0.630 ms; 0.662 with a zero moment in every wave, on the
+// general forms.
 __device__ __forceinline__ void adam8_four(const StepCoef& c, bool usual, float gscale, uint32_t key, int64_t e, int here,
                                            const float g[4], float p[4], u32x2& codes, uint32_t& scales) {
     float m[4], s[4], v[4];
