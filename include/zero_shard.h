@@ -652,8 +652,8 @@ int zero_moments8_unpack(float* exp_avg, float* exp_avg_sq, const void* moments8
  * first *device_bytes bytes to device memory, 16-byte aligned, and passes both
  * to the calls below.  With table NULL or capacity below *bytes it writes
  * only the sizes and returns ZERO_ENOSPC.  state_bits is 32, 8, or 0 for a
- * table of gradients only (the norm pass; other fields ignored).  About 8
- * bytes per 8192 elements and 80 per tensor.  A list whose buffers move needs
+ * table of gradients only (the norm pass; other fields ignored).  About 16
+ * bytes per 8192 elements and 180 per tensor.  A list whose buffers move needs
  * a new table (the device copy must not change under a step in flight).
  *
  * zero_multi_unscale_norm_overflow: as zero_shard_unscale_norm_overflow over

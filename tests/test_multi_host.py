@@ -15,7 +15,7 @@ from zero_sharded_mixed_partition_amd import _lib as L  # noqa: E402
 from test_binding_checks import FakeDev, FakeState  # noqa: E402
 
 AL = 1 << 40                        # a plausible, 16-byte aligned device address
-HDR = "<Iiiiiiqqqqqqqqqq"
+HDR = "<Iiiiiiqqqqqqqqqqqqq"
 
 
 def tensor(base, n, gdt=L.ZERO_BF16, pdt=L.ZERO_BF16, group=0, bits=32, **over):
@@ -58,14 +58,18 @@ def test_table_contents():
     st, buf, dev = build(tensors)
     assert st == L.ZERO_OK
     raw = buf.raw
-    (_, bits, n_groups, n_user, n_tensors, n_empty, n_chunks, desc_at, map_at, empty_at, device_bytes, ranges_at,
-     n_ranges, grads_at, n_grads, size) = struct.unpack_from(HDR, raw)
+    (_, bits, n_groups, n_user, n_tensors, n_empty, n_chunks, n_units, unit_log2, desc_at, chunks_at, units_at, empty_at,
+     device_bytes, ranges_at, n_ranges, grads_at, n_grads, size) = struct.unpack_from(HDR, raw)
     assert (bits, n_groups, n_user, n_tensors, n_empty) == (32, 3, 6, 4, 2)
     chunks = [-(-n // 8192) for n in sizes]
     assert n_chunks == sum(chunks) and device_bytes == dev <= size
-    refs = [struct.unpack_from("<II", raw, map_at + 8 * c) for c in range(n_chunks)]
+    refs = [struct.unpack_from("<II", raw, chunks_at + 8 * c) for c in range(n_chunks)]
     live = [i for i, n in enumerate(sizes) if n]
     assert refs == [(k, c) for k, i in enumerate(live) for c in range(chunks[i])]
+    # 1 + 32 + 33 + 157 tasks; 8 a unit take 8 + 32 + 40 + 160 workgroups, 16 take 272, over a tenth more
+    assert (unit_log2, n_units) == (3, 30)
+    refs = [struct.unpack_from("<II", raw, units_at + 8 * c) for c in range(n_units)]
+    assert refs == [(k, u) for k, i in enumerate(live) for u in range(-(-sizes[i] // 2048))]
     first = 0
     for k, i in enumerate(live):
         f = struct.unpack_from("<QQQQQqiiiIIIii", raw, desc_at + k * 80)
@@ -90,7 +94,7 @@ def test_table_joins_written_ranges():
                       exp_avg_sq=AL + (2 << 20) + 4 * n * i, grad=AL + (3 << 20) + 2 * n * i,
                       param_out=AL + (4 << 20) + 2 * n * i) for i in range(k)]
     st, buf, _ = build(tensors)
-    assert st == L.ZERO_OK and struct.unpack_from(HDR, buf.raw)[12] == 4
+    assert st == L.ZERO_OK and struct.unpack_from(HDR, buf.raw)[15] == 4
 
 
 def test_table_refusals():
@@ -134,7 +138,7 @@ def test_table_refuses_overlaps():
     assert build([tensor(AL, 33, exp_avg_sq=AL + (1 << 20) + 72)], 8)[0] == L.ZERO_OK
     # a table of gradients looks at nothing else
     st, buf, _ = build([L.zero_tensor(None, None, None, AL, None, 100, L.ZERO_F16, 0, 0, 0)] * 2, 0)
-    assert st == L.ZERO_OK and struct.unpack_from(HDR, buf.raw)[14] == 1     # gradients that overlap are one range
+    assert st == L.ZERO_OK and struct.unpack_from(HDR, buf.raw)[17] == 1     # gradients that overlap are one range
 
 
 def test_workspace():
@@ -143,8 +147,13 @@ def test_workspace():
     assert lib.zero_multi_norm_workspace_bytes(ctypes.create_string_buffer(256)) == 0
     small, large = table_of(5), table_of(5, 8192 * 5000, bits=0)      # gradients only: nothing overlaps
     assert lib.zero_multi_norm_workspace_bytes(small) == 256
-    # 512 blocks and 2 tensors: a partial each, the scale's factor, and a flag per block
-    assert lib.zero_multi_norm_workspace_bytes(large) == -(-((512 + 2 + 1) * 8 + 512 * 4) // 256) * 256
+    # blocks and tensors: a partial each, the scale's factor, and a flag per block
+    want = lambda blocks, tensors: -(-((blocks + tensors + 1) * 8 + blocks * 4) // 256) * 256  # noqa: E731
+    assert lib.zero_multi_norm_workspace_bytes(large) == want(512, 2)
+    short = table_of(5, 8192 * 4095, bits=0)
+    assert lib.zero_multi_norm_workspace_bytes(short) == want(1024, 2)
+    many = build([tensor(AL + (i << 28), 8192 * 3, group=0) for i in range(2000)], 0)[1]
+    assert lib.zero_multi_norm_workspace_bytes(many) == want(1024, 2000)
 
 
 D = AL + (1 << 39)                  # where the scalars and the table's device copy lie
@@ -424,13 +433,18 @@ def test_multi_adam_refuses_bad_lists():
         Z.ShardAdam8(FakeDev(5, F32), moments8=FakeDev(15, U8), scales8=FakeDev(2, U8))
 
 
-def test_table_phases():
+def test_table_phases_and_units():
     """32-bit tensors whose master starts off a 256-byte boundary: the update's
-    tasks start before the tensor, and take one chunk more where that spills."""
-    for off, n, bits, want in ((1, 8192, 32, (2, 1)), (63, 8130, 32, (2, 63)), (63, 8129, 32, (1, 63)), (64, 8192, 32, (1, 0)),
-                               (1, 8192, 8, (1, 0)), (5, 1, 32, (1, 5))):
-        st, buf, _ = build([tensor(AL, n, master=AL + 4 * off)], bits)
+    tasks start before the tensor, and take one more where that spills.  Units
+    are as large as idle workgroups (at most a tenth of the tasks) allow."""
+    for off, n, bits, count, want in ((1, 8192, 32, 1, (1, 2, 9)), (0, 8192, 32, 1, (0, 5, 1)), (64, 8192, 32, 1, (0, 5, 1)),
+                                      (63, 8130, 32, 1, (63, 2, 9)), (63, 8129, 32, 1, (63, 5, 1)),
+                                      (1, 8192, 8, 1, (0, 5, 1)), (5, 1, 32, 1, (5, 0, 1)), (0, 500, 32, 30, (0, 1, 30)),
+                                      (0, 64, 8, 30, (0, 0, 30)), (0, 256 * 60, 32, 2, (0, 5, 4))):
+        st, buf, _ = build([tensor(AL + (i << 28), n, master=AL + (i << 28) + 4 * off) for i in range(count)], bits)
         assert st == L.ZERO_OK
-        hdr = struct.unpack_from(HDR, buf.raw)
-        f = struct.unpack_from("<QQQQQqiiiIIIii", buf.raw, hdr[7])
-        assert (f[11], f[12]) == want == (hdr[6], f[12]), (off, n, bits)
+        h = struct.unpack_from(HDR, buf.raw)
+        f = struct.unpack_from("<QQQQQqiiiIIIii", buf.raw, h[9])
+        assert (f[12], h[8], h[7]) == want, (off, n, bits, f[12], h[8], h[7])
+
+

@@ -202,9 +202,13 @@ __device__ __forceinline__ uint32_t encode4_nearest(const float x[4], float scal
 // ---------------------------------------------------------------- one task of the step
 
 // Root and quotient, correctly rounded as sqrtf and / give them, without their
-// scaling and special cases: root_normal for every v in [2^-96, FLT_MAX]
-// (all 1.9e9 of them compared), quotient_normal where no step under- or
-// overflows (2.6e10 random pairs compared).
+// scaling and special cases.  root_normal: for every v in [2^-96, FLT_MAX] (all
+// 1.9e9 of them compared).  quotient_normal: where no step under- or overflows.
+// There y is the correctly rounded reciprocal (all 2^23 mantissas compared), so
+// a * y is off by at most 1.5 units in the last place, the residual is exact,
+// and the last step can only misround a quotient that lies within 3 / (2D)
+// units of the middle between two floats, D being d's mantissa as an integer;
+// all quotients within 64 / (2D) units of one (3.7e8) were compared.
 __device__ __forceinline__ float root_normal(float v) {
     const float y = __builtin_amdgcn_rsqf(v);
     const float s = v * y;

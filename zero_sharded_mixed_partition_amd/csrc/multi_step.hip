@@ -3,10 +3,10 @@
 //
 // The list is described once, in a table (zero_multi_table_build): one
 // descriptor per tensor (its pointers, element types and hyperparameter group)
-// and one entry per chunk of kChunk elements naming its tensor.  A workgroup
-// finds its work with two dependent scalar loads, whatever the number and the
-// sizes of the tensors, and a tensor of a few hundred elements costs a few
-// idle workgroups.  The map costs 8 bytes per 8192 elements.
+// and two maps, from the norm pass's chunks and from the update's units of work
+// to their tensors.  A workgroup finds its work with two dependent scalar
+// loads, whatever the number and the sizes of the tensors.  Each map costs 8
+// bytes per 8192 elements, the second one more where tensors are small.
 //
 //  multi_sqnorm + multi_norm_finish: each block sums the exact fp64 squares
 //          of its chunks and leaves one partial per tensor it meets, in a slot
@@ -30,8 +30,13 @@
 namespace zero_shard {
 namespace {
 
-constexpr int64_t kChunk = 8192;                          // elements per map entry
-constexpr int kTasksPerChunk = (int)(kChunk / kTask);
+constexpr int64_t kChunk = 8192;                          // elements per entry of the norm pass's map
+// A unit of the update is 2^k consecutive tasks of one tensor, k <= kMaxUnit;
+// a tensor's last unit leaves workgroups idle.  The table takes the largest k
+// whose workgroups exceed the tasks by no more than a tenth: 3,000 tensors of
+// 500 elements take 2 tasks a unit and 9.7 us, with 32 a unit 108 us (8 bits:
+// 10.6 and 82); 39 tensors of 1.07B elements keep 32 a unit and a map of 1 MB.
+constexpr int kMaxUnit = 5;
 // LDS reserved per one-wave workgroup and never used, to cap residency (as for
 // the shards' updates).  Measured on MI355X, 1.07B elements in 39 tensors with
 // bf16 gradients and copies: 32 bits 6.62 TB/s at 15 KiB (10 resident per CU),
@@ -40,6 +45,11 @@ constexpr int kTasksPerChunk = (int)(kChunk / kTask);
 // 6.32 TB/s (10 KiB).
 constexpr size_t kLds32 = 15 * 1024, kLds8 = 7 * 1024;
 constexpr int64_t kMultiMaxGrid = (int64_t(1) << 26) - 1;
+// Blocks of the norm pass: 512 (2 per CU, as the shard's pass) for long runs of
+// chunks, twice as many where a block would meet several tensors or only a few
+// chunks.  1.07B elements in 39 tensors: 306 us with 512, 311 with 1024; 67M in
+// 4: 24.5 and 25.6; 17M in 4: 10.0 and 9.4; 3,000 tensors of 500: 13.8 and
+// 11.0; 10,000 of 64: 26.2 and 18.3.
 constexpr int kMultiNormBlocks = 512;
 // A list's fp32 tensors may start anywhere.  The update's tasks are laid out so
 // that the master's runs start at multiples of 256 bytes: otherwise two waves,
@@ -68,12 +78,12 @@ struct TensorDesc {
     int32_t reserved;
 };
 
-struct ChunkRef {
-    uint32_t tensor, chunk;   // index of the descriptor, and which chunk of that tensor
+struct PieceRef {
+    uint32_t tensor, piece;   // index of the descriptor, and which chunk or unit of that tensor
 };
 
 // At the start of the table.  The device image is [0, device_bytes): this
-// header, the descriptors of the tensors that hold elements, the chunk map and
+// header, the descriptors of the tensors that hold elements, the two maps and
 // the caller's indices of the empty ones.  The host part behind it holds the
 // address ranges that the update writes and those of the gradients, each merged
 // and sorted, so that a call checks a pointer against the whole list at once.
@@ -81,8 +91,9 @@ struct TableHeader {
     uint32_t magic;
     int32_t state_bits, n_groups;
     int32_t n_user, n_tensors, n_empty;
-    int64_t n_chunks;
-    int64_t desc_at, map_at, empty_at, device_bytes;
+    int64_t n_chunks, n_units;
+    int64_t unit_log2;
+    int64_t desc_at, chunks_at, units_at, empty_at, device_bytes;
     int64_t ranges_at, n_ranges;
     int64_t grads_at, n_grads, bytes;
 };
@@ -99,14 +110,19 @@ const T* at(const void* table, int64_t offset) {
 // What the kernels need of a table, by value.
 struct TableRef {
     const TensorDesc* desc;
-    const ChunkRef* map;
+    const PieceRef* chunks;
+    const PieceRef* units;
     const uint32_t* empty;
-    int64_t n_chunks;
+    int64_t n_chunks, n_units;
+    int32_t unit_log2;
     int32_t n_tensors, n_empty;
 
     // the table does not change while a kernel runs: scalar reads
-    __device__ __forceinline__ const ZS_CONSTANT ChunkRef& chunk(int64_t i) const {
-        return ((const ZS_CONSTANT ChunkRef*)map)[i];
+    __device__ __forceinline__ const ZS_CONSTANT PieceRef& chunk(int64_t i) const {
+        return ((const ZS_CONSTANT PieceRef*)chunks)[i];
+    }
+    __device__ __forceinline__ const ZS_CONSTANT PieceRef& unit(int64_t i) const {
+        return ((const ZS_CONSTANT PieceRef*)units)[i];
     }
     __device__ __forceinline__ const ZS_CONSTANT TensorDesc& tensor(int64_t i) const {
         return ((const ZS_CONSTANT TensorDesc*)desc)[i];
@@ -133,7 +149,7 @@ __device__ __forceinline__ void tensor_squares(const void* G, int64_t n, uint32_
         for (int u = 0; u < kLoads; ++u) accumulate_vec<DT>(q[u], acc, bad);
     }
     if (c == stop) return;
-    // the tensor's last, partial chunk (the update may have one chunk more, which holds nothing here)
+    // the tensor's last, partial chunk
     for (int64_t i = (int64_t)c * kChunk + threadIdx.x * kPer; i < n; i += kBlock * kPer) {
         if (i + kPer <= n) {
             accumulate_vec<DT>(ld16_any(static_cast<const char*>(G) + i * kSize), acc, bad);
@@ -167,9 +183,9 @@ __global__ __launch_bounds__(kBlock) void multi_sqnorm(TableRef t, double inv2, 
     const int64_t end = block_begin((int64_t)blockIdx.x + 1, gridDim.x, t.n_chunks);
     uint32_t all_bad = 0;
     for (int64_t c = block_begin(blockIdx.x, gridDim.x, t.n_chunks); c < end;) {
-        const ZS_CONSTANT ChunkRef& ref = t.chunk(c);
+        const ZS_CONSTANT PieceRef& ref = t.chunk(c);
         const ZS_CONSTANT TensorDesc& d = t.tensor(ref.tensor);
-        const uint32_t first = ref.chunk, left = d.n_chunks - first;
+        const uint32_t first = ref.piece, left = d.n_chunks - first;
         const uint32_t stop = first + (left < end - c ? left : (uint32_t)(end - c));
         double acc = 0.0;
         uint32_t bad = 0;
@@ -354,9 +370,10 @@ struct CoefSet {
 template <int BITS>
 __device__ __forceinline__ void list_wave(const TableRef& t, int64_t w, const StepCoef* coefs, const uint32_t* keys,
                                           uint32_t key, const double* d_sq) {
-    const ZS_CONSTANT ChunkRef& ref = t.chunk(w / kTasksPerChunk);
+    const ZS_CONSTANT PieceRef& ref = t.unit(w >> t.unit_log2);
     const ZS_CONSTANT TensorDesc& d = t.tensor(ref.tensor);
-    const int64_t base = (int64_t)ref.chunk * kChunk + (w % kTasksPerChunk) * kTask - (BITS == 32 ? d.shift : 0);
+    const int64_t task = ((int64_t)ref.piece << t.unit_log2) + (w & ((1 << t.unit_log2) - 1));
+    const int64_t base = task * kTask - (BITS == 32 ? d.shift : 0);
     if (base >= d.numel) return;
     const StepCoef c = coefs[d.group];
     if (keys != nullptr) key = keys[d.group];
@@ -369,7 +386,7 @@ template <int BITS>
 __global__ __launch_bounds__(kTaskThreads) void multi_adam(CoefSet cs, TableRef t, const double* __restrict__ d_sq,
                                                            const int32_t* __restrict__ d_ovf) {
     if (d_ovf != nullptr && *d_ovf != 0) return;          // skipped step: nothing is written
-    for (int64_t w = blockIdx.x; w < t.n_chunks * kTasksPerChunk; w += gridDim.x)
+    for (int64_t w = blockIdx.x; w < t.n_units << t.unit_log2; w += gridDim.x)
         list_wave<BITS>(t, w, cs.c, cs.key, 0, d_sq);
 }
 
@@ -380,7 +397,7 @@ __global__ __launch_bounds__(kTaskThreads) void multi_adam_devcoef(const StepCoe
                                                                    const int32_t* __restrict__ d_ovf) {
     if (d_ovf != nullptr && *d_ovf != 0) return;
     const uint32_t key = BITS == 8 ? dither_key(seed, (uint64_t)*d_step) : 0;
-    for (int64_t w = blockIdx.x; w < t.n_chunks * kTasksPerChunk; w += gridDim.x)
+    for (int64_t w = blockIdx.x; w < t.n_units << t.unit_log2; w += gridDim.x)
         list_wave<BITS>(t, w, coefs, nullptr, key, d_sq);
 }
 
@@ -388,13 +405,15 @@ __global__ __launch_bounds__(kTaskThreads) void multi_adam_devcoef(const StepCoe
 
 int64_t pad16(int64_t x) { return (x + 15) & ~(int64_t)15; }
 
-// at least one block: it also leaves the factor for the second kernel
-int norm_grid(int64_t n_chunks) {
-    return (int)(n_chunks < 1 ? 1 : n_chunks < kMultiNormBlocks ? n_chunks : kMultiNormBlocks);
+// At least one block: it also leaves the factor for the second kernel.
+int norm_grid(const TableHeader& h) {
+    const bool short_runs = h.n_chunks <= 8 * kMultiNormBlocks || h.n_chunks < 8 * (int64_t)h.n_tensors;
+    const int64_t most = short_runs ? 2 * kMultiNormBlocks : kMultiNormBlocks;
+    return (int)(h.n_chunks < 1 ? 1 : h.n_chunks < most ? h.n_chunks : most);
 }
 
 size_t norm_workspace(const TableHeader& h) {
-    const size_t nb = (size_t)norm_grid(h.n_chunks);
+    const size_t nb = (size_t)norm_grid(h);
     return (((nb + (size_t)h.n_tensors + 1) * sizeof(double) + nb * sizeof(uint32_t)) + 255) & ~(size_t)255;
 }
 
@@ -411,8 +430,9 @@ int read_table(const void* table, const void* d_table, TableHeader* h) {
 }
 
 TableRef table_ref(const TableHeader& h, const void* d_table) {
-    return TableRef{at<TensorDesc>(d_table, h.desc_at), at<ChunkRef>(d_table, h.map_at),
-                    at<uint32_t>(d_table, h.empty_at), h.n_chunks, h.n_tensors, h.n_empty};
+    return TableRef{at<TensorDesc>(d_table, h.desc_at), at<PieceRef>(d_table, h.chunks_at),
+                    at<PieceRef>(d_table, h.units_at), at<uint32_t>(d_table, h.empty_at), h.n_chunks, h.n_units,
+                    (int32_t)h.unit_log2, h.n_tensors, h.n_empty};
 }
 
 // Whether [p, p + bytes) meets one of n sorted, disjoint address ranges.
@@ -491,7 +511,7 @@ int multi_norm(const void* table, const void* d_table, double inv2, const double
     for (int j = 0; j < 6; ++j)
         if (meets(at<AddressRange>(table, h.grads_at), h.n_grads, out[j].p, out[j].bytes))
             return fail(ZERO_EINVAL, "an output of the norm pass lies in a gradient");
-    const int nb = norm_grid(h.n_chunks);
+    const int nb = norm_grid(h);
     double* slots = static_cast<double*>(d_workspace);
     uint32_t* flags = reinterpret_cast<uint32_t*>(slots + nb + h.n_tensors + 1);
     const TableRef t = table_ref(h, d_table);
@@ -519,7 +539,7 @@ int check_update(const void* table, const void* d_table, int32_t n_groups, const
 }
 
 dim3 update_grid(const TableHeader& h) {
-    const int64_t w = h.n_chunks * kTasksPerChunk;
+    const int64_t w = h.n_units << h.unit_log2;
     return dim3((unsigned)(w < kMultiMaxGrid ? w : kMultiMaxGrid));
 }
 
@@ -534,8 +554,15 @@ int32_t phase_of(const zero_tensor& t, int32_t state_bits) {
     return state_bits == 32 ? (int32_t)(reinterpret_cast<uintptr_t>(t.master) / sizeof(float) % kPhase) : 0;
 }
 
-int64_t chunks_of(const zero_tensor& t, int32_t state_bits) {
-    return (t.numel + phase_of(t, state_bits) + kChunk - 1) / kChunk;
+int64_t chunks_of(const zero_tensor& t) { return (t.numel + kChunk - 1) / kChunk; }
+
+// Tasks of the update that a tensor takes (0 for an empty one).
+int64_t tasks_of(const zero_tensor& t, int32_t state_bits) {
+    return t.numel ? (t.numel + phase_of(t, state_bits) + kTask - 1) / kTask : 0;
+}
+
+int64_t units_of(const zero_tensor& t, int32_t state_bits, int unit_log2) {
+    return (tasks_of(t, state_bits) + (1 << unit_log2) - 1) >> unit_log2;
 }
 
 int build_table(const zero_tensor* tensors, int32_t n_tensors, int32_t state_bits, void* table, size_t capacity,
@@ -569,7 +596,7 @@ int build_table(const zero_tensor* tensors, int32_t n_tensors, int32_t state_bit
             ++h.n_empty;
             continue;
         }
-        h.n_chunks += chunks_of(t, state_bits);
+        h.n_chunks += chunks_of(t);
         if (h.n_chunks > (int64_t)UINT32_MAX) return fail(ZERO_ERANGE, "the list is too long");
         ++h.n_tensors;
         if (t.grad == nullptr) return fail(ZERO_EINVAL, "tensor %d: grad is NULL", i);
@@ -607,9 +634,20 @@ int build_table(const zero_tensor* tensors, int32_t n_tensors, int32_t state_bit
         if (!ranges.empty() && ranges.back().hi == r.lo) ranges.back().hi = r.hi;
         else ranges.push_back({r.lo, r.hi});
     }
+    if (state_bits) {
+        int64_t tasks = 0;
+        for (int32_t i = 0; i < n_tensors; ++i) tasks += tasks_of(tensors[i], state_bits);
+        for (h.unit_log2 = kMaxUnit;; --h.unit_log2) {
+            h.n_units = 0;
+            for (int32_t i = 0; i < n_tensors; ++i) h.n_units += units_of(tensors[i], state_bits, (int)h.unit_log2);
+            if (h.unit_log2 == 0 || (h.n_units << h.unit_log2) <= tasks + tasks / 10) break;
+        }
+        if (h.n_units > (int64_t)UINT32_MAX) return fail(ZERO_ERANGE, "the list is too long");
+    }
     h.desc_at = pad16((int64_t)sizeof(TableHeader));
-    h.map_at = pad16(h.desc_at + h.n_tensors * (int64_t)sizeof(TensorDesc));
-    h.empty_at = pad16(h.map_at + h.n_chunks * (int64_t)sizeof(ChunkRef));
+    h.chunks_at = pad16(h.desc_at + h.n_tensors * (int64_t)sizeof(TensorDesc));
+    h.units_at = pad16(h.chunks_at + h.n_chunks * (int64_t)sizeof(PieceRef));
+    h.empty_at = pad16(h.units_at + h.n_units * (int64_t)sizeof(PieceRef));
     h.device_bytes = pad16(h.empty_at + h.n_empty * (int64_t)sizeof(uint32_t));
     h.ranges_at = h.device_bytes;
     h.n_ranges = (int64_t)ranges.size();
@@ -623,6 +661,8 @@ int build_table(const zero_tensor* tensors, int32_t n_tensors, int32_t state_bit
     char* out = static_cast<char*>(table);
     std::memset(out, 0, (size_t)h.bytes);
     std::memcpy(out, &h, sizeof(h));
+    PieceRef* chunks = reinterpret_cast<PieceRef*>(out + h.chunks_at);
+    PieceRef* units = reinterpret_cast<PieceRef*>(out + h.units_at);
     uint32_t chunk = 0, tensor = 0, empty = 0;
     for (int32_t i = 0; i < n_tensors; ++i) {
         const zero_tensor& t = tensors[i];
@@ -637,7 +677,7 @@ int build_table(const zero_tensor* tensors, int32_t n_tensors, int32_t state_bit
         d.gdt = t.grad_dtype;
         d.user = (uint32_t)i;
         d.first_chunk = chunk;
-        d.n_chunks = (uint32_t)chunks_of(t, state_bits);
+        d.n_chunks = (uint32_t)chunks_of(t);
         d.shift = phase_of(t, state_bits);
         if (state_bits) {
             d.master = t.master;
@@ -648,11 +688,10 @@ int build_table(const zero_tensor* tensors, int32_t n_tensors, int32_t state_bit
             d.group = t.group;
         }
         std::memcpy(out + h.desc_at + tensor * sizeof(d), &d, sizeof(d));
-        for (uint32_t c = 0; c < d.n_chunks; ++c) {
-            const ChunkRef r{tensor, c};
-            std::memcpy(out + h.map_at + (int64_t)(chunk + c) * (int64_t)sizeof(r), &r, sizeof(r));
-        }
+        for (uint32_t c = 0; c < d.n_chunks; ++c) *chunks++ = PieceRef{tensor, c};
         chunk += d.n_chunks;
+        const uint32_t n_units = state_bits ? (uint32_t)units_of(t, state_bits, (int)h.unit_log2) : 0;
+        for (uint32_t u = 0; u < n_units; ++u) *units++ = PieceRef{tensor, u};
         ++tensor;
     }
     if (!ranges.empty()) std::memcpy(out + h.ranges_at, ranges.data(), ranges.size() * sizeof(AddressRange));
@@ -755,7 +794,7 @@ int zero_multi_adam_step(const void* table, const void* d_table, const zero_adam
         if (cs.c[g].clip && d_global_sqnorm == nullptr) return fail(ZERO_EINVAL, "clipping needs d_global_sqnorm");
         cs.key[g] = dither_key(seed, (uint64_t)hp[g].step);
     }
-    if (h.n_chunks == 0) return ZERO_OK;
+    if (h.n_units == 0) return ZERO_OK;
     const hipStream_t s = static_cast<hipStream_t>(hip_stream);
     const TableRef t = table_ref(h, d_table);
     if (h.state_bits == 8)
@@ -782,7 +821,7 @@ int zero_multi_adam_step_coef(const void* table, const void* d_table, const void
     if (written(table, h, d_coefs, (int64_t)n_groups * (int64_t)sizeof(StepCoef)) ||
         written(table, h, d_step, sizeof(int64_t)))
         return fail(ZERO_EINVAL, "d_coefs or d_step lies in a buffer the update writes");
-    if (h.n_chunks == 0) return ZERO_OK;
+    if (h.n_units == 0) return ZERO_OK;
     const hipStream_t s = static_cast<hipStream_t>(hip_stream);
     const TableRef t = table_ref(h, d_table);
     const StepCoef* c = static_cast<const StepCoef*>(d_coefs);

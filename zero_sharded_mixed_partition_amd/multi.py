@@ -23,6 +23,14 @@ from .moments8 import _buf, _codes_bytes, _current_device, _scales_bytes, _seed
 MAX_GROUPS = 16
 
 
+def _f32_bytes(n: int) -> int:
+    return 4 * n
+
+
+def _where(grads):
+    return [(g.data_ptr(), g.dtype) for g in grads]
+
+
 class TensorTable:
     """The list's table (zero_multi_table_build): a host part and its device
     copy.  Holds references to the tensors.  groups: hyperparameter group per
@@ -49,7 +57,8 @@ class TensorTable:
         self.masters, self.exp_avgs, self.exp_avg_sqs = own(masters), own(exp_avgs), own(exp_avg_sqs)
         self.params_out, self.groups = own(params_out), own(groups)
         self.n_groups = 1 + max(self.groups) if self.groups else 1
-        self._kept = []                        # descriptions that recorded graphs read
+        self._kept = []                        # tables that recorded graphs read
+        self._describe(grads)
         self._build(grads)
 
     @classmethod
@@ -58,14 +67,13 @@ class TensorTable:
         return cls(None, None, None, grads, state_bits=0)
 
     def set_grads(self, grads) -> None:
-        """Describe the list anew with other gradient tensors (a no-op if they
-        lie where the present ones do).  The new device copy is enqueued on the
+        """Describe the list anew with other gradient tensors of the same lengths
+        (a no-op if they lie where the present ones do).  The new device copy is enqueued on the
         current stream.  A graph recorded with the table keeps reading the old
         description (which the table then keeps alive): record it again."""
         if len(grads) != self.n_tensors:
             raise ValueError(f"{len(grads)} gradients for {self.n_tensors} tensors")
-        now = tuple((g.data_ptr(), g.dtype, g.numel()) for g in grads)
-        if now != self._grad_key:
+        if _where(grads) != self._grad_key:
             old, captured = (self.host, self.device), self._captured
             self._build(grads)
             if captured:
@@ -73,26 +81,32 @@ class TensorTable:
             elif old[1] is not None:
                 old[1].record_stream(torch.cuda.current_stream())    # a step there may still read it
 
-    def _build(self, grads) -> None:
-        grads = list(grads)
-        arr = (_L.zero_tensor * max(1, self.n_tensors))()
-        bits, index = self.state_bits, -1
-        if self.n_tensors:
-            index = grads[0].get_device() if hasattr(grads[0], "get_device") else -1
-        for i, g in enumerate(grads):
-            n, t = g.numel(), arr[i]
-            t.grad, t.numel, t.grad_dtype = _buf(g, None, 0, f"grads[{i}]", index), n, dtype_code(g)
-            if not bits:
-                continue
-            kinds = (torch.uint8, _codes_bytes(n), _scales_bytes(n)) if bits == 8 else (torch.float32, 4 * n, 4 * n)
-            t.master = _buf(self.masters[i], torch.float32, 4 * n, f"masters[{i}]", index, n)
-            t.exp_avg = _buf(self.exp_avgs[i], kinds[0], kinds[1], f"exp_avgs[{i}]", index)
-            t.exp_avg_sq = _buf(self.exp_avg_sqs[i], kinds[0], kinds[2], f"exp_avg_sqs[{i}]", index)
+    def _describe(self, grads) -> None:
+        """The C descriptions of the whole list."""
+        self._c = (_L.zero_tensor * max(1, self.n_tensors))()
+        bits = self.state_bits
+        self._index = grads[0].get_device() if grads and hasattr(grads[0], "get_device") else -1
+        self._numels = [g.numel() for g in grads]
+        if not bits:
+            return
+        kinds = (torch.uint8, _codes_bytes, _scales_bytes) if bits == 8 else (torch.float32, _f32_bytes, _f32_bytes)
+        for i, n in enumerate(self._numels):
+            t = self._c[i]
+            t.master = _buf(self.masters[i], torch.float32, 4 * n, f"masters[{i}]", self._index, n)
+            t.exp_avg = _buf(self.exp_avgs[i], kinds[0], kinds[1](n), f"exp_avgs[{i}]", self._index)
+            t.exp_avg_sq = _buf(self.exp_avg_sqs[i], kinds[0], kinds[2](n), f"exp_avg_sqs[{i}]", self._index)
             p = None if self.params_out is None else self.params_out[i]
             if p is not None:
-                t.param_out, t.param_dtype = _buf(p, None, 2 * n, f"params_out[{i}]", index, n), dtype_code(p)
+                t.param_out, t.param_dtype = _buf(p, None, 2 * n, f"params_out[{i}]", self._index, n), dtype_code(p)
             if self.groups is not None:
                 t.group = int(self.groups[i])
+
+    def _build(self, grads) -> None:
+        """The table for these gradients, the rest of the list being described."""
+        arr, bits, index = self._c, self.state_bits, self._index
+        for i, (g, n) in enumerate(zip(grads, self._numels)):
+            t = arr[i]
+            t.grad, t.numel, t.grad_dtype = _buf(g, None, 0, f"grads[{i}]", index, n), n, dtype_code(g)
         size, dev_size = ctypes.c_size_t(), ctypes.c_size_t()
         build = _L.lib().zero_multi_table_build
         st = build(arr, self.n_tensors, bits, None, 0, ctypes.byref(size), ctypes.byref(dev_size))
@@ -106,10 +120,10 @@ class TensorTable:
         host = torch.empty(size.value, dtype=torch.uint8, pin_memory=on_gpu)
         _L.check(build(arr, self.n_tensors, bits, host.data_ptr(), size.value, ctypes.byref(size),
                        ctypes.byref(dev_size)), "zero_multi_table_build")
-        self.grads, self.host = grads, host
-        self._grad_key = tuple((g.data_ptr(), g.dtype, g.numel()) for g in grads)
+        self.grads, self.host = list(grads), host
+        self._grad_key = _where(grads)
         self.device = host[:dev_size.value].to(torch.device("cuda", index), non_blocking=True) if on_gpu else None
-        self._index, self._captured = index, False
+        self._captured = False
         self._addresses = self.host.data_ptr(), None if self.device is None else self.device.data_ptr()
 
     def _ptrs(self, current: int):

@@ -118,8 +118,8 @@ class MultiAdam:
              allreduce: Optional[Callable[[torch.Tensor, torch.Tensor], None]] = None,
              unscaled: bool = False) -> Optional[bool]:
         """One full step.  grads: this step's gradients, where they are not in the
-        buffers given before (the table is then described anew: a host-side
-        cost of some microseconds a tensor).  allreduce as in ShardAdam.step.
+        buffers given before (the table is then built anew, which costs the host
+        about a microsecond a tensor).  allreduce as in ShardAdam.step.
         unscaled: the gradients are already divided by the loss scale.  Returns
         True if the step was skipped (None with device_state)."""
         if grads is not None:
