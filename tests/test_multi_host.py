@@ -402,6 +402,12 @@ def test_tensors_on_another_device_are_refused(monkeypatch):
             args[i] = Placed(t.numel(), t.dtype, t.data_ptr(), index=0 if i == k else 1)
         with pytest.raises(ValueError, match="current device is cuda:1"):
             Z.zero_shard_adam8_step(*args, Z.AdamHyper(), stream=0)
+    class OtherStream:
+        device_index, cuda_stream = 0, 4096
+
+    with pytest.raises(ValueError, match="stream of cuda:0"):
+        Z.zero_shard_adam8_step(*(Placed(t.numel(), t.dtype, t.data_ptr(), index=1) for t in args), Z.AdamHyper(),
+                                stream=OtherStream())
     m, a, b, g, p = fake_list([100, 7])
     t = Z.TensorTable(m, a, b, g, p)
     t._index = 0

@@ -103,7 +103,7 @@ def dtype_code(t) -> int:
 _raw_stream = None
 
 
-def _stream(stream) -> Optional[int]:
+def _stream(stream, device: int = -1) -> Optional[int]:
     if stream is None:
         import torch
         global _raw_stream
@@ -111,7 +111,9 @@ def _stream(stream) -> Optional[int]:
             # torch's handle of the current stream without a Stream object around it (2.5 us less per call)
             _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                                   lambda _: torch.cuda.current_stream().cuda_stream)
-        return _raw_stream(torch.cuda.current_device())
+        return _raw_stream(torch.cuda.current_device() if device < 0 else device)
+    if device >= 0 and getattr(stream, "device_index", device) != device:
+        raise ValueError(f"stream of cuda:{stream.device_index}, the current device is cuda:{device}")
     return getattr(stream, "cuda_stream", stream)
 
 

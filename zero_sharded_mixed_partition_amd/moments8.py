@@ -28,7 +28,17 @@ def zero_scales8_bytes(n: int) -> int:
 
 
 def _current_device() -> int:
-    return torch.cuda.current_device() if torch.cuda.is_initialized() else -1
+    return torch.cuda.current_device() if _on_gpu or _gpu_in_use() else -1
+
+
+_on_gpu = False
+
+
+def _gpu_in_use() -> bool:
+    """Whether this process has a GPU context (remembered once it has)."""
+    global _on_gpu
+    _on_gpu = torch.cuda.is_initialized()
+    return _on_gpu
 
 
 def _buf(t, dtype, nbytes: int, what: str, device: int, exact: int = -1) -> Optional[int]:
@@ -43,14 +53,13 @@ def _buf(t, dtype, nbytes: int, what: str, device: int, exact: int = -1) -> Opti
     n = t.numel()
     if exact >= 0 and n != exact:
         raise ValueError(f"{what}: {n} elements, {exact} expected")
-    if not t.is_cuda:
-        raise ValueError(f"{what}: device tensor expected")
+    if not (t.get_device() == device if device >= 0 else t.is_cuda):
+        raise ValueError(f"{what}: " + (f"on {t.device}, the current device is cuda:{device}" if device >= 0 and t.is_cuda
+                                        else "device tensor expected"))
     if not t.is_contiguous():
         raise ValueError(f"{what}: contiguous tensor expected")
     if n * t.element_size() < nbytes:
         raise ValueError(f"{what}: {n * t.element_size()} bytes, the call accesses {nbytes}")
-    if device >= 0 and t.get_device() != device:
-        raise ValueError(f"{what}: on {t.device}, the current device is cuda:{device}")
     return t.data_ptr()
 
 
@@ -87,7 +96,7 @@ def zero_shard_adam8_step(master, moments8, scales8, grad, param_out, hp: AdamHy
     pm, pc, ps, pg, pp = _step8_ptrs(master, moments8, scales8, grad, gd, param_out, n, dev)
     _L.check(_L.lib().zero_shard_adam8_step(pm, pc, ps, pg, gd, pp, pd, n, ctypes.byref(params), _seed(seed),
                                             _buf(global_sqnorm, torch.float64, 8, "global_sqnorm", dev),
-                                            _buf(global_overflow, torch.int32, 4, "global_overflow", dev), _stream(stream)),
+                                            _buf(global_overflow, torch.int32, 4, "global_overflow", dev), _stream(stream, dev)),
              "zero_shard_adam8_step")
 
 
@@ -106,7 +115,7 @@ def zero_shard_adam8_step_coef(master, moments8, scales8, grad, param_out, d_coe
                                                  _buf(d_step, torch.int64, 8, "d_step", dev),
                                                  _buf(global_sqnorm, torch.float64, 8, "global_sqnorm", dev),
                                                  _buf(global_overflow, torch.int32, 4, "global_overflow", dev),
-                                                 _stream(stream)), "zero_shard_adam8_step_coef")
+                                                 _stream(stream, dev)), "zero_shard_adam8_step_coef")
 
 
 def zero_moments8_pack(moments8, scales8, exp_avg, exp_avg_sq, n: Optional[int] = None, stream=None) -> None:
@@ -116,7 +125,7 @@ def zero_moments8_pack(moments8, scales8, exp_avg, exp_avg_sq, n: Optional[int] 
     _L.check(_L.lib().zero_moments8_pack(_buf(moments8, torch.uint8, _codes_bytes(n), "moments8", dev),
                                          _buf(scales8, torch.uint8, _scales_bytes(n), "scales8", dev),
                                          _buf(exp_avg, torch.float32, 4 * n, "exp_avg", dev), _buf(exp_avg_sq, torch.float32, 4 * n, "exp_avg_sq", dev), n,
-                                         _stream(stream)), "zero_moments8_pack")
+                                         _stream(stream, dev)), "zero_moments8_pack")
 
 
 def zero_moments8_unpack(exp_avg, exp_avg_sq, moments8, scales8, n: Optional[int] = None, stream=None) -> None:
@@ -125,5 +134,5 @@ def zero_moments8_unpack(exp_avg, exp_avg_sq, moments8, scales8, n: Optional[int
     dev = _current_device()
     _L.check(_L.lib().zero_moments8_unpack(_buf(exp_avg, torch.float32, 4 * n, "exp_avg", dev), _buf(exp_avg_sq, torch.float32, 4 * n, "exp_avg_sq", dev),
                                            _buf(moments8, torch.uint8, _codes_bytes(n), "moments8", dev),
-                                           _buf(scales8, torch.uint8, _scales_bytes(n), "scales8", dev), n, _stream(stream)),
+                                           _buf(scales8, torch.uint8, _scales_bytes(n), "scales8", dev), n, _stream(stream, dev)),
              "zero_moments8_unpack")

@@ -140,7 +140,7 @@ def zero_multi_norm_workspace_bytes(table: TensorTable) -> int:
 
 def _norm_args(table, sqnorm, overflow, tensor_sqnorm, workspace):
     dev = _current_device()
-    return (table._ptrs(dev),
+    return (dev, table._ptrs(dev),
             (_buf(sqnorm, torch.float64, 8, "sqnorm", dev), _buf(overflow, torch.int32, 4, "overflow", dev),
              _buf(tensor_sqnorm, torch.float64, 8 * table.n_tensors, "tensor_sqnorm", dev)),
             (_buf(workspace, None, 0, "workspace", dev), workspace.numel() * workspace.element_size()))
@@ -151,8 +151,8 @@ def zero_multi_unscale_norm_overflow(table: TensorTable, inv_loss_scale: float, 
     """Enqueue the norm pass over the list's gradients: sqnorm (float64 [1]),
     overflow (int32 [1]) and, if given, each tensor's own sum of squares
     (tensor_sqnorm, float64 [n_tensors])."""
-    tab, out, ws = _norm_args(table, sqnorm, overflow, tensor_sqnorm, workspace)
-    _L.check(_L.lib().zero_multi_unscale_norm_overflow(*tab, float(inv_loss_scale), *out, *ws, _stream(stream)),
+    dev, tab, out, ws = _norm_args(table, sqnorm, overflow, tensor_sqnorm, workspace)
+    _L.check(_L.lib().zero_multi_unscale_norm_overflow(*tab, float(inv_loss_scale), *out, *ws, _stream(stream, dev)),
              "zero_multi_unscale_norm_overflow")
 
 
@@ -160,9 +160,9 @@ def zero_multi_unscale_norm_overflow_dev(table: TensorTable, state: StepState, s
                                          tensor_sqnorm=None, unscaled: bool = False, stream=None) -> None:
     """The norm pass with the loss scale from the device state; unscaled: the
     gradients are already unscaled."""
-    tab, out, ws = _norm_args(table, sqnorm, overflow, tensor_sqnorm, workspace)
+    dev, tab, out, ws = _norm_args(table, sqnorm, overflow, tensor_sqnorm, workspace)
     _L.check(_L.lib().zero_multi_unscale_norm_overflow_dev(*tab, 1 if unscaled else 0, state.ptr(), *out, *ws,
-                                                           _stream(stream)),
+                                                           _stream(stream, dev)),
              "zero_multi_unscale_norm_overflow_dev")
 
 
@@ -172,17 +172,17 @@ def _hypers(hps):
     return (zero_adam_hyper * len(hps))(*[_hyper(h) for h in hps])
 
 
-def _coefs_ptr(d_coefs, n_groups: int) -> Optional[int]:
-    return _buf(d_coefs, None, n_groups * zero_adam_coef_bytes(), "d_coefs", _current_device())
+def _coefs_ptr(d_coefs, n_groups: int, dev: int) -> Optional[int]:
+    return _buf(d_coefs, None, n_groups * zero_adam_coef_bytes(), "d_coefs", dev)
 
 
 def zero_multi_norm_decide_dev(table: TensorTable, hps: Sequence[AdamHyper], state: StepState, sqnorm, overflow,
                                d_coefs, workspace, tensor_sqnorm=None, unscaled: bool = False, stream=None) -> None:
     """The norm pass of a single rank, whose last kernel also makes the step's
     decision: one coefficient block per set into d_coefs, the state advanced."""
-    tab, out, ws = _norm_args(table, sqnorm, overflow, tensor_sqnorm, workspace)
+    dev, tab, out, ws = _norm_args(table, sqnorm, overflow, tensor_sqnorm, workspace)
     _L.check(_L.lib().zero_multi_norm_decide_dev(*tab, 1 if unscaled else 0, _hypers(hps), len(hps), state.ptr(), *out,
-                                                 _coefs_ptr(d_coefs, len(hps)), *ws, _stream(stream)),
+                                                 _coefs_ptr(d_coefs, len(hps), dev), *ws, _stream(stream, dev)),
              "zero_multi_norm_decide_dev")
 
 
@@ -190,9 +190,10 @@ def zero_multi_decide_dev(hps: Sequence[AdamHyper], state: StepState, global_ove
                           unscaled: bool = False, stream=None) -> None:
     """The decision alone: d_coefs <- the blocks of step applied + 1, the state
     advanced by the flag."""
+    dev = _current_device()
     _L.check(_L.lib().zero_multi_decide_dev(_hypers(hps), len(hps), 1 if unscaled else 0, state.ptr(),
-                                            _buf(global_overflow, torch.int32, 4, "global_overflow", _current_device()),
-                                            _coefs_ptr(d_coefs, len(hps)), _stream(stream)), "zero_multi_decide_dev")
+                                            _buf(global_overflow, torch.int32, 4, "global_overflow", dev),
+                                            _coefs_ptr(d_coefs, len(hps), dev), _stream(stream, dev)), "zero_multi_decide_dev")
 
 
 def zero_multi_adam_step(table: TensorTable, hps: Sequence[AdamHyper], global_sqnorm=None, global_overflow=None,
@@ -205,7 +206,7 @@ def zero_multi_adam_step(table: TensorTable, hps: Sequence[AdamHyper], global_sq
     arr = (zero_adam_params * len(hps))(*[h.c() for h in hps])
     _L.check(_L.lib().zero_multi_adam_step(*table._ptrs(dev), arr, len(hps), _seed(seed),
                                            _buf(global_sqnorm, torch.float64, 8, "global_sqnorm", dev),
-                                           _buf(global_overflow, torch.int32, 4, "global_overflow", dev), _stream(stream)),
+                                           _buf(global_overflow, torch.int32, 4, "global_overflow", dev), _stream(stream, dev)),
              "zero_multi_adam_step")
 
 
@@ -215,8 +216,8 @@ def zero_multi_adam_step_coef(table: TensorTable, d_coefs, n_groups: int, global
     d_coefs and, for 8-bit moments, the step that keys the rounding from d_step
     (int64 [1])."""
     dev = _current_device()
-    _L.check(_L.lib().zero_multi_adam_step_coef(*table._ptrs(dev), _coefs_ptr(d_coefs, n_groups), n_groups, _seed(seed),
+    _L.check(_L.lib().zero_multi_adam_step_coef(*table._ptrs(dev), _coefs_ptr(d_coefs, n_groups, dev), n_groups, _seed(seed),
                                                 _buf(d_step, torch.int64, 8, "d_step", dev),
                                                 _buf(global_sqnorm, torch.float64, 8, "global_sqnorm", dev),
                                                 _buf(global_overflow, torch.int32, 4, "global_overflow", dev),
-                                                _stream(stream)), "zero_multi_adam_step_coef")
+                                                _stream(stream, dev)), "zero_multi_adam_step_coef")
