@@ -372,6 +372,20 @@ def test_binding_checks_list_calls():
         Z.zero_multi_adam_step(t, hps, FakeDev(1, F32), ov, stream=0)
 
 
+def test_gradients_of_another_length_or_order_in_the_same_place_are_refused():
+    """A view that begins where the described gradient does is not that gradient."""
+    m, a, b, g, p = fake_list([100, 7])
+    t = Z.TensorTable(m, a, b, g, p)
+    with pytest.raises(ValueError, match="elements"):
+        t.set_grads([FakeDev(50, g[0].dtype, g[0].data_ptr()), g[1]])
+    turned = FakeDev(100, g[0].dtype, g[0].data_ptr())
+    turned.is_contiguous = lambda: False
+    with pytest.raises(ValueError, match="contiguous"):
+        t.set_grads([turned, g[1]])
+    t.set_grads(g)
+    assert t.grads == g
+
+
 class Placed(FakeDev):
     """A stand-in that knows its device."""
 

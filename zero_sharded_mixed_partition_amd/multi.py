@@ -28,7 +28,7 @@ def _f32_bytes(n: int) -> int:
 
 
 def _where(grads):
-    return [(g.data_ptr(), g.dtype) for g in grads]
+    return [(g.data_ptr(), g.dtype, g.numel(), g.is_contiguous()) for g in grads]
 
 
 class TensorTable:
@@ -59,7 +59,7 @@ class TensorTable:
         self.n_groups = 1 + max(self.groups) if self.groups else 1
         self._kept = []                        # tables that recorded graphs read
         self._describe(grads)
-        self._build(grads)
+        self._build(grads, _where(grads))
 
     @classmethod
     def of_grads(cls, grads) -> "TensorTable":
@@ -73,9 +73,10 @@ class TensorTable:
         description (which the table then keeps alive): record it again."""
         if len(grads) != self.n_tensors:
             raise ValueError(f"{len(grads)} gradients for {self.n_tensors} tensors")
-        if _where(grads) != self._grad_key:
+        key = _where(grads)
+        if key != self._grad_key:
             old, captured = (self.host, self.device), self._captured
-            self._build(grads)
+            self._build(grads, key)
             if captured:
                 self._kept.append(old)
             elif old[1] is not None:
@@ -101,7 +102,7 @@ class TensorTable:
             if self.groups is not None:
                 t.group = int(self.groups[i])
 
-    def _build(self, grads) -> None:
+    def _build(self, grads, key) -> None:
         """The table for these gradients, the rest of the list being described."""
         arr, bits, index = self._c, self.state_bits, self._index
         for i, (g, n) in enumerate(zip(grads, self._numels)):
@@ -121,7 +122,7 @@ class TensorTable:
         _L.check(build(arr, self.n_tensors, bits, host.data_ptr(), size.value, ctypes.byref(size),
                        ctypes.byref(dev_size)), "zero_multi_table_build")
         self.grads, self.host = list(grads), host
-        self._grad_key = _where(grads)
+        self._grad_key = key
         self.device = host[:dev_size.value].to(torch.device("cuda", index), non_blocking=True) if on_gpu else None
         self._captured = False
         self._addresses = self.host.data_ptr(), None if self.device is None else self.device.data_ptr()
