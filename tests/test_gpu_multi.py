@@ -439,6 +439,28 @@ def test_another_stream(Z):
         assert torch.equal(a, b)
 
 
+def test_a_replaced_table_outlives_its_readers_on_another_stream(Z):
+    """The memory of the device copy that a stream still has to read is not
+    handed out again when the gradients move."""
+    x, y = (List(Z, SIZES, 62, bits=8, **MIXED) for _ in range(2))
+    moved = [g.clone() for g in x.G]
+    big, sq = torch.empty(1 << 28, device="cuda"), scalar(SQ, torch.float64)
+    torch.cuda.synchronize()
+    old, st = x.table.device.data_ptr(), torch.cuda.Stream()
+    with torch.cuda.stream(st):
+        for _ in range(100):                             # 17 ms or more of writes before the step's reads
+            big.zero_()
+        Z.zero_multi_adam_step(x.table, [Z.AdamHyper(**h) for h in HPS], sq, seed=11)
+    x.table.set_grads(moved)
+    again = [torch.empty_like(x.table.device) for _ in range(4)]
+    if not st.query():                                   # else there is nothing to show
+        assert old not in [t.data_ptr() for t in again]
+    torch.cuda.synchronize()
+    y.step(Z)
+    for a, b in zip(x.P + x.A, y.P + y.A):
+        assert torch.equal(a, b)
+
+
 def test_norm_matches_the_shard_pass(Z):
     """One tensor: the same exact squares as the shard's norm pass, against
     the oracle's exact sum."""

@@ -431,6 +431,37 @@ def test_tensors_on_another_device_are_refused(monkeypatch):
         Z.zero_multi_unscale_norm_overflow(t, 1.0, FakeDev(1, F64), FakeDev(1, I32), FakeDev(256, U8), stream=0)
 
 
+def test_the_device_copy_waits_for_every_stream_that_read_it(monkeypatch):
+    """A table used on a stream other than its own is given back to the
+    allocator with that stream recorded, once; a raw handle cannot be."""
+    class Stream:
+        def __init__(self, handle):
+            self.cuda_stream, self.device_index = handle, 0
+
+    class Device:
+        def __init__(self):
+            self.seen = []
+
+        def record_stream(self, s):
+            self.seen.append(s.cuda_stream)
+
+        def data_ptr(self):
+            return 1 << 45
+
+    m, a, b, g, p = fake_list([100, 7])
+    t = Z.TensorTable(m, a, b, g, p)
+    t._index, t.device, t._streams, t._captured = 0, Device(), {64}, True
+    for handle in (64, 128, 192, 128):
+        t._ptrs(0, Stream(handle))
+    t._ptrs(0, 256)
+    assert t.device.seen == [128, 192]
+    monkeypatch.setattr(Z, "_raw_stream", lambda device: 512)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: Stream(512))
+    t._ptrs(0, None)
+    t._ptrs(0, None)
+    assert t.device.seen == [128, 192, 512]
+
+
 def test_np_seed_range():
     """Any integer seeds the rounding: it is taken modulo 2^64."""
     from zero_sharded_mixed_partition_amd.moments8 import _seed

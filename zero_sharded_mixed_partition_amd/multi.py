@@ -33,9 +33,10 @@ def _where(grads):
 
 class TensorTable:
     """The list's table (zero_multi_table_build): a host part and its device
-    copy.  Holds references to the tensors.  groups: hyperparameter group per
-    tensor (default 0).  state_bits 8: exp_avgs and exp_avg_sqs are the
-    tensors' moments8 and scales8 (uint8)."""
+    copy.  Holds references to the tensors and describes their addresses: that
+    one is resized or given other storage afterwards is not seen.  groups:
+    hyperparameter group per tensor (default 0).  state_bits 8: exp_avgs and
+    exp_avg_sqs are the tensors' moments8 and scales8 (uint8)."""
 
     def __init__(self, masters, exp_avgs, exp_avg_sqs, grads, params_out=None, groups: Optional[Sequence[int]] = None,
                  state_bits: int = 32):
@@ -68,9 +69,11 @@ class TensorTable:
 
     def set_grads(self, grads) -> None:
         """Describe the list anew with other gradient tensors of the same lengths
-        (a no-op if they lie where the present ones do).  The new device copy is enqueued on the
-        current stream.  A graph recorded with the table keeps reading the old
-        description (which the table then keeps alive): record it again."""
+        (a no-op if they lie where the present ones do).  The new device copy is
+        enqueued on the current stream; the old one lives until every torch stream
+        that read it has passed (a raw stream handle is the caller's to wait for).
+        A graph recorded with the table keeps reading the old description (which
+        the table then keeps alive): record it again."""
         if len(grads) != self.n_tensors:
             raise ValueError(f"{len(grads)} gradients for {self.n_tensors} tensors")
         key = _where(grads)
@@ -79,8 +82,6 @@ class TensorTable:
             self._build(grads, key)
             if captured:
                 self._kept.append(old)
-            elif old[1] is not None:
-                old[1].record_stream(torch.cuda.current_stream())    # a step there may still read it
 
     def _describe(self, grads) -> None:
         """The C descriptions of the whole list."""
@@ -125,13 +126,23 @@ class TensorTable:
         self._grad_key = key
         self.device = host[:dev_size.value].to(torch.device("cuda", index), non_blocking=True) if on_gpu else None
         self._captured = False
+        # raw handles of the streams that have read the device copy; its own needs no record
+        self._streams = {_stream(None, index)} if on_gpu else set()
         self._addresses = self.host.data_ptr(), None if self.device is None else self.device.data_ptr()
 
-    def _ptrs(self, current: int):
-        if self._index >= 0 and self._index != current:
+    def _ptrs(self, current: int, stream):
+        if self._index < 0:
+            return self._addresses
+        if self._index != current:
             raise ValueError(f"the table's tensors are on cuda:{self._index}, the current device is cuda:{current}")
-        if self._index >= 0 and not self._captured:
+        if not self._captured:
             self._captured = torch.cuda.is_current_stream_capturing()
+        if not isinstance(stream, int):
+            raw = _stream(stream, current)
+            if raw not in self._streams:
+                # the allocator keeps the device copy until this stream has passed the calls that read it
+                self._streams.add(raw)
+                self.device.record_stream(torch.cuda.current_stream() if stream is None else stream)
         return self._addresses
 
 
@@ -139,9 +150,9 @@ def zero_multi_norm_workspace_bytes(table: TensorTable) -> int:
     return int(_L.lib().zero_multi_norm_workspace_bytes(table.host.data_ptr()))
 
 
-def _norm_args(table, sqnorm, overflow, tensor_sqnorm, workspace):
+def _norm_args(table, sqnorm, overflow, tensor_sqnorm, workspace, stream):
     dev = _current_device()
-    return (dev, table._ptrs(dev),
+    return (dev, table._ptrs(dev, stream),
             (_buf(sqnorm, torch.float64, 8, "sqnorm", dev), _buf(overflow, torch.int32, 4, "overflow", dev),
              _buf(tensor_sqnorm, torch.float64, 8 * table.n_tensors, "tensor_sqnorm", dev)),
             (_buf(workspace, None, 0, "workspace", dev), workspace.numel() * workspace.element_size()))
@@ -152,7 +163,7 @@ def zero_multi_unscale_norm_overflow(table: TensorTable, inv_loss_scale: float, 
     """Enqueue the norm pass over the list's gradients: sqnorm (float64 [1]),
     overflow (int32 [1]) and, if given, each tensor's own sum of squares
     (tensor_sqnorm, float64 [n_tensors])."""
-    dev, tab, out, ws = _norm_args(table, sqnorm, overflow, tensor_sqnorm, workspace)
+    dev, tab, out, ws = _norm_args(table, sqnorm, overflow, tensor_sqnorm, workspace, stream)
     _L.check(_L.lib().zero_multi_unscale_norm_overflow(*tab, float(inv_loss_scale), *out, *ws, _stream(stream, dev)),
              "zero_multi_unscale_norm_overflow")
 
@@ -161,7 +172,7 @@ def zero_multi_unscale_norm_overflow_dev(table: TensorTable, state: StepState, s
                                          tensor_sqnorm=None, unscaled: bool = False, stream=None) -> None:
     """The norm pass with the loss scale from the device state; unscaled: the
     gradients are already unscaled."""
-    dev, tab, out, ws = _norm_args(table, sqnorm, overflow, tensor_sqnorm, workspace)
+    dev, tab, out, ws = _norm_args(table, sqnorm, overflow, tensor_sqnorm, workspace, stream)
     _L.check(_L.lib().zero_multi_unscale_norm_overflow_dev(*tab, 1 if unscaled else 0, state.ptr(), *out, *ws,
                                                            _stream(stream, dev)),
              "zero_multi_unscale_norm_overflow_dev")
@@ -181,7 +192,7 @@ def zero_multi_norm_decide_dev(table: TensorTable, hps: Sequence[AdamHyper], sta
                                d_coefs, workspace, tensor_sqnorm=None, unscaled: bool = False, stream=None) -> None:
     """The norm pass of a single rank, whose last kernel also makes the step's
     decision: one coefficient block per set into d_coefs, the state advanced."""
-    dev, tab, out, ws = _norm_args(table, sqnorm, overflow, tensor_sqnorm, workspace)
+    dev, tab, out, ws = _norm_args(table, sqnorm, overflow, tensor_sqnorm, workspace, stream)
     _L.check(_L.lib().zero_multi_norm_decide_dev(*tab, 1 if unscaled else 0, _hypers(hps), len(hps), state.ptr(), *out,
                                                  _coefs_ptr(d_coefs, len(hps), dev), *ws, _stream(stream, dev)),
              "zero_multi_norm_decide_dev")
@@ -205,7 +216,7 @@ def zero_multi_adam_step(table: TensorTable, hps: Sequence[AdamHyper], global_sq
         raise ValueError(f"1 to {MAX_GROUPS} hyperparameter sets expected, got {len(hps)}")
     dev = _current_device()
     arr = (zero_adam_params * len(hps))(*[h.c() for h in hps])
-    _L.check(_L.lib().zero_multi_adam_step(*table._ptrs(dev), arr, len(hps), _seed(seed),
+    _L.check(_L.lib().zero_multi_adam_step(*table._ptrs(dev, stream), arr, len(hps), _seed(seed),
                                            _buf(global_sqnorm, torch.float64, 8, "global_sqnorm", dev),
                                            _buf(global_overflow, torch.int32, 4, "global_overflow", dev), _stream(stream, dev)),
              "zero_multi_adam_step")
@@ -217,7 +228,7 @@ def zero_multi_adam_step_coef(table: TensorTable, d_coefs, n_groups: int, global
     d_coefs and, for 8-bit moments, the step that keys the rounding from d_step
     (int64 [1])."""
     dev = _current_device()
-    _L.check(_L.lib().zero_multi_adam_step_coef(*table._ptrs(dev), _coefs_ptr(d_coefs, n_groups, dev), n_groups, _seed(seed),
+    _L.check(_L.lib().zero_multi_adam_step_coef(*table._ptrs(dev, stream), _coefs_ptr(d_coefs, n_groups, dev), n_groups, _seed(seed),
                                                 _buf(d_step, torch.int64, 8, "d_step", dev),
                                                 _buf(global_sqnorm, torch.float64, 8, "global_sqnorm", dev),
                                                 _buf(global_overflow, torch.int32, 4, "global_overflow", dev),
