@@ -264,6 +264,39 @@ def test_multi_resumes_bit_for_bit(Z, tmp_path, bits):
 
 
 @pytest.mark.parametrize("bits", [32, 8])
+def test_parameters_of_several_dimensions(Z, tmp_path, bits):
+    """Matrices, a scalar and an empty one: built from moments of their shapes,
+    stepped as their flat forms are, saved and loaded."""
+    from zero_sharded_mixed_partition_amd import checkpoint
+    shapes = [(33, 7), (), (0, 4), (3, 5, 16), (1000,)]
+    rng = np.random.default_rng(9)
+    cols = [[torch.from_numpy(np.asarray(rng.uniform(1e-3, 1e-2, s), np.float32)).cuda() for s in shapes] for _ in range(3)]
+    G = [torch.from_numpy(np.asarray(rng.normal(0, 1e-2, s), np.float32)).cuda() for s in shapes]
+    opts = []
+    for flat in (False, True, False):
+        masters, m, v = ([(x.reshape(-1) if flat else x).clone() for x in col] for col in cols)
+        opts.append(Z.MultiAdam(masters, [g.reshape(-1) if flat else g for g in G], hyper=[HYPER], moments=(m, v),
+                                state_bits=bits))
+    flat_arrays = lambda o: [x.reshape(-1) for x in arrays(o)]  # noqa: E731
+    a, b, c = opts
+    for o in (a, b):
+        o.step()
+    assert same(flat_arrays(a), flat_arrays(b))
+    assert [tuple(x.shape) for x in a.masters] == shapes
+    checkpoint.save(a, str(tmp_path))
+    checkpoint.load(c, str(tmp_path))
+    assert same(flat_arrays(a), flat_arrays(c))
+    flat = checkpoint.state_dict(b)
+    checkpoint.load_state_dict(c, flat)
+    for o in (a, c):
+        o.step()
+    assert same(flat_arrays(a), flat_arrays(c))
+    flat["hyper"] = flat["hyper"] * 2
+    with pytest.raises(ValueError, match="groups"):
+        checkpoint.load_state_dict(c, flat)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
 def test_fragments_of_a_shard(Z, bits):
     """One rank's shard as a list of fragments that start anywhere.  With one
     group and no clipping its master, copy and (32 bits) moments equal the

@@ -499,3 +499,32 @@ def test_table_phases_and_units():
         assert (f[12], h[8], h[7]) == want, (off, n, bits, f[12], h[8], h[7])
 
 
+
+
+def test_checkpoint_of_parameters_of_several_dimensions(monkeypatch, tmp_path):
+    """Arrays load into tensors of the shape they were saved with or of its flat
+    form, and nothing is written when one does not fit or the groups differ."""
+    from types import SimpleNamespace
+    from zero_sharded_mixed_partition_amd import checkpoint
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: SimpleNamespace(synchronize=lambda: None))
+
+    def opt(*shapes, groups=1):
+        cols = [torch.full(s, 1.0 + i) for i, s in enumerate(shapes)]
+        return SimpleNamespace(state=None, t=0, scaler=Z.LossScaler(), hyper=[dict(lr=0.1)] * groups, seed=3, cols=cols,
+                               checkpoint_arrays=lambda: {f"master_{i}": x for i, x in enumerate(cols)})
+
+    shapes = [(3, 5), (), (0, 4), (7,)]
+    a, b, flat = opt(*shapes), opt(*shapes), opt((15,), (1,), (0,), (7,))
+    for x in a.cols:
+        x.mul_(10)
+    checkpoint.save(a, str(tmp_path))
+    checkpoint.load(b, str(tmp_path))
+    assert all(torch.equal(x, y) for x, y in zip(a.cols, b.cols))
+    c = opt(*shapes)
+    checkpoint.load_state_dict(c, checkpoint.state_dict(flat))
+    assert all(torch.equal(x.reshape(-1), y) for x, y in zip(c.cols, flat.cols))
+    for other, what in ((opt((5, 3), (), (0, 4), (7,)), "master_0"), (opt(*shapes, groups=2), "groups")):
+        before = [x.clone() for x in other.cols]
+        with pytest.raises(ValueError, match=what):
+            checkpoint.load(other, str(tmp_path))
+        assert all(torch.equal(x, y) for x, y in zip(before, other.cols))

@@ -5,8 +5,9 @@ exp_avg and exp_avg_sq partitions plus the step scalars (applied steps, loss
 scaler).  save() writes them as one .npy file each and one JSON file in a
 directory; load() restores them into a ShardAdam built over the same shard
 size.  ShardAdam8 saves its 8-bit moments as they are (codes and scales), and
-the seed of their rounding; MultiAdam saves its tensors in list order.  Because every step is deterministic, k steps, save, load and k more
-steps give the same bits as 2k uninterrupted steps.
+the seed of their rounding; MultiAdam saves its tensors in list order.  Because
+every step is deterministic, k steps, save, load and k more steps give the same
+bits as 2k uninterrupted steps.
 """
 import copy
 import json
@@ -41,11 +42,13 @@ def load_state_dict(opt, d: dict) -> None:
     for k, dst in arrays.items():
         if k not in d:
             raise ValueError(f"{k}: not in the checkpoint")
-        src, want = np.ascontiguousarray(d[k]), str(dst.dtype).replace("torch.", "")
-        if src.dtype.name != want or src.shape != (dst.numel(),):
-            raise ValueError(f"{k}: expected {want}[{dst.numel()}], got {src.dtype}{list(src.shape)}")
+        src, want = np.asarray(d[k]), str(dst.dtype).replace("torch.", "")
+        if src.dtype.name != want or src.shape not in ((dst.numel(),), tuple(dst.shape)):
+            raise ValueError(f"{k}: expected {want}{list(dst.shape)}, got {src.dtype}{list(src.shape)}")
+    if isinstance(opt.hyper, list) and len(d["hyper"]) != len(opt.hyper):
+        raise ValueError(f"{len(d['hyper'])} groups in the checkpoint, {len(opt.hyper)} expected")
     for k, dst in arrays.items():
-        dst.copy_(torch.from_numpy(np.ascontiguousarray(d[k])))
+        dst.copy_(torch.from_numpy(np.ascontiguousarray(d[k])).view(dst.shape))
     opt.t = int(d["t"])
     opt.scaler = LossScaler(**d["scaler"])
     opt.hyper = copy.deepcopy(d["hyper"])

@@ -75,8 +75,8 @@ class MultiAdam:
                 if state_bits == 8:
                     zero_moments8_pack(a[i], b[i], m, v)
                 else:
-                    a[i].copy_(m)
-                    b[i].copy_(v)
+                    a[i].copy_(m.reshape(-1))
+                    b[i].copy_(v.reshape(-1))
         self.table = TensorTable(masters, a, b, grads, params_out, groups=groups, state_bits=state_bits)
         self.masters, self.exp_avgs, self.exp_avg_sqs = list(masters), a, b
         self.scaler = scaler if scaler is not None else LossScaler.static(1.0)
