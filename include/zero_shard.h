@@ -662,7 +662,8 @@ int zero_moments8_unpack(float* exp_avg, float* exp_avg_sq, const void* moments8
  *   empty tensor).  The sums are taken in float64 in a fixed order that
  *   depends only on the sizes.
  *   Workspace: zero_multi_norm_workspace_bytes(table) bytes (0 if table is
- *   not a table).
+ *   not a table), clobbered.  Calls, and graphs recorded with them, that may
+ *   run at the same time need a workspace and outputs each.
  * zero_multi_adam_step: as zero_shard_adam_step (state_bits 32) or
  *   zero_shard_adam8_step (state_bits 8) on every tensor, with hp[group] of
  *   n_groups hyperparameter sets; the random bits of tensor i are those of
