@@ -1,0 +1,50 @@
+"""GPU: what a list's table keeps alive, and what its device copy waits for."""
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+SIZES = [700, 5, 8192, 20_001]
+HYPER = dict(lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.1)
+
+
+@pytest.fixture(scope="module")
+def Z():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import zero_sharded_mixed_partition_amd as Z
+    Z._L.lib()
+    return Z
+
+
+def normal(seed, scale, dtype=torch.float32):
+    gen = torch.Generator().manual_seed(seed)
+    return [(torch.randn(n, generator=gen) * scale).to(dtype).cuda() for n in SIZES]
+
+
+def same(a, b):
+    return all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_replay_reads_the_gradients_it_was_recorded_with(Z, bits):
+    """They are described no longer and the caller has dropped them: the memory
+    is not handed out again, and a replay steps with their values."""
+    opts = [Z.MultiAdam(normal(1, 0.02), normal(2, 1e-2, torch.bfloat16), hyper=[HYPER], state_bits=bits,
+                        device_state=True) for _ in range(2)]
+    rec, eager = opts
+    eager.step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        rec.step()
+    taken = {g.data_ptr() for g in rec.table.grads}
+    rec.table.set_grads([torch.zeros_like(g) for g in rec.table.grads])
+    fill = [torch.full((n,), float("nan"), dtype=torch.bfloat16, device="cuda") for n in SIZES * 8]
+    assert not taken & {x.data_ptr() for x in fill}
+    for k in range(3):
+        if k:
+            eager.step()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert same(rec.masters, eager.masters) and same(rec.exp_avgs, eager.exp_avgs)

@@ -58,7 +58,7 @@ class TensorTable:
         self.masters, self.exp_avgs, self.exp_avg_sqs = own(masters), own(exp_avgs), own(exp_avg_sqs)
         self.params_out, self.groups = own(params_out), own(groups)
         self.n_groups = 1 + max(self.groups) if self.groups else 1
-        self._kept = []                        # tables that recorded graphs read
+        self._kept = []                        # tables that recorded graphs read, and their gradients
         self._describe(grads)
         self._build(grads, _where(grads))
 
@@ -72,13 +72,13 @@ class TensorTable:
         (a no-op if they lie where the present ones do).  The new device copy is
         enqueued on the current stream; the old one lives until every torch stream
         that read it has passed (a raw stream handle is the caller's to wait for).
-        A graph recorded with the table keeps reading the old description (which
-        the table then keeps alive): record it again."""
+        A graph recorded with the table keeps reading the old gradients (which the
+        table then keeps alive, with their description): record it again."""
         if len(grads) != self.n_tensors:
             raise ValueError(f"{len(grads)} gradients for {self.n_tensors} tensors")
         key = _where(grads)
         if key != self._grad_key:
-            old, captured = (self.host, self.device), self._captured
+            old, captured = (self.host, self.device, self.grads), self._captured
             self._build(grads, key)
             if captured:
                 self._kept.append(old)
