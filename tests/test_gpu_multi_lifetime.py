@@ -48,3 +48,26 @@ def test_a_replay_reads_the_gradients_it_was_recorded_with(Z, bits):
         graph.replay()
         torch.cuda.synchronize()
         assert same(rec.masters, eager.masters) and same(rec.exp_avgs, eager.exp_avgs)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_stream_waits_for_a_table_built_on_another(Z, bits):
+    """The table is built on a stream that still has work to do, and used on
+    others that nobody made wait."""
+    state = {32: lambda: [torch.zeros(n, device="cuda") for n in SIZES],
+             8: lambda: [torch.zeros(2 * n + 8, dtype=torch.uint8, device="cuda") for n in SIZES]}[bits]
+    grads = normal(2, 1e-2, torch.bfloat16)
+    hp = [Z.AdamHyper(**HYPER, step=1)]
+    want = normal(1, 0.02)
+    Z.zero_multi_adam_step(Z.TensorTable(want, state(), state(), grads, state_bits=bits), hp)
+    got, other = [(normal(1, 0.02), state(), state()) for _ in range(2)]
+    torch.cuda.synchronize()
+    build, first, second = (torch.cuda.Stream() for _ in range(3))
+    with torch.cuda.stream(build):
+        torch.cuda._sleep(20_000_000)                      # some milliseconds
+        tables = [Z.TensorTable(*x, grads, state_bits=bits) for x in (got, other)]
+    with torch.cuda.stream(first):
+        Z.zero_multi_adam_step(tables[0], hp)
+    Z.zero_multi_adam_step(tables[1], hp, stream=second)
+    torch.cuda.synchronize()
+    assert same(got[0], want) and same(other[0], want)

@@ -35,3 +35,47 @@ def test_a_recorded_table_keeps_its_gradients():
     assert all(r() is not None for r in recorded)
     assert all(r() is None for r in later)                 # described after the recording, read by no graph
     assert t.grads == g
+
+
+def test_other_streams_wait_for_the_tables_copy(monkeypatch):
+    """The device copy is enqueued on the stream that was current when the table
+    was built: any other one waits for it, once, before its first call reads it.
+    A stream that records a graph cannot wait for work outside of it (the graph
+    is recorded after a synchronization); its later, eager calls wait."""
+    class Stream:
+        device_index = 0
+
+        def __init__(self, handle):
+            self.cuda_stream, self.waited = handle, []
+
+        def wait_event(self, e):
+            self.waited.append(e)
+
+    class Device:
+        def record_stream(self, s):
+            pass
+
+        def data_ptr(self):
+            return 1 << 45
+
+    t = Z.TensorTable(*fake_list([100, 7]))
+    copied = object()
+    t._index, t.device, t._streams, t._ready = 0, Device(), {64}, copied
+    recording = [False]
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: recording[0])
+    own, other, third = Stream(64), Stream(128), Stream(192)
+    for s in (own, other, other):
+        t._ptrs(0, s)
+    assert own.waited == [] and other.waited == [copied]
+    current = Stream(256)
+    monkeypatch.setattr(Z, "_raw_stream", lambda device: 256)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: current)
+    t._ptrs(0, None)
+    t._ptrs(0, None)
+    assert current.waited == [copied]
+    recording[0] = True
+    t._ptrs(0, third)
+    assert third.waited == [] and t._captured
+    recording[0] = False
+    t._ptrs(0, third)
+    assert third.waited == [copied]

@@ -70,8 +70,10 @@ class TensorTable:
     def set_grads(self, grads) -> None:
         """Describe the list anew with other gradient tensors of the same lengths
         (a no-op if they lie where the present ones do).  The new device copy is
-        enqueued on the current stream; the old one lives until every torch stream
-        that read it has passed (a raw stream handle is the caller's to wait for).
+        enqueued on the current stream, and torch streams that use the table wait
+        for it; the old one lives until every torch stream that read it has passed
+        (a raw stream handle is the caller's to wait for, and so is the copy if a
+        graph is recorded on another stream: torch.cuda.graph synchronizes first).
         A graph recorded with the table keeps reading the old gradients (which the
         table then keeps alive, with their description): record it again."""
         if len(grads) != self.n_tensors:
@@ -126,8 +128,12 @@ class TensorTable:
         self._grad_key = key
         self.device = host[:dev_size.value].to(torch.device("cuda", index), non_blocking=True) if on_gpu else None
         self._captured = False
-        # raw handles of the streams that have read the device copy; its own needs no record
+        # raw handles of the streams that have read the device copy; its own needs no wait and no record
         self._streams = {_stream(None, index)} if on_gpu else set()
+        self._ready = None
+        if on_gpu:
+            self._ready = torch.cuda.Event()
+            self._ready.record(torch.cuda.current_stream(index))
         self._addresses = self.host.data_ptr(), None if self.device is None else self.device.data_ptr()
 
     def _ptrs(self, current: int, stream):
@@ -140,9 +146,15 @@ class TensorTable:
         if not isinstance(stream, int):
             raw = _stream(stream, current)
             if raw not in self._streams:
-                # the allocator keeps the device copy until this stream has passed the calls that read it
-                self._streams.add(raw)
-                self.device.record_stream(torch.cuda.current_stream() if stream is None else stream)
+                # the stream waits for the device copy, and the allocator keeps it
+                # until the stream has passed the calls that read it
+                used = torch.cuda.current_stream() if stream is None else stream
+                self.device.record_stream(used)
+                recording = self._ready is not None and torch.cuda.is_current_stream_capturing()
+                if not recording:                     # a recording stream can wait for nothing outside its graph
+                    self._streams.add(raw)
+                    if self._ready is not None:
+                        used.wait_event(self._ready)
         return self._addresses
 
 
