@@ -40,16 +40,17 @@ class MultiAdam:
                  params_out: Optional[Sequence[Optional[torch.Tensor]]] = None, *, hyper: Sequence[dict] = ({},),
                  groups: Optional[Sequence[int]] = None, max_grad_norm=0.0, state_bits: int = 32, moments=None,
                  scaler: Optional[LossScaler] = None, applied_steps: int = 0, device_state: bool = False,
-                 tensor_norms: bool = False, seed: int = 0):
+                 tensor_norms: bool = False, seed: int = 0, device=None):
         """masters: fp32 tensors; grads: fp16, bf16 or fp32; params_out: the 16-bit
         copies (None entries: no copy).  hyper: one dict per group (lr, beta1,
         beta2, eps, weight_decay); groups: each tensor's group.  moments:
         (exp_avgs, exp_avg_sqs) fp32 lists to go on from, else zeros; with
         state_bits 8 they are rounded into the 8-bit format.  tensor_norms: the
         norm pass also fills self.tensor_sqnorm.  seed keys the rounding of 8-bit
-        moments."""
-        if not len(grads):
-            raise ValueError("an empty list")
+        moments.  device: where an empty list keeps its scalars (its steps update
+        nothing, but exchange and decide)."""
+        if not len(grads) and device is None:
+            raise ValueError("an empty list needs a device")
         if state_bits not in (8, 32):
             raise ValueError(f"state_bits must be 32 or 8, got {state_bits}")
         if not 1 <= len(hyper) <= MAX_GROUPS:
@@ -60,7 +61,7 @@ class MultiAdam:
         self.hyper = [dict(_HYPER, **h, max_grad_norm=max_grad_norm) for h in hyper]
         if groups is not None and any(not 0 <= g < len(self.hyper) for g in groups):
             raise ValueError(f"groups must lie in [0, {len(self.hyper)})")
-        dev, sizes = grads[0].device, [g.numel() for g in grads]
+        dev, sizes = grads[0].device if len(grads) else torch.device(device), [g.numel() for g in grads]
         if state_bits == 8:
             a = _slices(dev, torch.uint8, [_codes_bytes(n) for n in sizes])
             b = _slices(dev, torch.uint8, [_scales_bytes(n) for n in sizes])
@@ -99,9 +100,11 @@ class MultiAdam:
         """The fragments of a rank's shard (zero_rank_fragments) as a list:
         views of the shard's flat buffers.  groups: the group of each of the
         model's tensors; moments: the shard's flat fp32 moments to go on from.
-        The shard's padding is not touched."""
+        The shard's padding is not touched; a rank that holds nothing else has an
+        empty list, with which it takes part in the exchange and the decision."""
         def cut(flat):
             return [flat[b:b + n] for _, _, b, n in fragments]
+        kw.setdefault("device", master.device)
         return cls(cut(master), cut(grad), None if param_out is None else cut(param_out),
                    groups=[groups[t] for t, _, _, _ in fragments],
                    moments=None if moments is None else tuple(cut(m) for m in moments), **kw)
