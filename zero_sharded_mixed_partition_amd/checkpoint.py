@@ -5,7 +5,8 @@ exp_avg and exp_avg_sq partitions plus the step scalars (applied steps, loss
 scaler).  save() writes them as one .npy file each and one JSON file in a
 directory; load() restores them into a ShardAdam built over the same shard
 size.  ShardAdam8 saves its 8-bit moments as they are (codes and scales), and
-the seed of their rounding; MultiAdam saves its tensors in list order.  Because
+the seed of their rounding; MultiAdam saves its tensors in list order, and the
+group of each: a list of other tensors or with other groups is refused.  Because
 every step is deterministic, k steps, save, load and k more steps give the same
 bits as 2k uninterrupted steps.
 """
@@ -32,6 +33,8 @@ def state_dict(opt) -> dict:
     d["hyper"] = copy.deepcopy(opt.hyper)
     if hasattr(opt, "seed"):
         d["seed"] = opt.seed                           # keys the rounding of 8-bit moments
+    if hasattr(opt, "groups"):
+        d["groups"] = list(opt.groups)                 # one per tensor of a list
     return d
 
 
@@ -47,6 +50,10 @@ def load_state_dict(opt, d: dict) -> None:
             raise ValueError(f"{k}: expected {want}{list(dst.shape)}, got {src.dtype}{list(src.shape)}")
     if isinstance(opt.hyper, list) and len(d["hyper"]) != len(opt.hyper):
         raise ValueError(f"{len(d['hyper'])} groups in the checkpoint, {len(opt.hyper)} expected")
+    have, want = d.get("groups"), list(getattr(opt, "groups", ()))
+    if have is not None and list(have) != want:
+        raise ValueError(f"{len(have)} tensors in the checkpoint, {len(want)} expected" if len(have) != len(want) else
+                         "the checkpoint's tensors belong to other groups")
     for k, dst in arrays.items():
         dst.copy_(torch.from_numpy(np.ascontiguousarray(d[k])).view(dst.shape))
     opt.t = int(d["t"])
@@ -72,7 +79,7 @@ def save(opt, directory: str) -> None:
     d = state_dict(opt)
     for k in opt.checkpoint_arrays():
         np.save(os.path.join(directory, f"{k}.npy"), d[k])
-    meta = {k: d[k] for k in ("t", "skipped", "scaler", "hyper", "seed") if k in d}
+    meta = {k: d[k] for k in ("t", "skipped", "scaler", "hyper", "seed", "groups") if k in d}
     with open(os.path.join(directory, "scalars.json"), "w") as f:
         json.dump(meta, f, indent=1)
 

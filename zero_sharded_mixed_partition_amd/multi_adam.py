@@ -61,6 +61,7 @@ class MultiAdam:
         self.hyper = [dict(_HYPER, **h, max_grad_norm=max_grad_norm) for h in hyper]
         if groups is not None and any(not 0 <= g < len(self.hyper) for g in groups):
             raise ValueError(f"groups must lie in [0, {len(self.hyper)})")
+        self.groups = [0] * len(grads) if groups is None else [int(g) for g in groups]
         dev, sizes = grads[0].device if len(grads) else torch.device(device), [g.numel() for g in grads]
         if state_bits == 8:
             a = _slices(dev, torch.uint8, [_codes_bytes(n) for n in sizes])
@@ -78,7 +79,7 @@ class MultiAdam:
                 else:
                     a[i].copy_(m.reshape(-1))
                     b[i].copy_(v.reshape(-1))
-        self.table = TensorTable(masters, a, b, grads, params_out, groups=groups, state_bits=state_bits)
+        self.table = TensorTable(masters, a, b, grads, params_out, groups=self.groups, state_bits=state_bits)
         self.masters, self.exp_avgs, self.exp_avg_sqs = list(masters), a, b
         self.scaler = scaler if scaler is not None else LossScaler.static(1.0)
         self.t, self.seed = applied_steps, int(seed)
