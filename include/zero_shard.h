@@ -569,7 +569,9 @@ int zero_shard_grad_sum_norm_dev(float* acc, const void* const* slices, int32_t 
  * times 2^k, one k per block and moment:
  *     k = max(floor(log2(largest magnitude of the block)) - 7, -126)
  * (-126 for a block of zeros).  Positive s below 2^(k-9) is taken as 2^(k-9),
- * the smallest code.
+ * the smallest code.  Where k is 120 (exp_avg) or 56 (s), a finite value whose
+ * magnitude is above 240 * 2^k is taken as 240 * 2^k: the next code would stand
+ * for 2^128, or for a root whose square is 2^128.
  *  moments8  device, zero_moments8_bytes(n) = 8 ceil(n/4) bytes: for each four
  *            consecutive elements, four codes of exp_avg then four of s (zero
  *            codes where there is no element)

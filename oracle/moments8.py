@@ -52,11 +52,15 @@ def exponent_bytes(x: np.ndarray) -> np.ndarray:
 def encode(x: np.ndarray, scale_byte: np.ndarray, words=None, root: bool = False) -> np.ndarray:
     """Code of each x given its block's exponent byte (per element).  words: 32
     random bits per element (stochastic); None: to nearest even.  root: a
-    positive x is at least the smallest code."""
+    positive x is at least the smallest code.  In the blocks of float32's last
+    binade (2^120, roots: 2^56) no code is above 240: 256 * 2^120 and the square
+    of 256 * 2^56 are not float32 numbers."""
     y = np.asarray(x, np.float64) * np.ldexp(1.0, 127 - scale_byte.astype(np.int64))
     mag = np.abs(y)
     if root:
         mag = np.where((mag > 0) & (mag < 2.0 ** -9), 2.0 ** -9, mag)
+    last = np.asarray(scale_byte) == 127 + (56 if root else 120)
+    mag = np.where(last & (mag < 256), np.minimum(mag, 240.0), mag)
     _, e = np.frexp(mag)
     q = np.ldexp(1.0, np.maximum(e - 1, -6) - 3)           # spacing of the codes at this magnitude
     steps = mag / q

@@ -87,7 +87,8 @@ __global__ __launch_bounds__(kTaskThreads) void pack8(u32x2* __restrict__ C, uin
         const float smallest = __builtin_ldexpf(scale_of(sb), -9);
         for (int j = 0; j < 4; ++j) s[j] = floor_root(s[j], smallest);
         if (e0 < n) {
-            const u32x2 codes = {encode4_nearest(m, scale_of(mb)), encode4_nearest(s, scale_of(sb))};
+            u32x2 codes = {encode4_nearest(m, scale_of(mb)), encode4_nearest(s, scale_of(sb))};
+            hold_to_float32(codes, mb, sb);
             st_stream(codes, C + (e0 >> 2));
             if ((threadIdx.x & 7) == 0) S[e0 >> 5] = (uint16_t)(mb | (sb << 8));
         }

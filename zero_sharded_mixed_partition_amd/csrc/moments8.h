@@ -5,13 +5,15 @@
 // exp_avg_sq (s) are each stored as an OCP e4m3 code times a power of two per
 // block, value = code * 2^k, with k = floor(log2(largest magnitude of the
 // block)) - 7: the largest value lands in [128, 256), below e4m3's 448, so
-// rounding up never overflows, and the smallest code stands for 2^-16 to
-// 2^-17 of it.  Power-of-two scales make decoding exact, and gfx950 converts
-// two values with their scale in one instruction.  s instead of its square:
-// the update needs s itself, and the format's range of 2^17 below the block's
-// maximum then covers 2^34 of the second moment.  A positive s is stored as
-// at least the smallest code, so that m / (s + eps) cannot grow without bound
-// once s has become small beside its block.
+// rounding up never leaves the codes, and the smallest code stands for 2^-16 to
+// 2^-17 of it.  Only at float32's upper end would code 256 leave float32 (256 *
+// 2^120, or the square of 256 * 2^56): there codes end at 240.  Power-of-two
+// scales make decoding exact, and gfx950 converts two values with their scale
+// in one instruction.  s instead of its square: the update needs s itself, and
+// the format's range of 2^17 below the block's maximum then covers 2^34 of the
+// second moment.  A positive s is stored as at least the smallest code, so that
+// m / (s + eps) cannot grow without bound once s has become small beside its
+// block.
 //
 // Rounding in the step is stochastic.  With beta2 = 0.999 the second moment
 // moves by about 0.1% a step and e4m3 codes are 6-12% apart, so rounding to
@@ -199,6 +201,23 @@ __device__ __forceinline__ uint32_t encode4_nearest(const float x[4], float scal
     return __builtin_bit_cast(uint32_t, w);
 }
 
+// Codes of a block whose largest magnitude lies in float32's last binade, or
+// whose largest root lies in the last one whose squares are float32 numbers.
+constexpr uint32_t kLastMean = 127 + 120, kLastRoot = 127 + 56;
+
+// There code 256 (0x78) would stand for 2^128, or for a root whose square is
+// 2^128: values that round to it take the code below, 240 (0x77).  NaN stays.
+__device__ __forceinline__ uint32_t below_256(uint32_t codes) {
+    const uint32_t top = codes & (codes >> 1) & (codes >> 2) & (codes >> 3) & ~(codes << 3) & 0x08080808u;
+    return codes - (top >> 3);
+}
+
+__device__ __forceinline__ void hold_to_float32(u32x2& codes, uint32_t m_byte, uint32_t s_byte) {
+    if (!__any(m_byte == kLastMean || s_byte == kLastRoot)) return;
+    if (m_byte == kLastMean) codes[0] = below_256(codes[0]);
+    if (s_byte == kLastRoot) codes[1] = below_256(codes[1]);
+}
+
 // ---------------------------------------------------------------- one task of the step
 
 // Root and quotient, correctly rounded as sqrtf and / give them, without their
@@ -297,7 +316,8 @@ __device__ __forceinline__ void adam8_four(const StepCoef& c, bool usual, float 
     // below the sign bit the order of the bits is the order of the values; a NaN is above them all
     usual = usual && in_powers<-50, 40>(min_of4(mb[0], mb[1], mb[2], mb[3])) && in_powers<-50, 40>(m_top) &&
             in_powers<-96, 64>(min_of4(v0, v1, v2, v3)) && in_powers<-96, 64>(max_of4(v0, v1, v2, v3));
-    if (__all(usual)) {
+    usual = __all(usual);
+    if (usual) {
         for (int j = 0; j < 4; ++j) {
             s[j] = root_normal(v[j]);
             p[j] = fmaf(p[j], c.decay, quotient_normal(-(c.step_size * m[j]), fmaf(s[j], c.rsqrt_bc2, c.eps)));
@@ -314,6 +334,7 @@ __device__ __forceinline__ void adam8_four(const StepCoef& c, bool usual, float 
     for (int j = 0; j < 4; ++j) s[j] = floor_root(s[j], smallest);
     codes[0] = encode4_random(m, scale_of(m_byte), r);
     codes[1] = encode4_random(s, scale_of(s_byte), q);
+    if (!usual) hold_to_float32(codes, m_byte, s_byte);   // the usual range ends below
     scales = m_byte | (s_byte << 8);
 }
 
