@@ -222,21 +222,29 @@ __device__ __forceinline__ void hold_to_float32(u32x2& codes, uint32_t m_byte, u
 
 // Root and quotient, correctly rounded as sqrtf and / give them, without their
 // scaling and special cases.  root_normal: for every v in [2^-96, FLT_MAX] (all
-// 1.9e9 of them compared).  quotient_normal: where no step under- or overflows.
-// There y is the correctly rounded reciprocal (all 2^23 mantissas compared), so
-// a * y is off by at most 1.5 units in the last place, the residual is exact,
-// and the last step can only misround a quotient that lies within 3 / (2D)
-// units of the middle between two floats, D being d's mantissa as an integer;
-// all quotients within 64 / (2D) units of one (3.7e8) were compared.
+// 1.9e9 of them compared).  quotient_normal: where no step under- or overflows;
+// Newton's step for the reciprocal and Markstein's correction of the quotient
+// by its residual.  y is the correctly rounded reciprocal (all 2^23 mantissas
+// compared), so a * y is off by at most 1.5 units in the last place.  The
+// residual is an integer of up to 1.5 * 2^24 of its smallest units; beyond 2^24
+// it may be rounded, by one.  Before its rounding the last step is then off by
+// at most 3 / (2D) units for y's error and 2.01 / (2D) for the residual's, D
+// being d's mantissa as an integer, and it can misround only a quotient that
+// lies this close to the middle between two floats: all those within 64 / (2D)
+// units of one (3.7e8) were compared.
 __device__ __forceinline__ float root_normal(float v) {
     const float y = __builtin_amdgcn_rsqf(v);
     const float s = v * y;
     return fmaf(fmaf(-s, s, v), 0.5f * y, s);
 }
 
+__device__ __forceinline__ float reciprocal_normal(float d) {
+    const float y = __builtin_amdgcn_rcpf(d);
+    return fmaf(fmaf(-d, y, 1.0f), y, y);
+}
+
 __device__ __forceinline__ float quotient_normal(float a, float d) {
-    float y = __builtin_amdgcn_rcpf(d);
-    y = fmaf(fmaf(-d, y, 1.0f), y, y);
+    const float y = reciprocal_normal(d);
     const float q = a * y;
     return fmaf(fmaf(-d, q, a), y, q);
 }
@@ -265,7 +273,8 @@ __device__ __forceinline__ bool in_powers(uint32_t bits) {
 // Whether a step's coefficients allow root_normal and quotient_normal for
 // values in the ranges that adam8_four asks of its moments: then
 // d = s * RB + eps lies in [2^-48, 2^46], the numerator in [2^-74, 2^50] and
-// the quotient in [2^-120, 2^98], and its residuals are exact.
+// the quotient in [2^-120, 2^98], and the residuals' smallest units (2^-122 and
+// up, 2^-144 for the root's) are float32 numbers.
 __device__ __forceinline__ bool usual_coefficients(const StepCoef& c) {
     return in_powers<-24, 10>(__float_as_uint(c.step_size)) && in_powers<0, 12>(__float_as_uint(c.rsqrt_bc2)) &&
            __float_as_uint(c.eps) < (127u + 20u) << 23;
