@@ -71,3 +71,33 @@ def test_a_stream_waits_for_a_table_built_on_another(Z, bits):
     Z.zero_multi_adam_step(tables[1], hp, stream=second)
     torch.cuda.synchronize()
     assert same(got[0], want) and same(other[0], want)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_released_gradients_free_their_memory(Z, bits):
+    """New gradients every step, dropped after it: the memory is free between
+    the steps, the results are those of fixed buffers."""
+    # of a size that the allocator serves from blocks of their own
+    sizes = [3_000_001, 5_000_000]
+    make = lambda k: [torch.randn(n, generator=torch.Generator("cuda").manual_seed(10 * k + i), device="cuda")  # noqa: E731
+                      .mul_(1e-2).bfloat16() for i, n in enumerate(sizes)]
+    masters = lambda: [torch.zeros(n, device="cuda") for n in sizes]  # noqa: E731
+    fixed = make(0)
+    want = Z.MultiAdam(masters(), fixed, hyper=[HYPER], max_grad_norm=1.0, state_bits=bits, device_state=True)
+    got = Z.MultiAdam(masters(), make(0), hyper=[HYPER], max_grad_norm=1.0, state_bits=bits, device_state=True)
+    got.release_grads()
+    torch.cuda.synchronize()
+    base = torch.cuda.memory_allocated()
+    with pytest.raises(ValueError, match="released"):
+        got.step()
+    for k in range(4):
+        for x, y in zip(fixed, make(k)):
+            x.copy_(y)
+        want.step()
+        grads = make(k)
+        got.step(grads)
+        got.release_grads()
+        del grads, x, y
+        # the copy of a rebuilt table is all that may have come (less than its list's 2 bytes an element)
+        assert torch.cuda.memory_allocated() - base < sum(sizes) * 2 // 10
+    assert same(got.masters, want.masters) and same(got.exp_avgs, want.exp_avgs) and same(got.exp_avg_sqs, want.exp_avg_sqs)

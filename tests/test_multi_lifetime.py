@@ -79,3 +79,42 @@ def test_other_streams_wait_for_the_tables_copy(monkeypatch):
     recording[0] = False
     t._ptrs(0, third)
     assert third.waited == [copied]
+
+
+def test_released_gradients():
+    """A table lets go of its gradients when told to, and is not used until it
+    has others; ones in the same place need no new description.  What a graph
+    was recorded with stays."""
+    m, a, b, g, p = fake_list([100, 7])
+    t = Z.TensorTable(m, a, b, g, p)
+    seen = [weakref.ref(x) for x in g]
+    key, host = t._grad_key, t.host
+    t.release_grads()
+    t.release_grads()
+    del g
+    gc.collect()
+    assert all(r() is None for r in seen)
+    for call in (lambda: Z.zero_multi_adam_step(t, [Z.AdamHyper()], stream=0),
+                 lambda: Z.zero_multi_unscale_norm_overflow(t, 1.0, FakeDev(1, torch.float64), FakeDev(1, torch.int32),
+                                                            FakeDev(256, torch.uint8), stream=0)):
+        with pytest.raises(ValueError, match="released"):
+            call()
+    g = fake_list([100, 7])[3]
+    t.set_grads(g)                                         # where the former ones were
+    assert t.grads == g and t._grad_key is key and t.host is host
+    t._captured = True
+    seen = [weakref.ref(x) for x in g]
+    t.release_grads()
+    del g
+    gc.collect()
+    assert all(r() is not None for r in seen)
+    t.set_grads(moved([100, 7], 8))
+    gc.collect()
+    assert all(r() is not None for r in seen) and t.host is not host
+
+
+def test_released_gradients_of_an_empty_list():
+    t = Z.TensorTable.of_grads([])
+    t.release_grads()
+    t.set_grads([])
+    assert t.grads == []

@@ -33,8 +33,9 @@ def _where(grads):
 
 class TensorTable:
     """The list's table (zero_multi_table_build): a host part and its device
-    copy.  Holds references to the tensors and describes their addresses: that
-    one is resized or given other storage afterwards is not seen.  groups:
+    copy.  Holds references to the tensors (the gradients: until release_grads)
+    and describes their addresses: that one is resized or given other storage
+    afterwards is not seen.  groups:
     hyperparameter group per tensor (default 0).  state_bits 8: exp_avgs and
     exp_avg_sqs are the tensors' moments8 and scales8 (uint8)."""
 
@@ -84,6 +85,19 @@ class TensorTable:
             self._build(grads, key)
             if captured:
                 self._kept.append(old)
+        elif self.grads is None:
+            self.grads = list(grads)
+
+    def release_grads(self) -> None:
+        """Let go of the gradient tensors, once the calls that read them are
+        enqueued: else they stay allocated until set_grads names others.  The table
+        then needs set_grads before its next use (a no-op again if the allocator
+        put the new ones in the same place).  Gradients that a recorded graph reads
+        are kept.  As for any torch tensor, calls on another stream than the
+        gradients' own need record_stream on them first."""
+        if self._captured and self.grads is not None:
+            self._kept.append(self.grads)
+        self.grads = None
 
     def _describe(self, grads) -> None:
         """The C descriptions of the whole list."""
@@ -137,6 +151,8 @@ class TensorTable:
         self._addresses = self.host.data_ptr(), None if self.device is None else self.device.data_ptr()
 
     def _ptrs(self, current: int, stream):
+        if self.grads is None:
+            raise ValueError("the table's gradients were released: set_grads first")
         if self._index < 0:
             return self._addresses
         if self._index != current:

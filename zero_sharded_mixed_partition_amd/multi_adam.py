@@ -123,7 +123,8 @@ class MultiAdam:
              unscaled: bool = False) -> Optional[bool]:
         """One full step.  grads: this step's gradients, where they are not in the
         buffers given before (the table is then built anew, which costs the host
-        about a microsecond a tensor).  allreduce as in ShardAdam.step.
+        about a microsecond a tensor); the list holds them until it is given others
+        or release_grads() is called.  allreduce as in ShardAdam.step.
         unscaled: the gradients are already divided by the loss scale.  Returns
         True if the step was skipped (None with device_state)."""
         if grads is not None:
@@ -153,6 +154,12 @@ class MultiAdam:
         if not skip:
             self.t += 1
         return skip
+
+    def release_grads(self) -> None:
+        """After step(): let go of its gradients, so that clearing them (p.grad =
+        None) frees their memory for the next backward pass.  The next step then
+        has to be given its gradients."""
+        self.table.release_grads()
 
     def read_state(self):
         """device_state: copy the state to the host (waits for the steps enqueued
