@@ -102,7 +102,9 @@ class MultiAdam:
         views of the shard's flat buffers.  groups: the group of each of the
         model's tensors; moments: the shard's flat fp32 moments to go on from.
         The shard's padding is not touched; a rank that holds nothing else has an
-        empty list, with which it takes part in the exchange and the decision."""
+        empty list, with which it takes part in the exchange and the decision.
+        Where grad is an accumulated fp32 copy, which is already unscaled, steps
+        need unscaled=True."""
         def cut(flat):
             return [flat[b:b + n] for _, _, b, n in fragments]
         kw.setdefault("device", master.device)
@@ -125,8 +127,10 @@ class MultiAdam:
         buffers given before (the table is then built anew, which costs the host
         about a microsecond a tensor); the list holds them until it is given others
         or release_grads() is called.  allreduce as in ShardAdam.step.
-        unscaled: the gradients are already divided by the loss scale.  Returns
-        True if the step was skipped (None with device_state)."""
+        unscaled: the gradients are already divided by the loss scale, as the fp32
+        copy of ShardAdam.accumulate and reduce is: unlike ShardAdam, a list does
+        not tell that from their type.  Returns True if the step was skipped (None
+        with device_state)."""
         if grads is not None:
             self.table.set_grads(grads)
         if self.state is not None:
