@@ -595,7 +595,9 @@ int zero_shard_grad_sum_norm_dev(float* acc, const void* const* slices, int32_t 
  * and, modulo 2^64, key is the lower half of K2 ^ (K2 >> 32), with
  *     K0 = seed * 0x9E3779B97F4A7C15 + t * 0xBB67AE8584CAA73B,
  *     K2 = (K0 ^ (K0 >> 32)) * 0x6A09E667F3BCC909.
- * A step is thus reproducible bit for bit from its inputs, seed and t.
+ * A step is thus reproducible bit for bit from its inputs, seed and t.  Ranks
+ * that share a seed round element e of their shards with the same words: give
+ * each rank a seed of its own.
  * A moment that becomes inf or NaN is stored as NaN, and its block's scale and
  * other codes are then unspecified; with d_global_overflow given such a step
  * is skipped.
@@ -678,7 +680,8 @@ int zero_moments8_unpack(float* exp_avg, float* exp_avg_sq, const void* moments8
  * zero_multi_decide_dev: as zero_step_decide_dev for n_groups sets (their
  *   blocks to d_coefs, in order).  unscaled nonzero: the gradients are already
  *   unscaled (inv_loss_scale 1), whatever their type; zero: all of them are
- *   multiplied by 1/scale, fp32 ones too.
+ *   multiplied by 1/scale, fp32 ones too.  The sets are taken by value: a call
+ *   recorded in a graph keeps those it was recorded with.
  * zero_multi_unscale_norm_overflow_dev: the norm pass with 1/scale from
  *   d_state.  zero_multi_norm_decide_dev: that and the decision of a single
  *   rank, as zero_shard_norm_decide_dev.

@@ -35,7 +35,8 @@ class TensorTable:
     """The list's table (zero_multi_table_build): a host part and its device
     copy.  Holds references to the tensors (the gradients: until release_grads)
     and describes their addresses: that one is resized or given other storage
-    afterwards is not seen.  groups:
+    afterwards is not seen.  A recorded graph reads the device copy: keep the table
+    as long as the graph.  groups:
     hyperparameter group per tensor (default 0).  state_bits 8: exp_avgs and
     exp_avg_sqs are the tensors' moments8 and scales8 (uint8)."""
 
@@ -219,7 +220,8 @@ def _coefs_ptr(d_coefs, n_groups: int, dev: int) -> Optional[int]:
 def zero_multi_norm_decide_dev(table: TensorTable, hps: Sequence[AdamHyper], state: StepState, sqnorm, overflow,
                                d_coefs, workspace, tensor_sqnorm=None, unscaled: bool = False, stream=None) -> None:
     """The norm pass of a single rank, whose last kernel also makes the step's
-    decision: one coefficient block per set into d_coefs, the state advanced."""
+    decision: one coefficient block per set into d_coefs, the state advanced.  A
+    recorded call keeps the hyperparameters it was recorded with."""
     dev, tab, out, ws = _norm_args(table, sqnorm, overflow, tensor_sqnorm, workspace, stream)
     _L.check(_L.lib().zero_multi_norm_decide_dev(*tab, 1 if unscaled else 0, _hypers(hps), len(hps), state.ptr(), *out,
                                                  _coefs_ptr(d_coefs, len(hps), dev), *ws, _stream(stream, dev)),

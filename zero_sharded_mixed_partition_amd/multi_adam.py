@@ -7,7 +7,9 @@ without weight decay).  The step is ShardAdam's: the norm and overflow pass over
 all gradients, the data-parallel exchange of its two scalars, the decision, the
 update; host-scaled, or with the loss scaler and step counter in device memory
 (device_state=True), where a step never waits and can be recorded in a torch
-CUDA graph.
+CUDA graph.  A recorded step keeps the hyperparameters (and the seed) that it was
+recorded with, and reads the list's table: record it again to change them, and
+keep the MultiAdam as long as the graph.
 """
 from typing import Callable, Optional, Sequence
 
@@ -47,7 +49,8 @@ class MultiAdam:
         (exp_avgs, exp_avg_sqs) fp32 lists to go on from, else zeros; with
         state_bits 8 they are rounded into the 8-bit format.  tensor_norms: the
         norm pass also fills self.tensor_sqnorm.  seed keys the rounding of 8-bit
-        moments.  device: where an empty list keeps its scalars (its steps update
+        moments, with each tensor's and element's index: give each rank its own, else
+        they round with the same words.  device: where an empty list keeps its scalars (its steps update
         nothing, but exchange and decide)."""
         if not len(grads) and device is None:
             raise ValueError("an empty list needs a device")

@@ -19,9 +19,11 @@ class ShardAdam8(ShardAdam):
                  device_state: bool = False, seed: int = 0):
         """moments8, scales8: uint8 device tensors of zero_moments8_bytes(n) and
         zero_scales8_bytes(n) bytes, or None for moments of zero.  seed keys the
-        stochastic rounding (with the step's index), so equal runs agree bit for
-        bit.  A step with device_state=True can be recorded in a torch CUDA
-        graph."""
+        stochastic rounding (with the step's and the element's index), so equal
+        runs agree bit for bit; give each rank its own, else their shards are
+        rounded with the same words.  A step with device_state=True can be recorded
+        in a torch CUDA graph, which keeps the hyperparameters and the seed of its
+        recording."""
         if master.dtype != torch.float32 or not master.is_cuda or not master.is_contiguous():
             raise ValueError("master must be a contiguous fp32 device tensor")
         if (moments8 is None) != (scales8 is None):
