@@ -60,6 +60,7 @@ class TensorTable:
         self.masters, self.exp_avgs, self.exp_avg_sqs = own(masters), own(exp_avgs), own(exp_avg_sqs)
         self.params_out, self.groups = own(params_out), own(groups)
         self.n_groups = 1 + max(self.groups) if self.groups else 1
+        self._ready = None                     # the copy to the device has run
         self._kept = []                        # tables that recorded graphs read, and their gradients
         self._describe(grads)
         self._build(grads, _where(grads))
@@ -145,9 +146,9 @@ class TensorTable:
         self._captured = False
         # raw handles of the streams that have read the device copy; its own needs no wait and no record
         self._streams = {_stream(None, index)} if on_gpu else set()
-        self._ready = None
         if on_gpu:
-            self._ready = torch.cuda.Event()
+            if self._ready is None:
+                self._ready = torch.cuda.Event()
             self._ready.record(torch.cuda.current_stream(index))
         self._addresses = self.host.data_ptr(), None if self.device is None else self.device.data_ptr()
 
