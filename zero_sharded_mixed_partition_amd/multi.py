@@ -77,8 +77,8 @@ class TensorTable:
         for it; the old one lives until every torch stream that read it has passed
         (a raw stream handle is the caller's to wait for, and so is the copy if a
         graph is recorded on another stream: torch.cuda.graph synchronizes first).
-        A graph recorded with the table keeps reading the old gradients (which the
-        table then keeps alive, with their description): record it again."""
+        A graph that torch recorded with the table keeps reading the old gradients
+        (which the table then keeps alive, with their description): record it again."""
         if len(grads) != self.n_tensors:
             raise ValueError(f"{len(grads)} gradients for {self.n_tensors} tensors")
         key = _where(grads)
