@@ -153,16 +153,23 @@ def prepare(case, seed):
     if own:
         import zero_sharded_mixed_partition_amd as Z
 
+        # what lies between two groups is updated with the buffer it is in, as a row of its own
+        ends = [a + k * r * c for (k, r, c), a in zip(s["groups"], starts)]
+        gaps = [(a, b) for a, b in zip(ends, starts[1:] + [total]) if a < b and op != "orthogonalize"]
+        if op == "update":
+            for a, b in gaps:
+                s["ortho"][a:b] = 0.0
+
         def views(flat):
             if flat is None:
                 return None
             three = [flat[a:a + k * r * c].view(k, r, c) for (k, r, c), a in zip(s["groups"], starts)]
-            return three if case.get("batched") else [x for g in three for x in g]
+            return (three if case.get("batched") else [x for g in three for x in g]) + [flat[a:b].view(1, -1) for a, b in gaps]
 
         lists = {"momentums": views(s.get("momentum")), "grads": views(s.get("grad")), "masters": views(s.get("master")),
                  "params_out": views(s.get("param")), "updates": views(s.get("update")), "orthos": views(s.get("ortho"))}
         if op == "update":
-            lists["scales"] = [_growth(k, r, c) for k, r, c in s["groups"] for _ in range(k)]
+            lists["scales"] = [_growth(k, r, c) for k, r, c in s["groups"] for _ in range(k)] + [0.0] * len(gaps)
         s["table"] = Z.MatrixTable(**{k: v for k, v in lists.items() if v is not None})
         if op == "orthogonalize":
             s["workspace"] = torch.empty(Z.zero_multi_orthogonalize_workspace_bytes(s["table"]), dtype=torch.uint8,
