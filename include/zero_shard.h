@@ -37,7 +37,10 @@
  *    ranks' scalars, and the step on host cores (whose worker threads start
  *    on first use and live until the process ends);
  *  - the step with its moments in 8 bits (zero_shard_adam8_step*,
- *    zero_moments8_*), and the step over a list of tensors (zero_multi_*);
+ *    zero_moments8_*), the step over a list of tensors (zero_multi_*), and the
+ *    step by orthogonalised momentum over a list of matrices (zero_matrix_*,
+ *    zero_multi_momentum_step*, zero_multi_orthogonalize*,
+ *    zero_multi_muon_update);
  *  - physically contiguous memory (zero_device_alloc_contiguous, zero_pool_*),
  *    whose purpose is to allocate, and the measurement copies
  *    (zero_copy_reference, zero_copy_widen_reference on the device,
@@ -725,6 +728,105 @@ int zero_multi_adam_step(const void* table, const void* d_table, const zero_adam
 int zero_multi_adam_step_coef(const void* table, const void* d_table, const void* d_coefs, int32_t n_groups,
                               uint64_t seed, const int64_t* d_step, const double* d_global_sqnorm,
                               const int32_t* d_global_overflow, void* hip_stream);
+
+/* ---------------------------------------------------------------------------
+ * Extra: a step by orthogonalised momentum over a list of matrices: momentum
+ * of the gradients, its orthogonalisation, and the update of the master
+ * weights by the result.  (Momentum as an exponential average with Nesterov's
+ * form; orthogonalisation by an odd polynomial iteration, Bjorck & Bowie 1971,
+ * with the quintic steps and the use as an optimizer of Jordan et al. 2024.)
+ *
+ * zero_matrix, one per matrix or batch of matrices of one shape:
+ *  master      device, [batch][rows][cols] float32, updated in place
+ *  momentum    device, the same shape, float32, updated in place
+ *  grad        device, of grad_dtype, read only
+ *  update      device, of update_dtype (fp16, bf16 or fp32): what the momentum
+ *              pass writes and the orthogonalisation reads
+ *  ortho       device, of ortho_dtype (fp16 or bf16): what the orthogonalisation
+ *              writes and the update reads; may be `update` itself, in its type
+ *  param_out   device, of param_dtype (fp16 or bf16), or NULL (no copy)
+ *  scale       finite factor of the learning rate for this matrix
+ *  group       index into the step's hyperparameters, [0, ZERO_MAX_GROUPS)
+ * Matrices are row-major without gaps, and pointers need only be aligned to
+ * their elements.  A matrix may be empty.  Sides reach ZERO_MAX_MATRIX_SIDE.
+ * A call needs the buffers that it names below on every matrix that has
+ * elements; the others may be NULL.  Gradients may share memory with one
+ * another; no other buffer may overlap another one of the list.  A matrix has to
+ * be whole: the fragment of one that a rank's partition cuts through is gathered
+ * first.
+ *
+ * zero_matrix_table_build (host only): as zero_multi_table_build, the table of
+ *   such a list.  About 16 bytes per 8192 elements, 100 per matrix and 16 per
+ *   tile of the products.
+ * zero_multi_momentum_step (momentum, grad, update): per element, in float32,
+ *     g = (1 - mu) * (grad * s);  m = fma(mu, m, g);  u = nesterov ? fma(mu, m, g) : m
+ *   with s the factor of zero_shard_adam_step (the inverse loss scale times the
+ *   clip coefficient; no clipping where max_grad_norm <= 0) and mu the group's
+ *   momentum; m is stored, and u rounded to update_dtype.
+ * zero_multi_momentum_step_coef: s from a coefficient block in device memory
+ *   (of zero_multi_decide_dev, say; only its loss scale and clip norm are read).
+ * zero_multi_orthogonalize (update, ortho): each matrix U of the list on its
+ *   own, with |U| its Frobenius norm,
+ *     X = U / max(|U|, eps);  n_steps times  X = a X + (b X X^T + c X X^T X X^T) X
+ *   with (a, b, c) = coefs[3 k .. 3 k + 2] at step k; ortho = X.  (For X with
+ *   more rows than columns X X^T ... X is formed as X ... X^T X, which is equal.)
+ *   eps = 0 leaves a zero matrix zero.  X and the products are rounded to fp16
+ *   between steps, sums are float32: about 1.2e-3 off in all (relative,
+ *   Frobenius) with five steps of (3.4445, -4.7750, 2.0315) where singular values
+ *   are spread as those of a random matrix, more where they differ by
+ *   thousands.  A matrix that holds an inf or a NaN becomes NaN.  Coefficients
+ *   have to keep singular values of [0, 1] within 4, and |b x + c x^2| of their
+ *   squares within 32 (ZERO_ERANGE).  1 <= n_steps <= ZERO_MAX_ORTHO_STEPS.
+ *   Workspace: zero_multi_orthogonalize_workspace_bytes(table) bytes, 256-byte
+ *   aligned, clobbered: about 4 bytes an element, and 4 for each of a short
+ *   side's square, of the list or of a part of it of 2 GiB.  Calls, and graphs
+ *   recorded with them, that may run at the same time need a workspace each.
+ * zero_multi_muon_update (master, ortho; param_out): per element, in float32,
+ *     p = fma(p, 1 - lr * weight_decay, -((lr * scale) * o));  param = round(p)
+ * With d_global_overflow given and nonzero when the kernels run, a call writes
+ * nothing.  hp[group] of n_groups sets; the unused fields of a set are checked.
+ * Results repeat bit for bit, and depend on the matrix alone, not on the list.
+ * Errors: ZERO_EINVAL, ZERO_EALIGN, ZERO_ERANGE, ZERO_ENOSPC, ZERO_EHIP.
+ * ------------------------------------------------------------------------- */
+#define ZERO_MAX_MATRIX_SIDE (1 << 22)
+#define ZERO_MAX_ORTHO_STEPS 32
+
+typedef struct {
+    float* master;
+    float* momentum;
+    const void* grad;
+    void* update;
+    void* ortho;
+    void* param_out;
+    int64_t rows, cols, batch;
+    double scale;
+    int32_t grad_dtype, update_dtype, ortho_dtype, param_dtype;
+    int32_t group;
+    int32_t reserved;       /* 0 */
+} zero_matrix;
+
+typedef struct {
+    double lr;
+    double momentum;        /* [0, 1) */
+    double weight_decay;
+    int32_t nesterov;
+    int32_t reserved;       /* 0 */
+} zero_muon_params;
+
+int zero_matrix_table_build(const zero_matrix* matrices, int32_t n_matrices, void* table, size_t capacity, size_t* bytes,
+                            size_t* device_bytes);
+int zero_multi_momentum_step(const void* table, const void* d_table, const zero_muon_params* hp, int32_t n_groups,
+                             double inv_loss_scale, double max_grad_norm, const double* d_global_sqnorm,
+                             const int32_t* d_global_overflow, void* hip_stream);
+int zero_multi_momentum_step_coef(const void* table, const void* d_table, const zero_muon_params* hp, int32_t n_groups,
+                                  const void* d_coef, const double* d_global_sqnorm, const int32_t* d_global_overflow,
+                                  void* hip_stream);
+size_t zero_multi_orthogonalize_workspace_bytes(const void* table);
+int zero_multi_orthogonalize(const void* table, const void* d_table, const double* coefs, int32_t n_steps, double eps,
+                             const int32_t* d_global_overflow, void* d_workspace, size_t workspace_bytes,
+                             void* hip_stream);
+int zero_multi_muon_update(const void* table, const void* d_table, const zero_muon_params* hp, int32_t n_groups,
+                           const int32_t* d_global_overflow, void* hip_stream);
 
 /* ---------------------------------------------------------------------------
  * Extra, a measurement aid (not a step of the method): a plain device copy, one

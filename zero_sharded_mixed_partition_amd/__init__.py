@@ -18,14 +18,16 @@ in the library's kernels.
     zero_loss_scaler_update(scaler, overflow) -> skip
 
 moments8.py adds the shard's step with 8-bit moments, multi.py the step over a
-list of tensors; ShardAdam, ShardAdam8 and MultiAdam run whole steps.
+list of tensors, matrices.py the step by orthogonalised momentum over a list of
+matrices; ShardAdam, ShardAdam8, MultiAdam and MultiMuon run whole steps.
 """
 import ctypes
 from typing import List, Optional, Sequence, Tuple
 
 from . import _lib as _L
 from ._lib import (ZERO_BF16, ZERO_F16, ZERO_F32, ZeroShardError, zero_adam_hyper,  # noqa: F401
-                   zero_adam_params, zero_fragment, zero_loss_scaler, zero_step_state)
+                   zero_adam_params, zero_fragment, zero_loss_scaler, zero_muon_params,  # noqa: F401
+                   zero_step_state)
 
 __all__ = ["zero_partition_plan", "zero_rank_fragments", "zero_norm_workspace_bytes",
            "zero_shard_unscale_norm_overflow", "zero_shard_unscale_norm_overflow_noalloc", "zero_shard_adam_step",
@@ -44,7 +46,10 @@ __all__ = ["zero_partition_plan", "zero_rank_fragments", "zero_norm_workspace_by
            "zero_moments8_unpack", "zero_shard_adam8_step", "zero_shard_adam8_step_coef", "TensorTable", "MAX_GROUPS",
            "zero_multi_norm_workspace_bytes", "zero_multi_unscale_norm_overflow",
            "zero_multi_unscale_norm_overflow_dev", "zero_multi_norm_decide_dev", "zero_multi_decide_dev",
-           "zero_multi_adam_step", "zero_multi_adam_step_coef", "ShardAdam8", "MultiAdam"]
+           "zero_multi_adam_step", "zero_multi_adam_step_coef", "ShardAdam8", "MultiAdam", "MatrixTable", "MuonHyper",
+           "ORTHO_COEFS", "zero_multi_momentum_step", "zero_multi_momentum_step_coef",
+           "zero_multi_orthogonalize_workspace_bytes", "zero_multi_orthogonalize", "zero_multi_muon_update",
+           "MultiMuon", "muon_scale"]
 
 
 def zero_abi_version() -> int:
@@ -655,9 +660,13 @@ from .moments8 import (zero_moments8_bytes, zero_moments8_pack, zero_moments8_un
 from .multi import (MAX_GROUPS, TensorTable, zero_multi_adam_step, zero_multi_adam_step_coef,  # noqa: E402
                     zero_multi_decide_dev, zero_multi_norm_decide_dev, zero_multi_norm_workspace_bytes,
                     zero_multi_unscale_norm_overflow, zero_multi_unscale_norm_overflow_dev)
+from .matrices import (MatrixTable, MuonHyper, ORTHO_COEFS, zero_multi_momentum_step,  # noqa: E402
+                       zero_multi_momentum_step_coef, zero_multi_muon_update, zero_multi_orthogonalize,
+                       zero_multi_orthogonalize_workspace_bytes)
 from .shard import ShardAdam  # noqa: E402
 from .shard8 import ShardAdam8  # noqa: E402
 from .multi_adam import MultiAdam  # noqa: E402
+from .multi_muon import MultiMuon, muon_scale  # noqa: E402
 from .offload import OffloadShardAdam  # noqa: E402
 from . import checkpoint  # noqa: E402,F401
 

@@ -48,6 +48,17 @@ class zero_tensor(ctypes.Structure):
                 ("numel", c_i64), ("grad_dtype", c_i32), ("param_dtype", c_i32), ("group", c_i32), ("reserved", c_i32)]
 
 
+class zero_matrix(ctypes.Structure):
+    _fields_ = [("master", c_vp), ("momentum", c_vp), ("grad", c_vp), ("update", c_vp), ("ortho", c_vp), ("param_out", c_vp),
+                ("rows", c_i64), ("cols", c_i64), ("batch", c_i64), ("scale", c_dbl), ("grad_dtype", c_i32),
+                ("update_dtype", c_i32), ("ortho_dtype", c_i32), ("param_dtype", c_i32), ("group", c_i32),
+                ("reserved", c_i32)]
+
+
+class zero_muon_params(ctypes.Structure):
+    _fields_ = [("lr", c_dbl), ("momentum", c_dbl), ("weight_decay", c_dbl), ("nesterov", c_i32), ("reserved", c_i32)]
+
+
 c_u64 = ctypes.c_uint64
 P_sz = ctypes.POINTER(c_sz)
 
@@ -119,6 +130,14 @@ SIGNATURES = {
     "zero_multi_decide_dev": (c_i32, [ctypes.POINTER(zero_adam_hyper), c_i32, c_i32, c_vp, c_vp, c_vp, c_vp]),
     "zero_multi_adam_step": (c_i32, [c_vp, c_vp, ctypes.POINTER(zero_adam_params), c_i32, c_u64, c_vp, c_vp, c_vp]),
     "zero_multi_adam_step_coef": (c_i32, [c_vp, c_vp, c_vp, c_i32, c_u64, c_vp, c_vp, c_vp, c_vp]),
+    "zero_matrix_table_build": (c_i32, [ctypes.POINTER(zero_matrix), c_i32, c_vp, c_sz, P_sz, P_sz]),
+    "zero_multi_momentum_step": (c_i32, [c_vp, c_vp, ctypes.POINTER(zero_muon_params), c_i32, c_dbl, c_dbl, c_vp, c_vp,
+                                         c_vp]),
+    "zero_multi_momentum_step_coef": (c_i32, [c_vp, c_vp, ctypes.POINTER(zero_muon_params), c_i32, c_vp, c_vp, c_vp,
+                                              c_vp]),
+    "zero_multi_orthogonalize_workspace_bytes": (c_sz, [c_vp]),
+    "zero_multi_orthogonalize": (c_i32, [c_vp, c_vp, ctypes.POINTER(c_dbl), c_i32, c_dbl, c_vp, c_vp, c_sz, c_vp]),
+    "zero_multi_muon_update": (c_i32, [c_vp, c_vp, ctypes.POINTER(zero_muon_params), c_i32, c_vp, c_vp]),
     "zero_status_string": (ctypes.c_char_p, [c_i32]),
     "zero_last_error": (ctypes.c_char_p, []),
 }

@@ -25,18 +25,13 @@
 #include <type_traits>
 #include <vector>
 
+#include "list_table.h"
 #include "moments8.h"
 
 namespace zero_shard {
 namespace {
 
 constexpr int64_t kChunk = 8192;                          // elements per entry of the norm pass's map
-// A unit of the update is 2^k consecutive tasks of one tensor, k <= kMaxUnit;
-// a tensor's last unit leaves workgroups idle.  The table takes the largest k
-// whose workgroups exceed the tasks by no more than a tenth: 3,000 tensors of
-// 500 elements take 2 tasks a unit and 9.7 us, with 32 a unit 108 us (8 bits:
-// 10.6 and 82); 39 tensors of 1.07B elements keep 32 a unit and a map of 1 MB.
-constexpr int kMaxUnit = 5;
 // LDS reserved per one-wave workgroup and never used, to cap residency (as for
 // the shards' updates).  Measured on MI355X, 1.07B elements in 39 tensors with
 // bf16 gradients and copies: 32 bits 6.62 TB/s at 15 KiB (10 resident per CU),
@@ -51,14 +46,6 @@ constexpr int64_t kMultiMaxGrid = (int64_t(1) << 26) - 1;
 // 4: 24.5 and 25.6; 17M in 4: 10.0 and 9.4; 3,000 tensors of 500: 13.8 and
 // 11.0; 10,000 of 64: 26.2 and 18.3.
 constexpr int kMultiNormBlocks = 512;
-// A list's fp32 tensors may start anywhere.  The update's tasks are laid out so
-// that the master's runs start at multiples of 256 bytes: otherwise two waves,
-// on different XCDs, share the cache line between their runs and each writes
-// part of it.  Tensors cut end to end from flat buffers have the same phase in
-// every stream.  57 tensors of 11.2M elements in all, end to end, none aligned:
-// 50.4 us with it, 62.4 without (6.22 and 5.03 TB/s).  8-bit moments keep their
-// blocks, which start with the tensor.
-constexpr int64_t kPhase = 64;                            // elements
 constexpr uint32_t kTableMagic = 0x5A53544Du;
 
 // ---------------------------------------------------------------- the table
@@ -78,10 +65,6 @@ struct TensorDesc {
     int32_t reserved;
 };
 
-struct PieceRef {
-    uint32_t tensor, piece;   // index of the descriptor, and which chunk or unit of that tensor
-};
-
 // At the start of the table.  The device image is [0, device_bytes): this
 // header, the descriptors of the tensors that hold elements, the two maps and
 // the caller's indices of the empty ones.  The host part behind it holds the
@@ -97,15 +80,6 @@ struct TableHeader {
     int64_t ranges_at, n_ranges;
     int64_t grads_at, n_grads, bytes;
 };
-
-struct AddressRange {
-    uintptr_t lo, hi;
-};
-
-template <typename T>
-const T* at(const void* table, int64_t offset) {
-    return reinterpret_cast<const T*>(static_cast<const char*>(table) + offset);
-}
 
 // What the kernels need of a table, by value.
 struct TableRef {
@@ -403,8 +377,6 @@ __global__ __launch_bounds__(kTaskThreads) void multi_adam_devcoef(const StepCoe
 
 // ---------------------------------------------------------------- host side
 
-int64_t pad16(int64_t x) { return (x + 15) & ~(int64_t)15; }
-
 // At least one block: it also leaves the factor for the second kernel.
 int norm_grid(const TableHeader& h) {
     const bool short_runs = h.n_chunks <= 8 * kMultiNormBlocks || h.n_chunks < 8 * (int64_t)h.n_tensors;
@@ -433,14 +405,6 @@ TableRef table_ref(const TableHeader& h, const void* d_table) {
     return TableRef{at<TensorDesc>(d_table, h.desc_at), at<PieceRef>(d_table, h.chunks_at),
                     at<PieceRef>(d_table, h.units_at), at<uint32_t>(d_table, h.empty_at), h.n_chunks, h.n_units,
                     (int32_t)h.unit_log2, h.n_tensors, h.n_empty};
-}
-
-// Whether [p, p + bytes) meets one of n sorted, disjoint address ranges.
-bool meets(const AddressRange* r, int64_t n, const void* p, int64_t bytes) {
-    if (p == nullptr || bytes == 0) return false;
-    const uintptr_t lo = reinterpret_cast<uintptr_t>(p), hi = lo + (uintptr_t)bytes;
-    const AddressRange* f = std::upper_bound(r, r + n, lo, [](uintptr_t x, const AddressRange& a) { return x < a.hi; });
-    return f != r + n && f->lo < hi;
 }
 
 // ... one that the update writes
@@ -543,12 +507,6 @@ dim3 update_grid(const TableHeader& h) {
     return dim3((unsigned)(w < kMultiMaxGrid ? w : kMultiMaxGrid));
 }
 
-struct Region {
-    uintptr_t lo, hi;
-    bool write;
-    int32_t tensor;
-};
-
 // Elements that the first task of a tensor starts before it.
 int32_t phase_of(const zero_tensor& t, int32_t state_bits) {
     return state_bits == 32 ? (int32_t)(reinterpret_cast<uintptr_t>(t.master) / sizeof(float) % kPhase) : 0;
@@ -617,23 +575,10 @@ int build_table(const zero_tensor* tensors, int32_t n_tensors, int32_t state_bit
         add(t.exp_avg_sq, state_bits == 8 ? (int64_t)zero_scales8_bytes(t.numel) : t.numel * 4, true);
         if (t.param_out) add(t.param_out, t.numel * 2, true);
     }
-    // no written range may meet another range; gradients may be shared
-    std::sort(regions.begin(), regions.end(), [](const Region& a, const Region& b) { return a.lo < b.lo; });
-    uintptr_t any_hi = 0, write_hi = 0;
     std::vector<AddressRange> ranges, grads;
-    for (const Region& r : regions) {
-        if (r.lo < (r.write ? any_hi : write_hi))
-            return fail(ZERO_EINVAL, "tensor %d: a buffer the update writes overlaps another of the list", r.tensor);
-        any_hi = std::max(any_hi, r.hi);
-        if (!r.write) {
-            if (!grads.empty() && grads.back().hi >= r.lo) grads.back().hi = std::max(grads.back().hi, r.hi);
-            else grads.push_back({r.lo, r.hi});
-            continue;
-        }
-        write_hi = std::max(write_hi, r.hi);
-        if (!ranges.empty() && ranges.back().hi == r.lo) ranges.back().hi = r.hi;
-        else ranges.push_back({r.lo, r.hi});
-    }
+    const int32_t clash = merge_regions(regions, &ranges, &grads);
+    if (clash >= 0)
+        return fail(ZERO_EINVAL, "tensor %d: a buffer the update writes overlaps another of the list", clash);
     if (state_bits) {
         int64_t tasks = 0;
         for (int32_t i = 0; i < n_tensors; ++i) tasks += tasks_of(tensors[i], state_bits);

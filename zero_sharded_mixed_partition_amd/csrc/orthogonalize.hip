@@ -1,0 +1,559 @@
+// Orthogonalisation of a list of matrices by a quintic Newton-Schulz iteration:
+//
+//     X = U / max(|U|_F, eps),  then per step (a, b, c)  X <- a X + (b A + c A A) X,  A = X X^T
+//
+// on the short side: a matrix with more rows than columns is worked on
+// transposed, which its first load and last store do.
+//
+// What is rounded.  The iterate X and the two symmetric s x s matrices A and
+// B = b A + c A A are held in fp16 between the products, each times a power of
+// two that keeps typical entries far from fp16's small end (X: about sqrt(l),
+// A and B: 2^10); every sum is float32, |U|_F float64.  fp16 instead of bf16
+// because the iteration multiplies what is lost: on 1024 x 1024 matrices of
+// noise plus a low-rank part the result is 1.2e-3 off (relative, Frobenius)
+// with fp16 in these places and 1e-2 with bf16, at the same MFMA rate.
+//
+// Products.  All three run through one MFMA kernel in square tiles of T x T
+// over a padded copy in the workspace, so no load is bounded and padding stays
+// zero.  X X^T and A A are symmetric: only tiles on and below the diagonal are
+// formed, and stored twice.
+#include <hip/hip_runtime.h>
+
+#include <cmath>
+#include <vector>
+
+#include "matrix_table.h"
+
+namespace zero_shard {
+namespace {
+
+typedef _Float16 h8 __attribute__((ext_vector_type(8)));
+typedef _Float16 h4 __attribute__((ext_vector_type(4)));
+typedef short s4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+constexpr int kLog2A = 10;                       // A and B are held times 2^10
+constexpr int kDepth = 64;                       // elements of the inner dimension per stage
+constexpr int64_t kPassBytes = int64_t(2) << 30; // workspace of a pass, if it holds more than one matrix
+
+enum { kGram, kPoly, kApply };
+
+struct NsRef {
+    const MatrixItem* items;
+    const TileRef* tiles;
+    char* ws;
+    const int32_t* d_ovf;
+
+    __device__ __forceinline__ const ZS_CONSTANT TileRef& tile(int64_t i) const {
+        return ((const ZS_CONSTANT TileRef*)tiles)[i];
+    }
+    __device__ __forceinline__ const ZS_CONSTANT MatrixItem& item(uint32_t i) const {
+        return ((const ZS_CONSTANT MatrixItem*)items)[i];
+    }
+    __device__ __forceinline__ bool skipped() const { return d_ovf != nullptr && *d_ovf != 0; }
+};
+
+// ---------------------------------------------------------------- load and norm
+
+template <int DT>
+__device__ __forceinline__ void ld4(const void* U, int64_t e, int valid, float v[4]) {
+    if (valid >= 4) {
+        Grad4<DT> q;
+        q.load(U, e);
+        q.values(v);
+        return;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = k < valid ? ld_grad1<DT>(U, e + k) : 0.0f;
+}
+
+__device__ __forceinline__ void ld4(int dt, const void* U, int64_t e, int valid, float v[4]) {
+    if (dt == ZERO_F16) ld4<ZERO_F16>(U, e, valid, v);
+    else if (dt == ZERO_BF16) ld4<ZERO_BF16>(U, e, valid, v);
+    else ld4<ZERO_F32>(U, e, valid, v);
+}
+
+// The caller's rows and columns of a tile of the iterate.
+struct TileBox {
+    int r0, c0, rows, cols;                      // the caller's matrix
+};
+
+__device__ __forceinline__ TileBox tile_box(const ZS_CONSTANT MatrixItem& m, const ZS_CONSTANT TileRef& t, int tile) {
+    const int i = t.i * tile, j = t.j * tile;
+    return m.tall ? TileBox{j, i, m.l, m.s} : TileBox{i, j, m.s, m.l};
+}
+
+// One tile's sum of squares into its slot.
+__global__ __launch_bounds__(kBlock) void ortho_squares(NsRef ref, int64_t first, int tile) {
+    if (ref.skipped()) return;
+    __shared__ double s_sq[kWaves];
+    __shared__ uint32_t s_bad[kWaves];
+    const ZS_CONSTANT TileRef& t = ref.tile(first + blockIdx.x);
+    const ZS_CONSTANT MatrixItem& m = ref.item(t.item);
+    const TileBox box = tile_box(m, t, tile);
+    double acc = 0.0;
+    for (int k = threadIdx.x; k < tile * tile / 4; k += kBlock) {
+        const int r = box.r0 + k / (tile / 4), c = box.c0 + k % (tile / 4) * 4;
+        if (r >= box.rows || c >= box.cols) continue;
+        float v[4];
+        ld4(m.udt, m.in, (int64_t)r * box.cols + c, box.cols - c, v);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc = fma((double)v[e], (double)v[e], acc);
+    }
+    uint32_t none = 0;
+    block_reduce(acc, none, s_sq, s_bad);
+    if (threadIdx.x == 0) reinterpret_cast<double*>(ref.ws + m.slots)[t.i * (m.lp / tile) + t.j] = acc;
+}
+
+// The factor 2^log2_scale / max(|U|_F, eps); NaN if U is not finite, so that all of the result is.
+__device__ __forceinline__ double norm_factor(const ZS_CONSTANT MatrixItem& m, const char* ws, double eps, double* s_sq,
+                                              uint32_t* s_bad) {
+    const double* slots = reinterpret_cast<const double*>(ws + m.slots);
+    double acc = 0.0;
+    for (int k = threadIdx.x; k < m.n_slots; k += kBlock) acc += slots[k];
+    uint32_t none = 0;
+    block_reduce(acc, none, s_sq, s_bad);
+    if (threadIdx.x == 0) s_sq[0] = acc;
+    __syncthreads();
+    const double norm = sqrt(s_sq[0]);
+    if (!(norm < INFINITY)) return NAN;
+    const double by = norm > eps ? norm : eps;
+    return by > 0.0 ? ldexp(1.0, m.log2_scale) / by : 0.0;
+}
+
+// The tile of X = U * factor, with its padding, in 64 x 64 blocks.
+__global__ __launch_bounds__(kBlock) void ortho_load(NsRef ref, int64_t first, int tile, double eps) {
+    if (ref.skipped()) return;
+    __shared__ double s_sq[kWaves];
+    __shared__ uint32_t s_bad[kWaves];
+    __shared__ _Float16 block[64][68];
+    const ZS_CONSTANT TileRef& t = ref.tile(first + blockIdx.x);
+    const ZS_CONSTANT MatrixItem& m = ref.item(t.item);
+    const double f = norm_factor(m, ref.ws, eps, s_sq, s_bad);
+    const TileBox box = tile_box(m, t, tile);
+    _Float16* X = reinterpret_cast<_Float16*>(ref.ws + m.x0);
+    const int p = threadIdx.x / 16, q = threadIdx.x % 16 * 4;
+    for (int sub = 0; sub < (tile / 64) * (tile / 64); ++sub) {
+        const int r0 = box.r0 + sub / (tile / 64) * 64, c0 = box.c0 + sub % (tile / 64) * 64;
+        for (int k = p; k < 64; k += 16) {
+            const int r = r0 + k, c = c0 + q;
+            float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            if (r < box.rows && c < box.cols) ld4(m.udt, m.in, (int64_t)r * box.cols + c, box.cols - c, v);
+            h4 h;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) h[e] = r < box.rows && c + e < box.cols ? (_Float16)(float)((double)v[e] * f) : (_Float16)0;
+            if (m.tall) *reinterpret_cast<h4*>(&block[k][q]) = h;
+            else *reinterpret_cast<h4*>(X + (int64_t)r * m.lp + c) = h;
+        }
+        if (!m.tall) continue;
+        __syncthreads();
+        for (int k = p; k < 64; k += 16) {
+            const h4 h = {block[q][k], block[q + 1][k], block[q + 2][k], block[q + 3][k]};
+            *reinterpret_cast<h4*>(X + (int64_t)(c0 + k) * m.lp + r0 + q) = h;
+        }
+        __syncthreads();
+    }
+}
+
+// ---------------------------------------------------------------- products
+
+// 16 bytes per lane from base + offset straight into the LDS: lane l's at lds + 16 l.
+__device__ __forceinline__ void load_lds(const void* base, uint32_t offset, uint32_t lds) {
+    __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                     :
+                     : "s"(lds), "v"(offset), "s"(base)
+                     : "memory");
+}
+
+typedef __attribute__((address_space(3))) char lds_char;
+
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+    return (uint32_t)(uintptr_t)(lds_char*)(char*)p;
+}
+
+__device__ __forceinline__ h8 lds_h8(uint32_t a) { return *(__attribute__((address_space(3))) h8*)(uintptr_t)a; }
+
+// Four values down a column of 4 x 16 blocks (a lane of 16 gives the address of a fourth of a row).
+__device__ __forceinline__ h4 lds_column(uint32_t a) {
+    return __builtin_bit_cast(h4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4*)(uintptr_t)a));
+}
+
+// Operands in the LDS.
+//  rows:    [T][64] of a matrix whose inner dimension is contiguous; the eight
+//           16-byte pieces of row r lie in the order piece ^ (r & 7), so that
+//           eight lanes that read one piece of eight rows meet all banks.
+//  columns: [64][T], the inner dimension down the rows, read through the
+//           transposing load; the 64-byte pieces of row r lie in the order
+//           piece ^ f(r), so that the four rows of a read meet all banks.
+template <int T, int WM, int WN>
+struct Product {
+    static constexpr int kThreads = 64 * WM * WN;
+    static constexpr int kTM = T / WM / 32, kTN = T / WN / 32;      // 32 x 32 results per wave
+    static constexpr int kOperand = T * kDepth * 2;                  // bytes
+    static constexpr int kLoads = kOperand / 1024 / (WM * WN);       // 1 KB each, per wave and operand
+    static constexpr int kLds = 4 * kOperand;                        // two operands, two stages
+
+    __device__ static __forceinline__ int column_swizzle(int r) { return T == 64 ? (r >> 1) & 1 : r & 3; }
+
+    // Where this lane reads its n-th piece of a [T][64] operand, from its first element.
+    __device__ static __forceinline__ uint32_t row_offset(int wave, int lane, int n, int ld) {
+        const int r = (wave * kLoads + n) * 8 + lane / 8;
+        return (uint32_t)r * (uint32_t)ld * 2 + (uint32_t)((lane & 7) ^ (r & 7)) * 16;
+    }
+    // ... of a [64][T] operand
+    __device__ static __forceinline__ uint32_t column_offset(int wave, int lane, int n, int ld) {
+        const int at = (wave * kLoads + n) * 64 + lane, r = at / (T / 8), piece = at % (T / 8);
+        return (uint32_t)r * (uint32_t)ld * 2 + (uint32_t)(((piece >> 2) ^ column_swizzle(r)) * 4 + (piece & 3)) * 16;
+    }
+};
+
+struct NsStep {
+    float a, b, c;
+    int32_t odd;                                   // the iterate is in x1
+    int32_t last;
+};
+
+template <int DT>
+__device__ __forceinline__ void st_ortho(void* out, int64_t e, float v) {
+    global(static_cast<uint16_t*>(out))[e] = (uint16_t)to16<DT>(v);
+}
+
+// One tile of a product.  M runs over the tile's rows for kGram and kPoly and
+// over its columns for kApply, whose result a lane thus holds as four
+// neighbours of a row.
+template <int T, int WM, int WN, int MODE>
+__global__ __launch_bounds__(64 * WM * WN) void ortho_product(NsRef ref, int64_t first, NsStep step) {
+    using P = Product<T, WM, WN>;
+    if (ref.skipped()) return;
+    __shared__ __attribute__((aligned(1024))) char smem[P::kLds];
+    const ZS_CONSTANT TileRef& t = ref.tile(first + blockIdx.x);
+    const ZS_CONSTANT MatrixItem& m = ref.item(t.item);
+    const int ti = t.i, tj = t.j, sp = m.sp, lp = m.lp;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const char* X = ref.ws + (step.odd ? m.x1 : m.x0);
+    char* A = ref.ws + m.a;
+    char* B = ref.ws + m.b;
+
+    // the M operand, the N operand, and how far a stage moves them
+    const char *pm, *pn;
+    int64_t move_m;
+    uint32_t om[P::kLoads], on[P::kLoads];
+    int depth;
+    if (MODE == kGram) {
+        pm = X + (int64_t)ti * T * lp * 2;
+        pn = X + (int64_t)tj * T * lp * 2;
+        move_m = kDepth * 2;
+        depth = lp;
+    } else if (MODE == kPoly) {
+        pm = A + (int64_t)ti * T * sp * 2;
+        pn = A + (int64_t)tj * T * sp * 2;
+        move_m = kDepth * 2;
+        depth = sp;
+    } else {
+        pm = X + (int64_t)tj * T * 2;
+        pn = B + (int64_t)ti * T * sp * 2;
+        move_m = (int64_t)kDepth * lp * 2;
+        depth = sp;
+    }
+#pragma unroll
+    for (int n = 0; n < P::kLoads; ++n) {
+        om[n] = MODE == kApply ? P::column_offset(wave, lane, n, lp) : P::row_offset(wave, lane, n, MODE == kGram ? lp : sp);
+        on[n] = P::row_offset(wave, lane, n, MODE == kGram ? lp : sp);
+    }
+    const uint32_t lds = lds_address(smem);
+    const auto issue = [&](int stage, int k) {
+        const char* bm = pm + k * move_m;
+        const char* bn = pn + (int64_t)k * (kDepth * 2);
+        const uint32_t at = lds + stage * 2 * P::kOperand + wave * P::kLoads * 1024;
+#pragma unroll
+        for (int n = 0; n < P::kLoads; ++n) load_lds(bm, om[n], at + n * 1024);
+#pragma unroll
+        for (int n = 0; n < P::kLoads; ++n) load_lds(bn, on[n], at + P::kOperand + n * 1024);
+    };
+
+    const int wm = wave / WN * (T / WM), wn = wave % WN * (T / WN);
+    f32x16 acc[P::kTM][P::kTN];
+#pragma unroll
+    for (int x = 0; x < P::kTM; ++x)
+#pragma unroll
+        for (int y = 0; y < P::kTN; ++y) acc[x][y] = f32x16{};
+
+    const int stages = depth / kDepth;
+    issue(0, 0);
+    for (int k = 0; k < stages; ++k) {
+        __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
+        if (k + 1 < stages) issue((k + 1) & 1, k + 1);
+        const uint32_t lm = lds + (k & 1) * 2 * P::kOperand, ln = lm + P::kOperand;
+#pragma unroll
+        for (int kk = 0; kk < kDepth / 16; ++kk) {
+            h8 fm[P::kTM], fn[P::kTN];
+#pragma unroll
+            for (int x = 0; x < P::kTM; ++x) {
+                if (MODE == kApply) {
+                    const int r = kk * 16 + (lane >> 5) * 8 + ((lane & 15) >> 2);
+                    const int c = wm + x * 32 + ((lane >> 4) & 1) * 16 + (lane & 3) * 4;
+                    h4 part[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int row = r + 4 * e;
+                        part[e] = lds_column(lm + row * (T * 2) + (((c >> 5) ^ P::column_swizzle(row)) << 6) + (c & 31) * 2);
+                    }
+                    fm[x] = __builtin_shufflevector(part[0], part[1], 0, 1, 2, 3, 4, 5, 6, 7);
+                } else {
+                    const int row = wm + x * 32 + (lane & 31);
+                    fm[x] = lds_h8(lm + row * 128 + (((kk * 2 + (lane >> 5)) ^ (row & 7)) << 4));
+                }
+            }
+#pragma unroll
+            for (int y = 0; y < P::kTN; ++y) {
+                const int row = wn + y * 32 + (lane & 31);
+                fn[y] = lds_h8(ln + row * 128 + (((kk * 2 + (lane >> 5)) ^ (row & 7)) << 4));
+            }
+#pragma unroll
+            for (int x = 0; x < P::kTM; ++x)
+#pragma unroll
+                for (int y = 0; y < P::kTN; ++y)
+                    acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fm[x], fn[y], acc[x][y], 0, 0, 0);
+        }
+    }
+
+    // a lane holds four neighbours along M of one N, for each of four groups
+#pragma unroll
+    for (int x = 0; x < P::kTM; ++x)
+#pragma unroll
+        for (int y = 0; y < P::kTN; ++y)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const int im = wm + x * 32 + g * 8 + (lane >> 5) * 4, in = wn + y * 32 + (lane & 31);
+                float v[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = acc[x][y][g * 4 + e];
+                if (MODE == kApply) {
+                    const int64_t row = (int64_t)ti * T + in, col = (int64_t)tj * T + im;
+                    const h4 old = *reinterpret_cast<const h4*>(X + (row * lp + col) * 2);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[e] = fmaf(step.a, (float)old[e], ldexpf(v[e], -kLog2A));
+                    if (!step.last) {
+                        h4 h;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) h[e] = (_Float16)v[e];
+                        *reinterpret_cast<h4*>(ref.ws + (step.odd ? m.x0 : m.x1) + (row * lp + col) * 2) = h;
+                    } else if (row < m.s) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            if (col + e >= m.l) break;
+                            const int64_t at = m.tall ? (col + e) * m.s + row : row * m.l + col + e;
+                            const float o = ldexpf(v[e], -m.log2_scale);
+                            if (m.odt == ZERO_F16) st_ortho<ZERO_F16>(m.out, at, o);
+                            else st_ortho<ZERO_BF16>(m.out, at, o);
+                        }
+                    }
+                } else {
+                    const int64_t r = (int64_t)ti * T + im, c = (int64_t)tj * T + in;      // symmetric: [c][r .. r + 3] too
+                    h4 h;
+                    if (MODE == kGram) {
+                        const int shift = kLog2A - 2 * m.log2_scale;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) h[e] = (_Float16)ldexpf(v[e], shift);
+                    } else {
+                        const h4 old = *reinterpret_cast<const h4*>(A + (c * sp + r) * 2);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) h[e] = (_Float16)fmaf(step.b, (float)old[e], step.c * ldexpf(v[e], -kLog2A));
+                    }
+                    _Float16* out = reinterpret_cast<_Float16*>(MODE == kGram ? A : B);
+                    *reinterpret_cast<h4*>(out + c * sp + r) = h;
+                    if (ti != tj) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) out[(r + e) * sp + c] = h[e];
+                    }
+                }
+            }
+}
+
+// ---------------------------------------------------------------- host side
+
+int64_t pad_to(int64_t x, int64_t t) { return (x + t - 1) / t * t; }
+int64_t pad256(int64_t x) { return pad_to(x, 256); }
+
+int tile_of(int64_t s) { return s >= 1024 ? 256 : s > 256 ? 128 : 64; }
+
+// Blocks go to the eight XCDs in turn: the list is dealt out so that each XCD
+// takes a run of it, whose tiles share their operands in one L2.
+void deal_out(std::vector<TileRef>& tiles, size_t first) {
+    const std::vector<TileRef> run(tiles.begin() + first, tiles.end());
+    const size_t n = run.size();
+    size_t start = 0;
+    for (size_t xcd = 0; xcd < 8; ++xcd)
+        for (size_t b = xcd; b < n; b += 8) tiles[first + b] = run[start++];
+}
+
+int64_t place(int64_t* at, int64_t bytes) {
+    const int64_t here = *at;
+    *at += pad256(bytes);
+    return here;
+}
+
+template <int MODE>
+int launch_product(const OrthoPass& p, const NsRef& ref, const NsStep& step, hipStream_t s) {
+    const int64_t first = MODE == kApply ? p.x_first : p.sym_first, n = MODE == kApply ? p.n_x : p.n_sym;
+    if (p.tile == 256)
+        hipLaunchKernelGGL((ortho_product<256, 2, 4, MODE>), dim3((unsigned)n), dim3(512), 0, s, ref, first, step);
+    else if (p.tile == 128)
+        hipLaunchKernelGGL((ortho_product<128, 2, 2, MODE>), dim3((unsigned)n), dim3(256), 0, s, ref, first, step);
+    else
+        hipLaunchKernelGGL((ortho_product<64, 2, 2, MODE>), dim3((unsigned)n), dim3(256), 0, s, ref, first, step);
+    return launch_status("ortho_product");
+}
+
+// The singular values start in [0, 1].  What each step makes of the largest
+// interval they can be in has to stay within what fp16 holds of X, A and B at
+// their scales, with room for single entries.
+int check_coefs(const double* coefs, int32_t n_steps) {
+    if (coefs == nullptr) return fail(ZERO_EINVAL, "coefs is NULL");
+    if (n_steps < 1 || n_steps > ZERO_MAX_ORTHO_STEPS)
+        return fail(ZERO_EINVAL, "n_steps must lie in [1, %d] (got %d)", ZERO_MAX_ORTHO_STEPS, n_steps);
+    double top = 1.0;
+    for (int k = 0; k < n_steps; ++k) {
+        const double a = coefs[3 * k], b = coefs[3 * k + 1], c = coefs[3 * k + 2];
+        if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c)) return fail(ZERO_EINVAL, "coefs must be finite");
+        double next = 0.0, poly = 0.0;
+        for (int i = 0; i <= 4096; ++i) {
+            const double x = top * i / 4096, y = x * x;
+            poly = std::max(poly, std::fabs(y * (b + c * y)));
+            next = std::max(next, std::fabs(x * (a + y * (b + c * y))));
+        }
+        if (poly > 32.0 || next > 4.0)
+            return fail(ZERO_ERANGE, "step %d takes singular values of [0, 1] to %g (at most 4), its polynomial to %g (at most 32)",
+                        k, next, poly);
+        top = next;
+    }
+    return ZERO_OK;
+}
+
+}  // namespace
+
+int plan_ortho(const std::vector<OrthoMatrix>& matrices, OrthoPlan* plan) {
+    for (const int tile : {256, 128, 64}) {
+        std::vector<size_t> mine;
+        for (size_t k = 0; k < matrices.size(); ++k)
+            if (tile_of(std::min(matrices[k].rows, matrices[k].cols)) == tile) mine.push_back(k);
+        for (size_t done = 0; done < mine.size();) {
+            OrthoPass pass{};
+            pass.tile = tile;
+            int64_t at = 0;
+            const size_t first_item = plan->items.size();
+            for (; done < mine.size(); ++done) {
+                const OrthoMatrix& m = matrices[mine[done]];
+                MatrixItem it{};
+                it.in = m.in;
+                it.out = m.out;
+                it.tall = m.rows > m.cols;
+                it.s = (int32_t)std::min(m.rows, m.cols);
+                it.l = (int32_t)std::max(m.rows, m.cols);
+                it.sp = (int32_t)pad_to(it.s, tile);
+                it.lp = (int32_t)pad_to(it.l, tile);
+                it.udt = m.udt;
+                it.odt = m.odt;
+                while (it.log2_scale < 12 && (int64_t(4) << (2 * it.log2_scale)) <= it.l) ++it.log2_scale;
+                const int64_t n_tiles = (int64_t)(it.sp / tile) * (it.lp / tile);
+                if (n_tiles > INT32_MAX) return fail(ZERO_ERANGE, "a matrix of %d x %d is too large", it.s, it.l);
+                it.n_slots = (int32_t)n_tiles;
+                const int64_t x = (int64_t)it.sp * it.lp * 2, a = (int64_t)it.sp * it.sp * 2;
+                if (plan->items.size() > first_item && at + 2 * (x + a) > kPassBytes) break;
+                it.x0 = place(&at, x);
+                it.x1 = place(&at, x);
+                it.a = place(&at, a);
+                it.b = place(&at, a);
+                it.slots = place(&at, n_tiles * 8);
+                plan->items.push_back(it);
+            }
+            plan->workspace = std::max(plan->workspace, at);
+            pass.n_items = (int32_t)(plan->items.size() - first_item);
+            // four tile rows at a time, column by column
+            constexpr int kBand = 4;
+            pass.sym_first = (int64_t)plan->tiles.size();
+            for (size_t k = first_item; k < plan->items.size(); ++k) {
+                const int n = plan->items[k].sp / tile;
+                for (int i0 = 0; i0 < n; i0 += kBand)
+                    for (int j = 0; j < std::min(i0 + kBand, n); ++j)
+                        for (int i = std::max(i0, j); i < std::min(i0 + kBand, n); ++i)
+                            plan->tiles.push_back({(uint32_t)k, (uint16_t)i, (uint16_t)j});
+            }
+            pass.n_sym = (int64_t)plan->tiles.size() - pass.sym_first;
+            deal_out(plan->tiles, (size_t)pass.sym_first);
+            pass.x_first = (int64_t)plan->tiles.size();
+            for (size_t k = first_item; k < plan->items.size(); ++k) {
+                const int n = plan->items[k].sp / tile, nl = plan->items[k].lp / tile;
+                for (int i0 = 0; i0 < n; i0 += kBand)
+                    for (int j = 0; j < nl; ++j)
+                        for (int i = i0; i < std::min(i0 + kBand, n); ++i)
+                            plan->tiles.push_back({(uint32_t)k, (uint16_t)i, (uint16_t)j});
+            }
+            pass.n_x = (int64_t)plan->tiles.size() - pass.x_first;
+            deal_out(plan->tiles, (size_t)pass.x_first);
+            if (std::max(pass.n_x, pass.n_sym) > INT32_MAX) return fail(ZERO_ERANGE, "the list is too long");
+            plan->passes.push_back(pass);
+        }
+    }
+    return ZERO_OK;
+}
+
+}  // namespace zero_shard
+
+using namespace zero_shard;
+
+extern "C" {
+
+size_t zero_multi_orthogonalize_workspace_bytes(const void* table) {
+    clear_error();
+    MatrixHeader h;
+    if (table == nullptr) return 0;
+    std::memcpy(&h, table, sizeof(h));
+    return h.magic == kMatrixMagic ? (size_t)h.workspace_bytes : 0;
+}
+
+int zero_multi_orthogonalize(const void* table, const void* d_table, const double* coefs, int32_t n_steps, double eps,
+                             const int32_t* d_global_overflow, void* d_workspace, size_t workspace_bytes,
+                             void* hip_stream) {
+    clear_error();
+    MatrixHeader h;
+    int rc = read_matrix_table(table, d_table, kCanOrtho, "the orthogonalisation (update, ortho)", &h);
+    if (rc == ZERO_OK) rc = check_coefs(coefs, n_steps);
+    if (rc != ZERO_OK) return rc;
+    if (!(eps >= 0.0) || !std::isfinite(eps)) return fail(ZERO_EINVAL, "eps must be finite and >= 0");
+    if ((uintptr_t)d_global_overflow & 3u) return fail(ZERO_EALIGN, "d_global_overflow misaligned");
+    if (h.n_entries == 0) return ZERO_OK;
+    if (d_workspace == nullptr) return fail(ZERO_EINVAL, "d_workspace is NULL");
+    if ((uintptr_t)d_workspace & 255u) return fail(ZERO_EALIGN, "d_workspace must be 256-byte aligned");
+    if (workspace_bytes < (size_t)h.workspace_bytes)
+        return fail(ZERO_ENOSPC, "workspace %zu bytes, need %lld", workspace_bytes, (long long)h.workspace_bytes);
+    if (matrix_touched(table, h, d_workspace, h.workspace_bytes) ||
+        overlaps(d_workspace, h.workspace_bytes, d_table, h.device_bytes) ||
+        (d_global_overflow && overlaps(d_workspace, h.workspace_bytes, d_global_overflow, sizeof(int32_t))))
+        return fail(ZERO_EINVAL, "the workspace overlaps a buffer of the list, the table or the flag");
+    if (matrix_written(table, h, d_global_overflow, sizeof(int32_t)))
+        return fail(ZERO_EINVAL, "the flag lies in a buffer the call writes");
+    const hipStream_t s = static_cast<hipStream_t>(hip_stream);
+    const NsRef ref{at<MatrixItem>(d_table, h.items_at), at<TileRef>(d_table, h.tiles_at), static_cast<char*>(d_workspace),
+                    d_global_overflow};
+    const OrthoPass* passes = at<OrthoPass>(table, h.passes_at);
+    for (int p = 0; p < h.n_passes; ++p) {
+        const OrthoPass& pass = passes[p];
+        hipLaunchKernelGGL(ortho_squares, dim3((unsigned)pass.n_x), dim3(kBlock), 0, s, ref, pass.x_first, pass.tile);
+        rc = launch_status("ortho_squares");
+        if (rc != ZERO_OK) return rc;
+        hipLaunchKernelGGL(ortho_load, dim3((unsigned)pass.n_x), dim3(kBlock), 0, s, ref, pass.x_first, pass.tile, eps);
+        rc = launch_status("ortho_load");
+        for (int k = 0; k < n_steps && rc == ZERO_OK; ++k) {
+            const NsStep step{(float)coefs[3 * k], (float)coefs[3 * k + 1], (float)coefs[3 * k + 2], k & 1, k + 1 == n_steps};
+            rc = launch_product<kGram>(pass, ref, step, s);
+            if (rc == ZERO_OK) rc = launch_product<kPoly>(pass, ref, step, s);
+            if (rc == ZERO_OK) rc = launch_product<kApply>(pass, ref, step, s);
+        }
+        if (rc != ZERO_OK) return rc;
+    }
+    return ZERO_OK;
+}
+
+}  // extern "C"

@@ -121,25 +121,33 @@ class TensorTable:
             if self.groups is not None:
                 t.group = int(self.groups[i])
 
+    _builder = "zero_multi_table_build"
+
+    def _describe_grads(self, grads) -> None:
+        for i, (g, n) in enumerate(zip(grads, self._numels)):
+            t = self._c[i]
+            t.grad, t.numel, t.grad_dtype = _buf(g, None, 0, f"grads[{i}]", self._index, n), n, dtype_code(g)
+
+    def _write(self, where, capacity: int, size, dev_size) -> int:
+        """The table's bytes at `where`, and its sizes."""
+        return _L.lib().zero_multi_table_build(self._c, self.n_tensors, self.state_bits, where, capacity,
+                                               ctypes.byref(size), ctypes.byref(dev_size))
+
     def _build(self, grads, key) -> None:
         """The table for these gradients, the rest of the list being described."""
-        arr, bits, index = self._c, self.state_bits, self._index
-        for i, (g, n) in enumerate(zip(grads, self._numels)):
-            t = arr[i]
-            t.grad, t.numel, t.grad_dtype = _buf(g, None, 0, f"grads[{i}]", index, n), n, dtype_code(g)
+        index = self._index
+        self._describe_grads(grads)
         size, dev_size = ctypes.c_size_t(), ctypes.c_size_t()
-        build = _L.lib().zero_multi_table_build
-        st = build(arr, self.n_tensors, bits, None, 0, ctypes.byref(size), ctypes.byref(dev_size))
+        st = self._write(None, 0, size, dev_size)
         if st != _L.ZERO_ENOSPC:
-            _L.check(st, "zero_multi_table_build")
+            _L.check(st, self._builder)
         on_gpu = index >= 0
         if on_gpu and torch.cuda.is_current_stream_capturing():
             raise RuntimeError("a table cannot be built while its stream records a graph")
         # pinned: the copy to the device needs no wait, and torch's host allocator
         # hands the memory out again only after the copy has run
         host = torch.empty(size.value, dtype=torch.uint8, pin_memory=on_gpu)
-        _L.check(build(arr, self.n_tensors, bits, host.data_ptr(), size.value, ctypes.byref(size),
-                       ctypes.byref(dev_size)), "zero_multi_table_build")
+        _L.check(self._write(host.data_ptr(), size.value, size, dev_size), self._builder)
         self.grads, self.host = list(grads), host
         self._grad_key = key
         self.device = host[:dev_size.value].to(torch.device("cuda", index), non_blocking=True) if on_gpu else None
