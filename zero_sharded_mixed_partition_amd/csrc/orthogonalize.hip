@@ -20,6 +20,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cmath>
+#include <type_traits>
 #include <vector>
 
 #include "matrix_table.h"
@@ -30,10 +31,9 @@ namespace {
 typedef _Float16 h8 __attribute__((ext_vector_type(8)));
 typedef _Float16 h4 __attribute__((ext_vector_type(4)));
 typedef short s4 __attribute__((ext_vector_type(4)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr int kLog2A = 10;                       // A and B are held times 2^10
-constexpr int kDepth = 64;                       // elements of the inner dimension per stage
+constexpr int kPanel = 32;                       // columns of a panel, and the inner elements of a stage
 constexpr int64_t kPassBytes = int64_t(2) << 30; // workspace of a pass, if it holds more than one matrix
 
 enum { kGram, kPoly, kApply };
@@ -71,6 +71,13 @@ __device__ __forceinline__ void ld4(int dt, const void* U, int64_t e, int valid,
     if (dt == ZERO_F16) ld4<ZERO_F16>(U, e, valid, v);
     else if (dt == ZERO_BF16) ld4<ZERO_BF16>(U, e, valid, v);
     else ld4<ZERO_F32>(U, e, valid, v);
+}
+
+// Where element (r, c) of a matrix of `rows` rows is in the workspace: panels
+// of 32 columns, each with its rows end to end.  A stage of either operand of
+// any product is then made of runs of at least 1 KB.
+__device__ __forceinline__ int64_t panel_at(int64_t r, int64_t c, int64_t rows) {
+    return ((c / kPanel) * rows + r) * kPanel + c % kPanel;
 }
 
 // The caller's rows and columns of a tile of the iterate.
@@ -143,13 +150,13 @@ __global__ __launch_bounds__(kBlock) void ortho_load(NsRef ref, int64_t first, i
 #pragma unroll
             for (int e = 0; e < 4; ++e) h[e] = r < box.rows && c + e < box.cols ? (_Float16)(float)((double)v[e] * f) : (_Float16)0;
             if (m.tall) *reinterpret_cast<h4*>(&block[k][q]) = h;
-            else *reinterpret_cast<h4*>(X + (int64_t)r * m.lp + c) = h;
+            else *reinterpret_cast<h4*>(X + panel_at(r, c, m.sp)) = h;
         }
         if (!m.tall) continue;
         __syncthreads();
         for (int k = p; k < 64; k += 16) {
             const h4 h = {block[q][k], block[q + 1][k], block[q + 2][k], block[q + 3][k]};
-            *reinterpret_cast<h4*>(X + (int64_t)(c0 + k) * m.lp + r0 + q) = h;
+            *reinterpret_cast<h4*>(X + panel_at(c0 + k, r0 + q, m.sp)) = h;
         }
         __syncthreads();
     }
@@ -178,32 +185,51 @@ __device__ __forceinline__ h4 lds_column(uint32_t a) {
     return __builtin_bit_cast(h4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4*)(uintptr_t)a));
 }
 
-// Operands in the LDS.
-//  rows:    [T][64] of a matrix whose inner dimension is contiguous; the eight
-//           16-byte pieces of row r lie in the order piece ^ (r & 7), so that
-//           eight lanes that read one piece of eight rows meet all banks.
-//  columns: [64][T], the inner dimension down the rows, read through the
-//           transposing load; the 64-byte pieces of row r lie in the order
-//           piece ^ f(r), so that the four rows of a read meet all banks.
+// A wave's share of a T x T tile of a product, WM x WN waves.
+//
+// A stage is 32 inner elements of both operands, 64 bytes a row: 16 rows for
+// each 1 KB that a wave loads at a time, straight into the LDS.  S stages lie
+// there; S - 2 are on their way while one is multiplied, since a load that
+// misses the L2 takes longer than a stage.  One barrier a stage: behind it the
+// next stage has landed for all waves, and the last one's place is free.
+//
+// Operands in the LDS, as the 16 x 16 x 32 MFMA takes them (lane l: row or
+// column l % 16, inner elements 8 (l / 16) .. + 7):
+//  rows:     of a matrix whose inner dimension runs along the panel's columns.
+//            The 16-byte pieces of row r lie in the order piece ^ (r / 4) % 4,
+//            so that 16 lanes which read one piece of 16 rows meet all 64 banks.
+//  columns:  the inner dimension runs down the panel's rows, read through the
+//            transposing load: 16 lanes take 4 rows of 16 elements.  The 32-byte
+//            halves of rows 8 to 15 of 16 are swapped, so that the two groups
+//            of rows that a half wave reads meet all banks.
 template <int T, int WM, int WN>
 struct Product {
-    static constexpr int kThreads = 64 * WM * WN;
-    static constexpr int kTM = T / WM / 32, kTN = T / WN / 32;      // 32 x 32 results per wave
-    static constexpr int kOperand = T * kDepth * 2;                  // bytes
-    static constexpr int kLoads = kOperand / 1024 / (WM * WN);       // 1 KB each, per wave and operand
-    static constexpr int kLds = 4 * kOperand;                        // two operands, two stages
+    static constexpr int kWaves = WM * WN;
+    static constexpr int kUM = T / WM / 16, kUN = T / WN / 16;       // 16 x 16 results per wave
+    static constexpr int kOperand = T * kPanel * 2;                  // bytes of a stage
+    static constexpr int kLoads = kOperand / 1024 / kWaves;          // per wave and operand
+    static constexpr int kStages = 5;
+    static constexpr int kStage = 2 * kOperand;
+    static_assert(kLoads >= 1 && kStages * kStage <= 160 * 1024, "stages do not fit the LDS");
 
-    __device__ static __forceinline__ int column_swizzle(int r) { return T == 64 ? (r >> 1) & 1 : r & 3; }
-
-    // Where this lane reads its n-th piece of a [T][64] operand, from its first element.
-    __device__ static __forceinline__ uint32_t row_offset(int wave, int lane, int n, int ld) {
-        const int r = (wave * kLoads + n) * 8 + lane / 8;
-        return (uint32_t)r * (uint32_t)ld * 2 + (uint32_t)((lane & 7) ^ (r & 7)) * 16;
+    // Where this lane reads its n-th piece of an operand of rows, from the first.
+    __device__ static __forceinline__ uint32_t row_offset(int wave, int lane, int n) {
+        const int r = (wave * kLoads + n) * 16 + lane / 4;
+        return (uint32_t)(r * 64 + ((lane & 3) ^ ((r >> 2) & 3)) * 16);
     }
-    // ... of a [64][T] operand
-    __device__ static __forceinline__ uint32_t column_offset(int wave, int lane, int n, int ld) {
-        const int at = (wave * kLoads + n) * 64 + lane, r = at / (T / 8), piece = at % (T / 8);
-        return (uint32_t)r * (uint32_t)ld * 2 + (uint32_t)(((piece >> 2) ^ column_swizzle(r)) * 4 + (piece & 3)) * 16;
+    // ... of an operand of columns: T / 32 panels of 32 rows, panel_bytes apart
+    __device__ static __forceinline__ int64_t column_offset(int wave, int lane, int n, int64_t panel_bytes) {
+        const int k = wave * kLoads + n, r = (k & 1) * 16 + lane / 4;
+        return (k >> 1) * panel_bytes + r * 64 + ((lane & 3) ^ ((r >> 2) & 2)) * 16;
+    }
+    // Where it finds its part of rows 0 .. 15, or of columns 0 .. 15, in the LDS.
+    __device__ static __forceinline__ uint32_t row_read(int lane, int first) {
+        const int r = first + (lane & 15);
+        return (uint32_t)(r * 64 + (((lane >> 4) ^ (r >> 2)) & 3) * 16);
+    }
+    __device__ static __forceinline__ uint32_t column_read(int lane, int first) {
+        const int r = (lane >> 4) * 8 + ((lane & 15) >> 2), half = (first >> 4) & 1;
+        return (uint32_t)((first / kPanel) * 2048 + r * 64 + (half ^ ((r >> 3) & 1)) * 32 + (lane & 3) * 8);
     }
 };
 
@@ -218,157 +244,195 @@ __device__ __forceinline__ void st_ortho(void* out, int64_t e, float v) {
     global(static_cast<uint16_t*>(out))[e] = (uint16_t)to16<DT>(v);
 }
 
+// Waits until no more than N of this wave's loads are on their way, then for the other waves.
+template <int N>
+__device__ __forceinline__ void wait_stage() {
+    __asm__ volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
 // One tile of a product.  M runs over the tile's rows for kGram and kPoly and
-// over its columns for kApply, whose result a lane thus holds as four
-// neighbours of a row.
+// over its columns for kApply, so that a lane ends with four neighbours of a
+// stored row: rows of X for kApply, of the transposed tile for the others.
 template <int T, int WM, int WN, int MODE>
 __global__ __launch_bounds__(64 * WM * WN) void ortho_product(NsRef ref, int64_t first, NsStep step) {
     using P = Product<T, WM, WN>;
+    constexpr int UM = P::kUM, UN = P::kUN, L = P::kLoads, S = P::kStages, NL = 2 * L;
     if (ref.skipped()) return;
-    __shared__ __attribute__((aligned(1024))) char smem[P::kLds];
+    __shared__ __attribute__((aligned(1024))) char smem[S * P::kStage];
     const ZS_CONSTANT TileRef& t = ref.tile(first + blockIdx.x);
     const ZS_CONSTANT MatrixItem& m = ref.item(t.item);
-    const int ti = t.i, tj = t.j, sp = m.sp, lp = m.lp;
+    const int ti = t.i, tj = t.j;
+    const int64_t sp = m.sp;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int wm = wave / WN * (T / WM), wn = wave % WN * (T / WN);
     const char* X = ref.ws + (step.odd ? m.x1 : m.x0);
     char* A = ref.ws + m.a;
     char* B = ref.ws + m.b;
 
-    // the M operand, the N operand, and how far a stage moves them
+    // the M operand, the N operand, and how far a stage moves the first
     const char *pm, *pn;
-    int64_t move_m;
-    uint32_t om[P::kLoads], on[P::kLoads];
-    int depth;
-    if (MODE == kGram) {
-        pm = X + (int64_t)ti * T * lp * 2;
-        pn = X + (int64_t)tj * T * lp * 2;
-        move_m = kDepth * 2;
-        depth = lp;
-    } else if (MODE == kPoly) {
-        pm = A + (int64_t)ti * T * sp * 2;
-        pn = A + (int64_t)tj * T * sp * 2;
-        move_m = kDepth * 2;
-        depth = sp;
+    int64_t move_m = sp * 64;
+    const int64_t move_n = sp * 64;
+    int n;
+    if constexpr (MODE == kApply) {
+        pm = X + (int64_t)tj * (T / kPanel) * sp * 64;
+        pn = B + ti * (T * 64);
+        move_m = kPanel * 64;
+        n = m.sp / kPanel;
     } else {
-        pm = X + (int64_t)tj * T * 2;
-        pn = B + (int64_t)ti * T * sp * 2;
-        move_m = (int64_t)kDepth * lp * 2;
-        depth = sp;
+        const char* from = MODE == kGram ? X : A;
+        pm = from + ti * (T * 64);
+        pn = from + tj * (T * 64);
+        n = (MODE == kGram ? m.lp : m.sp) / kPanel;
     }
+    uint32_t on[L];
+    const char* cm[MODE == kApply ? L : 1];
 #pragma unroll
-    for (int n = 0; n < P::kLoads; ++n) {
-        om[n] = MODE == kApply ? P::column_offset(wave, lane, n, lp) : P::row_offset(wave, lane, n, MODE == kGram ? lp : sp);
-        on[n] = P::row_offset(wave, lane, n, MODE == kGram ? lp : sp);
+    for (int q = 0; q < L; ++q) {
+        on[q] = P::row_offset(wave, lane, q);
+        if constexpr (MODE == kApply) cm[q] = pm + P::column_offset(wave, 0, q, sp * 64);
     }
-    const uint32_t lds = lds_address(smem);
-    const auto issue = [&](int stage, int k) {
-        const char* bm = pm + k * move_m;
-        const char* bn = pn + (int64_t)k * (kDepth * 2);
-        const uint32_t at = lds + stage * 2 * P::kOperand + wave * P::kLoads * 1024;
+    // the lane's part of the column offset is the same for all pieces: rows of 16 from an even or an odd half
+    uint32_t oc[MODE == kApply ? L : 1];
+    if constexpr (MODE == kApply) {
 #pragma unroll
-        for (int n = 0; n < P::kLoads; ++n) load_lds(bm, om[n], at + n * 1024);
+        for (int q = 0; q < L; ++q)
+            oc[q] = (uint32_t)(P::column_offset(wave, lane, q, 0) - P::column_offset(wave, 0, q, 0));
+    }
+    const uint32_t lds = lds_address(smem), mine = lds + wave * L * 1024;
+    uint32_t put = 0;
+    int left = n;
+    const auto load = [&](int q) {                 // the q-th load of a stage
+        if (q < L) {
+            if constexpr (MODE == kApply) load_lds(cm[q], oc[q], mine + put + q * 1024);
+            else load_lds(pm, on[q], mine + put + q * 1024);
+        } else {
+            load_lds(pn, on[q - L], mine + put + P::kOperand + (q - L) * 1024);
+        }
+        if (q == NL - 1) {
+            const bool more = --left > 0;
+            if constexpr (MODE == kApply) {
 #pragma unroll
-        for (int n = 0; n < P::kLoads; ++n) load_lds(bn, on[n], at + P::kOperand + n * 1024);
+                for (int k = 0; k < L; ++k) cm[k] += more ? move_m : 0;
+            } else {
+                pm += more ? move_m : 0;
+            }
+            pn += more ? move_n : 0;
+            put = put == (S - 1) * P::kStage ? 0 : put + P::kStage;
+        }
     };
 
-    const int wm = wave / WN * (T / WM), wn = wave % WN * (T / WN);
-    f32x16 acc[P::kTM][P::kTN];
+    f32x4 acc[UM][UN];
 #pragma unroll
-    for (int x = 0; x < P::kTM; ++x)
+    for (int x = 0; x < UM; ++x)
 #pragma unroll
-        for (int y = 0; y < P::kTN; ++y) acc[x][y] = f32x16{};
-
-    const int stages = depth / kDepth;
-    issue(0, 0);
-    for (int k = 0; k < stages; ++k) {
-        __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        __syncthreads();
-        if (k + 1 < stages) issue((k + 1) & 1, k + 1);
-        const uint32_t lm = lds + (k & 1) * 2 * P::kOperand, ln = lm + P::kOperand;
-#pragma unroll
-        for (int kk = 0; kk < kDepth / 16; ++kk) {
-            h8 fm[P::kTM], fn[P::kTN];
-#pragma unroll
-            for (int x = 0; x < P::kTM; ++x) {
-                if (MODE == kApply) {
-                    const int r = kk * 16 + (lane >> 5) * 8 + ((lane & 15) >> 2);
-                    const int c = wm + x * 32 + ((lane >> 4) & 1) * 16 + (lane & 3) * 4;
-                    h4 part[2];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int row = r + 4 * e;
-                        part[e] = lds_column(lm + row * (T * 2) + (((c >> 5) ^ P::column_swizzle(row)) << 6) + (c & 31) * 2);
-                    }
-                    fm[x] = __builtin_shufflevector(part[0], part[1], 0, 1, 2, 3, 4, 5, 6, 7);
-                } else {
-                    const int row = wm + x * 32 + (lane & 31);
-                    fm[x] = lds_h8(lm + row * 128 + (((kk * 2 + (lane >> 5)) ^ (row & 7)) << 4));
-                }
-            }
-#pragma unroll
-            for (int y = 0; y < P::kTN; ++y) {
-                const int row = wn + y * 32 + (lane & 31);
-                fn[y] = lds_h8(ln + row * 128 + (((kk * 2 + (lane >> 5)) ^ (row & 7)) << 4));
-            }
-#pragma unroll
-            for (int x = 0; x < P::kTM; ++x)
-#pragma unroll
-                for (int y = 0; y < P::kTN; ++y)
-                    acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fm[x], fn[y], acc[x][y], 0, 0, 0);
+        for (int y = 0; y < UN; ++y) acc[x][y] = f32x4{};
+    h8 fm[UM], fn[2][UN];
+    const uint32_t an = lds + P::kOperand + P::row_read(lane, wn);
+    const uint32_t am = lds + (MODE == kApply ? 0u : P::row_read(lane, wm));
+    // columns: 16 of a panel's 32 at a time; the two halves lie 32 bytes apart, either way round
+    const uint32_t ac0 = lds + P::column_read(lane, wm), ac1 = lds + P::column_read(lane, wm + 16);
+    const auto read_m = [&](uint32_t stage, int x) {
+        if constexpr (MODE == kApply) {
+            const uint32_t a = (x & 1 ? ac1 : ac0) + stage + (x >> 1) * 2048;
+            return __builtin_shufflevector(lds_column(a), lds_column(a + 4 * 64), 0, 1, 2, 3, 4, 5, 6, 7);
+        } else {
+            return lds_h8(am + stage + x * 1024);
         }
-    }
+    };
 
-    // a lane holds four neighbours along M of one N, for each of four groups
+    // Loads past the last stage read it again, into places that nothing reads any
+    // more: the loop has no other end to it, and its waits are constants.
+    for (int k = 0; k < S - 1; ++k)
 #pragma unroll
-    for (int x = 0; x < P::kTM; ++x)
+        for (int q = 0; q < NL; ++q) load(q);
+    wait_stage<(S - 2) * NL>();
 #pragma unroll
-        for (int y = 0; y < P::kTN; ++y)
+    for (int y = 0; y < UN; ++y) fn[0][y] = lds_h8(an + y * 1024);
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const int im = wm + x * 32 + g * 8 + (lane >> 5) * 4, in = wn + y * 32 + (lane & 31);
-                float v[4];
+    for (int x = 0; x < UM; ++x) fm[x] = read_m(0, x);
+    uint32_t next = P::kStage;
+    // One stage's products.  Between them, in this order, the loads of the stage
+    // S - 1 ahead and the reads of the next one: a row of M is read as soon as
+    // its products are issued, N into the other half of fn.
+    const auto multiply = [&](auto half) {
+        constexpr int p = decltype(half)::value;
+        constexpr int kSlots = UM * UN;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = acc[x][y][g * 4 + e];
-                if (MODE == kApply) {
-                    const int64_t row = (int64_t)ti * T + in, col = (int64_t)tj * T + im;
-                    const h4 old = *reinterpret_cast<const h4*>(X + (row * lp + col) * 2);
+        for (int x = 0; x < UM; ++x) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) v[e] = fmaf(step.a, (float)old[e], ldexpf(v[e], -kLog2A));
-                    if (!step.last) {
-                        h4 h;
+            for (int y = 0; y < UN; ++y) {
+                acc[x][y] = __builtin_amdgcn_mfma_f32_16x16x32_f16(fm[x], fn[p][y], acc[x][y], 0, 0, 0);
+                const int slot = x * UN + y;
+                const int q = slot * NL / kSlots;
+                if (q < (slot + 1) * NL / kSlots) load(q);
+                const int k = slot * UN / kSlots;
+                if (k < (slot + 1) * UN / kSlots) fn[1 - p][k] = lds_h8(an + next + k * 1024);
+                if (y == UN - 1) fm[x] = read_m(next, x);
+                if (slot & 1) __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+        next = next == (S - 1) * P::kStage ? 0 : next + P::kStage;
+    };
+    for (int k = 0; k < n; k += 2) {
+        wait_stage<(S - 3) * NL>();
+        multiply(std::integral_constant<int, 0>{});
+        wait_stage<(S - 3) * NL>();
+        multiply(std::integral_constant<int, 1>{});
+    }
+    wait_stage<0>();                               // nothing may land once the LDS is another workgroup's
+
+    // a lane holds four neighbours along M of one N
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) h[e] = (_Float16)v[e];
-                        *reinterpret_cast<h4*>(ref.ws + (step.odd ? m.x0 : m.x1) + (row * lp + col) * 2) = h;
-                    } else if (row < m.s) {
+    for (int x = 0; x < UM; ++x)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            if (col + e >= m.l) break;
-                            const int64_t at = m.tall ? (col + e) * m.s + row : row * m.l + col + e;
-                            const float o = ldexpf(v[e], -m.log2_scale);
-                            if (m.odt == ZERO_F16) st_ortho<ZERO_F16>(m.out, at, o);
-                            else st_ortho<ZERO_BF16>(m.out, at, o);
-                        }
-                    }
-                } else {
-                    const int64_t r = (int64_t)ti * T + im, c = (int64_t)tj * T + in;      // symmetric: [c][r .. r + 3] too
+        for (int y = 0; y < UN; ++y) {
+            const int im = wm + x * 16 + (lane >> 4) * 4, in = wn + y * 16 + (lane & 15);
+            float v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = acc[x][y][e];
+            if constexpr (MODE == kApply) {
+                const int64_t row = (int64_t)ti * T + in, col = (int64_t)tj * T + im, at = panel_at(row, col, sp);
+                const h4 old = *reinterpret_cast<const h4*>(X + at * 2);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = fmaf(step.a, (float)old[e], ldexpf(v[e], -kLog2A));
+                if (!step.last) {
                     h4 h;
-                    if (MODE == kGram) {
-                        const int shift = kLog2A - 2 * m.log2_scale;
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) h[e] = (_Float16)ldexpf(v[e], shift);
-                    } else {
-                        const h4 old = *reinterpret_cast<const h4*>(A + (c * sp + r) * 2);
+                    for (int e = 0; e < 4; ++e) h[e] = (_Float16)v[e];
+                    *reinterpret_cast<h4*>(ref.ws + (step.odd ? m.x0 : m.x1) + at * 2) = h;
+                } else if (row < m.s) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) h[e] = (_Float16)fmaf(step.b, (float)old[e], step.c * ldexpf(v[e], -kLog2A));
-                    }
-                    _Float16* out = reinterpret_cast<_Float16*>(MODE == kGram ? A : B);
-                    *reinterpret_cast<h4*>(out + c * sp + r) = h;
-                    if (ti != tj) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) out[(r + e) * sp + c] = h[e];
+                    for (int e = 0; e < 4; ++e) {
+                        if (col + e >= m.l) break;
+                        const int64_t to = m.tall ? (col + e) * m.s + row : row * m.l + col + e;
+                        const float o = ldexpf(v[e], -m.log2_scale);
+                        if (m.odt == ZERO_F16) st_ortho<ZERO_F16>(m.out, to, o);
+                        else st_ortho<ZERO_BF16>(m.out, to, o);
                     }
                 }
+            } else {
+                // symmetric: (c, r .. r + 3) is what the lane holds, (r .. r + 3, c) its mirror
+                const int64_t r = (int64_t)ti * T + im, c = (int64_t)tj * T + in, at = panel_at(c, r, sp);
+                h4 h;
+                if constexpr (MODE == kGram) {
+                    const int shift = kLog2A - 2 * m.log2_scale;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) h[e] = (_Float16)ldexpf(v[e], shift);
+                } else {
+                    const h4 old = *reinterpret_cast<const h4*>(A + at * 2);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) h[e] = (_Float16)fmaf(step.b, (float)old[e], step.c * ldexpf(v[e], -kLog2A));
+                }
+                _Float16* out = reinterpret_cast<_Float16*>(MODE == kGram ? A : B);
+                *reinterpret_cast<h4*>(out + at) = h;
+                if (ti != tj) {
+                    const int64_t mirror = panel_at(r, c, sp);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) out[mirror + e * kPanel] = h[e];
+                }
             }
+        }
 }
 
 // ---------------------------------------------------------------- host side
