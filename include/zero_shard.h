@@ -779,7 +779,7 @@ int zero_multi_adam_step_coef(const void* table, const void* d_table, const void
  *   squares within 32 (ZERO_ERANGE).  1 <= n_steps <= ZERO_MAX_ORTHO_STEPS.
  *   Workspace: zero_multi_orthogonalize_workspace_bytes(table) bytes, 256-byte
  *   aligned, clobbered: about 4 bytes an element, and 4 for each of a short
- *   side's square, of the list or of a part of it of 2 GiB.  Calls, and graphs
+ *   side's square, of the list or of a part of it of 4 GiB.  Calls, and graphs
  *   recorded with them, that may run at the same time need a workspace each.
  * zero_multi_muon_update (master, ortho; param_out): per element, in float32,
  *     p = fma(p, 1 - lr * weight_decay, -((lr * scale) * o));  param = round(p)

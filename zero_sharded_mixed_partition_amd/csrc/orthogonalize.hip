@@ -34,7 +34,7 @@ typedef short s4 __attribute__((ext_vector_type(4)));
 
 constexpr int kLog2A = 10;                       // A and B are held times 2^10
 constexpr int kPanel = 32;                       // columns of a panel, and the inner elements of a stage
-constexpr int64_t kPassBytes = int64_t(2) << 30; // workspace of a pass, if it holds more than one matrix
+constexpr int64_t kPassBytes = int64_t(4) << 30; // workspace of a pass, if it holds more than one matrix
 
 enum { kGram, kPoly, kApply };
 
@@ -233,6 +233,9 @@ struct Product {
     }
 };
 
+// Stages of an inner dimension, an even number: behind them the padding is zero.
+__device__ __host__ __forceinline__ int stages_of(int depth) { return (depth + 2 * kPanel - 1) / (2 * kPanel) * 2; }
+
 struct NsStep {
     float a, b, c;
     int32_t odd;                                   // the iterate is in x1
@@ -278,12 +281,12 @@ __global__ __launch_bounds__(64 * WM * WN) void ortho_product(NsRef ref, int64_t
         pm = X + (int64_t)tj * (T / kPanel) * sp * 64;
         pn = B + ti * (T * 64);
         move_m = kPanel * 64;
-        n = m.sp / kPanel;
+        n = stages_of(m.s);
     } else {
         const char* from = MODE == kGram ? X : A;
         pm = from + ti * (T * 64);
         pn = from + tj * (T * 64);
-        n = (MODE == kGram ? m.lp : m.sp) / kPanel;
+        n = stages_of(MODE == kGram ? m.l : m.s);
     }
     uint32_t on[L];
     const char* cm[MODE == kApply ? L : 1];
@@ -442,20 +445,54 @@ int64_t pad256(int64_t x) { return pad_to(x, 256); }
 
 int tile_of(int64_t s) { return s >= 1024 ? 256 : s > 256 ? 128 : 64; }
 
-// Blocks go to the eight XCDs in turn: the list is dealt out so that each XCD
-// takes a run of it, whose tiles share their operands in one L2.
+// Blocks go to the eight XCDs in turn.  A run of tiles of equal depth is dealt
+// out so that each XCD takes a part of it whose tiles share their operands in
+// one L2, and as many tiles as the others.
 void deal_out(std::vector<TileRef>& tiles, size_t first) {
     const std::vector<TileRef> run(tiles.begin() + first, tiles.end());
-    const size_t n = run.size();
-    size_t start = 0;
+    size_t next = 0;
     for (size_t xcd = 0; xcd < 8; ++xcd)
-        for (size_t b = xcd; b < n; b += 8) tiles[first + b] = run[start++];
+        for (size_t b = first + (xcd + 8 - first % 8) % 8; b < tiles.size(); b += 8) tiles[b] = run[next++];
 }
 
 int64_t place(int64_t* at, int64_t bytes) {
     const int64_t here = *at;
     *at += pad256(bytes);
     return here;
+}
+
+// A matrix's places in the workspace, from *at on.
+void place_item(MatrixItem* it, int64_t* at) {
+    const int64_t x = (int64_t)it->sp * it->lp * 2, a = (int64_t)it->sp * it->sp * 2;
+    it->x0 = place(at, x);
+    it->x1 = place(at, x);
+    it->a = place(at, a);
+    it->b = place(at, a);
+    it->slots = place(at, (int64_t)it->n_slots * 8);
+}
+
+// The tiles of the symmetric products (lower triangle), or of the iterate, of
+// the items from `first` on: the deepest products first, so that short ones fill
+// the end; within a matrix four tile rows at a time, column by column.
+void add_tiles(OrthoPlan* plan, size_t first, int tile, bool symmetric) {
+    constexpr int kBand = 4;
+    const auto depth = [&](uint32_t k) { return stages_of(symmetric ? plan->items[k].l : plan->items[k].s); };
+    std::vector<uint32_t> order;
+    for (size_t k = first; k < plan->items.size(); ++k) order.push_back((uint32_t)k);
+    std::stable_sort(order.begin(), order.end(), [&](uint32_t a, uint32_t b) { return depth(a) > depth(b); });
+    for (size_t o = 0; o < order.size();) {
+        const size_t run = plan->tiles.size();
+        const int d = depth(order[o]);
+        for (; o < order.size() && depth(order[o]) == d; ++o) {
+            const uint32_t k = order[o];
+            const int n = plan->items[k].sp / tile, nl = symmetric ? n : plan->items[k].lp / tile;
+            for (int i0 = 0; i0 < n; i0 += kBand)
+                for (int j = 0; j < (symmetric ? std::min(i0 + kBand, n) : nl); ++j)
+                    for (int i = symmetric ? std::max(i0, j) : i0; i < std::min(i0 + kBand, n); ++i)
+                        plan->tiles.push_back({k, (uint16_t)i, (uint16_t)j});
+        }
+        deal_out(plan->tiles, run);
+    }
 }
 
 template <int MODE>
@@ -499,63 +536,52 @@ int check_coefs(const double* coefs, int32_t n_steps) {
 
 int plan_ortho(const std::vector<OrthoMatrix>& matrices, OrthoPlan* plan) {
     for (const int tile : {256, 128, 64}) {
-        std::vector<size_t> mine;
-        for (size_t k = 0; k < matrices.size(); ++k)
-            if (tile_of(std::min(matrices[k].rows, matrices[k].cols)) == tile) mine.push_back(k);
+        std::vector<MatrixItem> mine;
+        int64_t total = 0;
+        for (const OrthoMatrix& m : matrices) {
+            if (tile_of(std::min(m.rows, m.cols)) != tile) continue;
+            MatrixItem it{};
+            it.in = m.in;
+            it.out = m.out;
+            it.tall = m.rows > m.cols;
+            it.s = (int32_t)std::min(m.rows, m.cols);
+            it.l = (int32_t)std::max(m.rows, m.cols);
+            it.sp = (int32_t)pad_to(it.s, tile);
+            it.lp = (int32_t)pad_to(it.l, tile);
+            it.udt = m.udt;
+            it.odt = m.odt;
+            while (it.log2_scale < 12 && (int64_t(4) << (2 * it.log2_scale)) <= it.l) ++it.log2_scale;
+            const int64_t n_tiles = (int64_t)(it.sp / tile) * (it.lp / tile);
+            if (n_tiles > INT32_MAX) return fail(ZERO_ERANGE, "a matrix of %d x %d is too large", it.s, it.l);
+            it.n_slots = (int32_t)n_tiles;
+            place_item(&it, &total);
+            mine.push_back(it);
+        }
+        // as many passes as the workspace takes, of about equal size; in each the deepest products first
+        const int64_t share = total / ((total + kPassBytes - 1) / kPassBytes + !total) + 1;
         for (size_t done = 0; done < mine.size();) {
             OrthoPass pass{};
             pass.tile = tile;
             int64_t at = 0;
-            const size_t first_item = plan->items.size();
-            for (; done < mine.size(); ++done) {
-                const OrthoMatrix& m = matrices[mine[done]];
-                MatrixItem it{};
-                it.in = m.in;
-                it.out = m.out;
-                it.tall = m.rows > m.cols;
-                it.s = (int32_t)std::min(m.rows, m.cols);
-                it.l = (int32_t)std::max(m.rows, m.cols);
-                it.sp = (int32_t)pad_to(it.s, tile);
-                it.lp = (int32_t)pad_to(it.l, tile);
-                it.udt = m.udt;
-                it.odt = m.odt;
-                while (it.log2_scale < 12 && (int64_t(4) << (2 * it.log2_scale)) <= it.l) ++it.log2_scale;
-                const int64_t n_tiles = (int64_t)(it.sp / tile) * (it.lp / tile);
-                if (n_tiles > INT32_MAX) return fail(ZERO_ERANGE, "a matrix of %d x %d is too large", it.s, it.l);
-                it.n_slots = (int32_t)n_tiles;
-                const int64_t x = (int64_t)it.sp * it.lp * 2, a = (int64_t)it.sp * it.sp * 2;
-                if (plan->items.size() > first_item && at + 2 * (x + a) > kPassBytes) break;
-                it.x0 = place(&at, x);
-                it.x1 = place(&at, x);
-                it.a = place(&at, a);
-                it.b = place(&at, a);
-                it.slots = place(&at, n_tiles * 8);
-                plan->items.push_back(it);
+            size_t end = done;
+            while (end < mine.size() && (end == done || at < share)) {
+                int64_t after = at;
+                place_item(&mine[end], &after);
+                if (end > done && after > kPassBytes) break;
+                at = after;
+                ++end;
             }
             plan->workspace = std::max(plan->workspace, at);
-            pass.n_items = (int32_t)(plan->items.size() - first_item);
-            // four tile rows at a time, column by column
-            constexpr int kBand = 4;
+            const size_t first_item = plan->items.size();
+            plan->items.insert(plan->items.end(), mine.begin() + done, mine.begin() + end);
+            pass.n_items = (int32_t)(end - done);
+            done = end;
             pass.sym_first = (int64_t)plan->tiles.size();
-            for (size_t k = first_item; k < plan->items.size(); ++k) {
-                const int n = plan->items[k].sp / tile;
-                for (int i0 = 0; i0 < n; i0 += kBand)
-                    for (int j = 0; j < std::min(i0 + kBand, n); ++j)
-                        for (int i = std::max(i0, j); i < std::min(i0 + kBand, n); ++i)
-                            plan->tiles.push_back({(uint32_t)k, (uint16_t)i, (uint16_t)j});
-            }
+            add_tiles(plan, first_item, tile, true);
             pass.n_sym = (int64_t)plan->tiles.size() - pass.sym_first;
-            deal_out(plan->tiles, (size_t)pass.sym_first);
             pass.x_first = (int64_t)plan->tiles.size();
-            for (size_t k = first_item; k < plan->items.size(); ++k) {
-                const int n = plan->items[k].sp / tile, nl = plan->items[k].lp / tile;
-                for (int i0 = 0; i0 < n; i0 += kBand)
-                    for (int j = 0; j < nl; ++j)
-                        for (int i = i0; i < std::min(i0 + kBand, n); ++i)
-                            plan->tiles.push_back({(uint32_t)k, (uint16_t)i, (uint16_t)j});
-            }
+            add_tiles(plan, first_item, tile, false);
             pass.n_x = (int64_t)plan->tiles.size() - pass.x_first;
-            deal_out(plan->tiles, (size_t)pass.x_first);
             if (std::max(pass.n_x, pass.n_sym) > INT32_MAX) return fail(ZERO_ERANGE, "the list is too long");
             plan->passes.push_back(pass);
         }
