@@ -33,7 +33,7 @@ struct MatrixDesc {
     int32_t reserved;
 };
 
-// One matrix of the orthogonalisation: s rows of l >= s elements (transposed if
+// One matrix of the orthogonalisation, as its tiled products see it: s rows of l >= s elements (transposed if
 // the caller's has more rows than columns), padded to sp x lp in the workspace.
 struct MatrixItem {
     const void* in;
@@ -49,15 +49,36 @@ struct MatrixItem {
     int32_t reserved;
 };
 
+// The same memory for a thin matrix (s <= 128), padded to sp rows.
+struct ThinItem {
+    const void* in;
+    void* out;
+    int64_t parts;                      // workspace: partial X X^T, float [n_parts][tiles of the lower triangle][256]
+    int64_t exponents;                  // workspace: each part's exponent, int32 [n_parts]
+    int64_t q;                          // workspace: the steps' polynomials, half, sp * sp a step (twice that for sp <= 64)
+    int64_t factor;                     // workspace: 1 / max(|U|, eps), double
+    int64_t chunks_per_part;
+    int32_t n_parts;
+    int32_t s, l, sp, n_chunks;
+    int32_t udt, odt;
+    int32_t tall;
+    int32_t log2_scale;
+    int32_t reserved;
+};
+static_assert(sizeof(ThinItem) == sizeof(MatrixItem), "one array holds both");
+
 struct TileRef {
     uint32_t item;
     uint16_t i, j;                      // tile row (along s) and tile column
 };
 
 // A run of items of one tile size that the workspace holds at once.
+// Thin ones (tile = minus the padded short side) have parts of X X^T in place of
+// the first list, and chunks of columns in place of the second.
 struct OrthoPass {
     int32_t tile;
     int32_t n_items;
+    int64_t first_item;
     int64_t sym_first, n_sym;           // tiles of the symmetric products, lower triangle
     int64_t x_first, n_x;               // tiles of the iterate
 };

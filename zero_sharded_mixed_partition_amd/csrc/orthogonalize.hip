@@ -23,35 +23,14 @@
 #include <type_traits>
 #include <vector>
 
-#include "matrix_table.h"
+#include "orthogonalize.h"
 
 namespace zero_shard {
 namespace {
 
-typedef _Float16 h8 __attribute__((ext_vector_type(8)));
-typedef _Float16 h4 __attribute__((ext_vector_type(4)));
-typedef short s4 __attribute__((ext_vector_type(4)));
-
-constexpr int kLog2A = 10;                       // A and B are held times 2^10
 constexpr int kPanel = 32;                       // columns of a panel, and the inner elements of a stage
-constexpr int64_t kPassBytes = int64_t(4) << 30; // workspace of a pass, if it holds more than one matrix
 
 enum { kGram, kPoly, kApply };
-
-struct NsRef {
-    const MatrixItem* items;
-    const TileRef* tiles;
-    char* ws;
-    const int32_t* d_ovf;
-
-    __device__ __forceinline__ const ZS_CONSTANT TileRef& tile(int64_t i) const {
-        return ((const ZS_CONSTANT TileRef*)tiles)[i];
-    }
-    __device__ __forceinline__ const ZS_CONSTANT MatrixItem& item(uint32_t i) const {
-        return ((const ZS_CONSTANT MatrixItem*)items)[i];
-    }
-    __device__ __forceinline__ bool skipped() const { return d_ovf != nullptr && *d_ovf != 0; }
-};
 
 // ---------------------------------------------------------------- load and norm
 
@@ -170,19 +149,6 @@ __device__ __forceinline__ void load_lds(const void* base, uint32_t offset, uint
                      :
                      : "s"(lds), "v"(offset), "s"(base)
                      : "memory");
-}
-
-typedef __attribute__((address_space(3))) char lds_char;
-
-__device__ __forceinline__ uint32_t lds_address(const void* p) {
-    return (uint32_t)(uintptr_t)(lds_char*)(char*)p;
-}
-
-__device__ __forceinline__ h8 lds_h8(uint32_t a) { return *(__attribute__((address_space(3))) h8*)(uintptr_t)a; }
-
-// Four values down a column of 4 x 16 blocks (a lane of 16 gives the address of a fourth of a row).
-__device__ __forceinline__ h4 lds_column(uint32_t a) {
-    return __builtin_bit_cast(h4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4*)(uintptr_t)a));
 }
 
 // A wave's share of a T x T tile of a product, WM x WN waves.
@@ -440,9 +406,6 @@ __global__ __launch_bounds__(64 * WM * WN) void ortho_product(NsRef ref, int64_t
 
 // ---------------------------------------------------------------- host side
 
-int64_t pad_to(int64_t x, int64_t t) { return (x + t - 1) / t * t; }
-int64_t pad256(int64_t x) { return pad_to(x, 256); }
-
 int tile_of(int64_t s) { return s >= 1024 ? 256 : s > 256 ? 128 : 64; }
 
 // Blocks go to the eight XCDs in turn.  A run of tiles of equal depth is dealt
@@ -453,12 +416,6 @@ void deal_out(std::vector<TileRef>& tiles, size_t first) {
     size_t next = 0;
     for (size_t xcd = 0; xcd < 8; ++xcd)
         for (size_t b = first + (xcd + 8 - first % 8) % 8; b < tiles.size(); b += 8) tiles[b] = run[next++];
-}
-
-int64_t place(int64_t* at, int64_t bytes) {
-    const int64_t here = *at;
-    *at += pad256(bytes);
-    return here;
 }
 
 // A matrix's places in the workspace, from *at on.
@@ -539,7 +496,7 @@ int plan_ortho(const std::vector<OrthoMatrix>& matrices, OrthoPlan* plan) {
         std::vector<MatrixItem> mine;
         int64_t total = 0;
         for (const OrthoMatrix& m : matrices) {
-            if (tile_of(std::min(m.rows, m.cols)) != tile) continue;
+            if (std::min(m.rows, m.cols) <= kThin || tile_of(std::min(m.rows, m.cols)) != tile) continue;
             MatrixItem it{};
             it.in = m.in;
             it.out = m.out;
@@ -550,7 +507,7 @@ int plan_ortho(const std::vector<OrthoMatrix>& matrices, OrthoPlan* plan) {
             it.lp = (int32_t)pad_to(it.l, tile);
             it.udt = m.udt;
             it.odt = m.odt;
-            while (it.log2_scale < 12 && (int64_t(4) << (2 * it.log2_scale)) <= it.l) ++it.log2_scale;
+            it.log2_scale = log2_scale(it.l);
             const int64_t n_tiles = (int64_t)(it.sp / tile) * (it.lp / tile);
             if (n_tiles > INT32_MAX) return fail(ZERO_ERANGE, "a matrix of %d x %d is too large", it.s, it.l);
             it.n_slots = (int32_t)n_tiles;
@@ -574,6 +531,7 @@ int plan_ortho(const std::vector<OrthoMatrix>& matrices, OrthoPlan* plan) {
             plan->workspace = std::max(plan->workspace, at);
             const size_t first_item = plan->items.size();
             plan->items.insert(plan->items.end(), mine.begin() + done, mine.begin() + end);
+            pass.first_item = (int64_t)first_item;
             pass.n_items = (int32_t)(end - done);
             done = end;
             pass.sym_first = (int64_t)plan->tiles.size();
@@ -586,7 +544,7 @@ int plan_ortho(const std::vector<OrthoMatrix>& matrices, OrthoPlan* plan) {
             plan->passes.push_back(pass);
         }
     }
-    return ZERO_OK;
+    return plan_thin(matrices, plan);
 }
 
 }  // namespace zero_shard
@@ -628,8 +586,20 @@ int zero_multi_orthogonalize(const void* table, const void* d_table, const doubl
     const NsRef ref{at<MatrixItem>(d_table, h.items_at), at<TileRef>(d_table, h.tiles_at), static_cast<char*>(d_workspace),
                     d_global_overflow};
     const OrthoPass* passes = at<OrthoPass>(table, h.passes_at);
+    ThinSteps steps{};
+    steps.n = n_steps;
+    for (int k = 0; k < n_steps; ++k) {
+        steps.a[k] = (float)coefs[3 * k];
+        steps.b[k] = (float)coefs[3 * k + 1];
+        steps.c[k] = (float)coefs[3 * k + 2];
+    }
     for (int p = 0; p < h.n_passes; ++p) {
         const OrthoPass& pass = passes[p];
+        if (pass.tile <= 0) {
+            rc = launch_thin(pass, ref, steps, eps, s);
+            if (rc != ZERO_OK) return rc;
+            continue;
+        }
         hipLaunchKernelGGL(ortho_squares, dim3((unsigned)pass.n_x), dim3(kBlock), 0, s, ref, pass.x_first, pass.tile);
         rc = launch_status("ortho_squares");
         if (rc != ZERO_OK) return rc;

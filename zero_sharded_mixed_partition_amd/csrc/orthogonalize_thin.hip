@@ -1,0 +1,684 @@
+// Orthogonalisation of matrices with a short side s of at most 128: low-rank
+// adapters, single heads, small layers.
+//
+// Every step multiplies X from the left by a polynomial of A = X X^T, and A of
+// the next step follows from A alone: with Q = a I + B, B = b A + c A A (all of
+// them symmetric, and functions of the first A, so they commute)
+//     X' = Q X,   A' = X' X'^T = Q A Q.
+// So U is read once for its A, which is s x s, all steps' B are formed from that
+// by one workgroup, and U is read again, multiplied by the steps' Q in turn
+// while it stays in registers, and stored.  Three launches, whatever the number
+// of steps, and 6 to 8 bytes an element; the tiled products take 17 launches and
+// 50 bytes.
+//
+// What is rounded.  A small singular value's square is far below A's largest
+// entries, and the steps multiply it by up to 11.8 each: A, Q A and B are held
+// as two fp16 each (22 bits, times 2^10), their products as three MFMAs of the
+// four (the lower halves' own is below 2^-22), sums in float32.  U enters A with
+// 11 bits or what it has of them, float32 as two fp16.  X stays in float32; in B
+// X both factors are two fp16 for s <= 64, and one for larger s, which costs the
+// result 1e-3 and saves two thirds of the products.  fp16's range: each chunk
+// of U is scaled by a power of two of its own, which follows it to the sum.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <climits>
+#include <cmath>
+#include <vector>
+
+#include "orthogonalize.h"
+
+namespace zero_shard {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kChunkElements = 16384;            // padded elements of U per chunk: 64 a thread
+
+template <int SP>
+struct Thin {
+    static constexpr int kR = SP / 16;                        // rows of 16 x 16 tiles
+    static constexpr int kTiles = kR * (kR + 1) / 2;          // of the lower triangle
+    static constexpr int kLC = kChunkElements / SP;           // columns of a chunk
+    static constexpr int kWaves2 = SP == 128 ? 12 : SP == 64 ? 5 : 3;   // of the second kernel: tiles divide evenly
+    static constexpr int kOwn = kTiles / kWaves2;
+    static constexpr bool kTwo = SP <= 64;                    // X and B as two fp16 in their product
+    static constexpr int kB = SP * SP * (kTwo ? 2 : 1);       // halves of a step's B
+    static constexpr int kStageLd = kLC + 4;                  // floats a row: four rows apart meet other banks
+};
+
+__device__ __forceinline__ int pair_index(int i, int j) { return i * (i + 1) / 2 + j; }
+
+// ---------------------------------------------------------------- a chunk of U
+
+// Eight consecutive elements, the first `valid` of them; whole: eight may be read.
+template <int DT>
+__device__ __forceinline__ void ld8(const void* U, int64_t e, int valid, bool whole, float v[8]) {
+    if (whole) {
+        if constexpr (DT == ZERO_F32) {
+            const f32x4 a = ld_any(static_cast<const float*>(U) + e), b = ld_any(static_cast<const float*>(U) + e + 4);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                v[k] = a[k];
+                v[k + 4] = b[k];
+            }
+        } else {
+            const u32x4 w = ld16_any(static_cast<const uint16_t*>(U) + e);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) unpack2<DT>(w[k], v[2 * k], v[2 * k + 1]);
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = k < valid ? v[k] : 0.0f;
+    } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = k < valid ? ld_grad1<DT>(U, e + k) : 0.0f;
+    }
+}
+
+// The caller's place of a thread's n-th vector of eight of a chunk: along the
+// long side for a wide matrix, along the short one for a tall one.
+template <int SP>
+struct Vector {
+    int r, c;                                    // in X: row, and column from the chunk's first
+    int64_t at;                                  // of its first element in the matrix
+    int valid;
+
+    __device__ __forceinline__ Vector(const ZS_CONSTANT ThinItem& m, int64_t first, int n) {
+        const int v = n * kThreads + threadIdx.x;
+        if (m.tall) {
+            r = v % (SP / 8) * 8;
+            c = v / (SP / 8);
+            at = (first + c) * m.s + r;
+            valid = first + c < m.l ? m.s - r : 0;
+        } else {
+            r = v / (Thin<SP>::kLC / 8);
+            c = v % (Thin<SP>::kLC / 8) * 8;
+            at = r * (int64_t)m.l + first + c;
+            const int64_t left = m.l - first - c;
+            valid = r < m.s ? (int)(left < 8 ? left : 8) : 0;
+        }
+        valid = valid < 0 ? 0 : valid > 8 ? 8 : valid;
+    }
+};
+
+template <int SP, int DT>
+__device__ __forceinline__ void load_chunk(const ZS_CONSTANT ThinItem& m, int64_t first, float x[8][8]) {
+    const int64_t all = (int64_t)m.s * m.l;
+    // a vector may run over its row's end into the next row, but not over the matrix's
+    const int64_t last = m.tall ? (first + Thin<SP>::kLC < m.l ? (first + Thin<SP>::kLC) * m.s : all)
+                                : (m.s - 1) * (int64_t)m.l + (first + Thin<SP>::kLC < m.l ? first + Thin<SP>::kLC : m.l);
+    if (last + 8 <= all) {
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+            const Vector<SP> v(m, first, n);
+            ld8<DT>(m.in, v.valid ? v.at : 0, v.valid, true, x[n]);
+        }
+    } else {
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+            const Vector<SP> v(m, first, n);
+            const bool whole = v.at + 8 <= all;
+            ld8<DT>(m.in, v.valid ? v.at : 0, v.valid, v.valid > 0 && whole, x[n]);
+        }
+    }
+}
+
+template <int SP>
+__device__ __forceinline__ void load_chunk(const ZS_CONSTANT ThinItem& m, int64_t first, float x[8][8]) {
+    if (m.udt == ZERO_F16) load_chunk<SP, ZERO_F16>(m, first, x);
+    else if (m.udt == ZERO_BF16) load_chunk<SP, ZERO_BF16>(m, first, x);
+    else load_chunk<SP, ZERO_F32>(m, first, x);
+}
+
+// ---------------------------------------------------------------- first kernel: parts of U U^T
+
+// The chunk in the LDS as halves.  Wide: [SP][kLC], the 16-byte pieces of row r
+// in the order piece ^ r % 16.  Tall: [kLC][SP] for the transposing load, the
+// 32-byte pieces of row r in an order by r, so that rows 0 .. 3 and 8 .. 11 of
+// 16, which a half wave reads, meet all banks.
+template <int SP>
+__device__ __forceinline__ int tall_order(int r) {
+    if (SP == 128) return (r & 3) | ((r >> 1) & 4);
+    if (SP == 64) return ((r >> 1) & 1) | ((r >> 2) & 2);
+    return (r >> 3) & 1;
+}
+
+template <int SP>
+__device__ __forceinline__ h8 chunk_fragment(uint32_t lds, bool tall, int i, int kk, int lane) {
+    if (tall) {
+        const int r = kk * 32 + (lane >> 4) * 8 + ((lane & 15) >> 2);
+        const uint32_t a = lds + r * (SP * 2) + (i ^ tall_order<SP>(r)) * 32 + (lane & 3) * 8;
+        const int r4 = r + 4;
+        const uint32_t b = lds + r4 * (SP * 2) + (i ^ tall_order<SP>(r4)) * 32 + (lane & 3) * 8;
+        return __builtin_shufflevector(lds_column(a), lds_column(b), 0, 1, 2, 3, 4, 5, 6, 7);
+    }
+    const int r = i * 16 + (lane & 15);
+    return lds_h8(lds + r * (Thin<SP>::kLC * 2) + (((kk * 4 + (lane >> 4)) ^ (r & 15)) << 4));
+}
+
+// One part of an item: chunks_per_part chunks, summed in order.
+template <int SP>
+__global__ __launch_bounds__(kThreads) void thin_gram(NsRef ref, int64_t first) {
+    using H = Thin<SP>;
+    constexpr int R = H::kR;
+    if (ref.skipped()) return;
+    __shared__ __attribute__((aligned(1024))) char smem[2 * kChunkElements * 2];
+    __shared__ uint32_t s_top[kThreads / 64];
+    const ZS_CONSTANT TileRef& t = ref.tile(first + blockIdx.x);
+    const ZS_CONSTANT ThinItem& m = ((const ZS_CONSTANT ThinItem*)ref.items)[t.item];
+    const int part = t.i, lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t hi = lds_address(smem), lo = hi + kChunkElements * 2;
+    const bool two = m.udt == ZERO_F32, tall = m.tall != 0;
+    // SP 128: a wave owns tile rows `wave` and 7 - wave, nine tiles.  Else: all
+    // tiles, on every fourth step of the chunk's inner dimension.
+    constexpr int kOwn = SP == 128 ? 12 : H::kTiles;
+    f32x4 acc[kOwn];
+#pragma unroll
+    for (int k = 0; k < kOwn; ++k) acc[k] = f32x4{};
+    int run = INT_MIN / 4;                       // exponent that the sums are scaled by
+    bool bad = false;
+    const int64_t c_end = (part + 1) * m.chunks_per_part < m.n_chunks ? (part + 1) * m.chunks_per_part : m.n_chunks;
+    for (int64_t chunk = part * m.chunks_per_part; chunk < c_end; ++chunk) {
+        float x[8][8];
+        load_chunk<SP>(m, chunk * H::kLC, x);
+        uint32_t top = 0;
+#pragma unroll
+        for (int n = 0; n < 8; ++n)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const uint32_t b = __float_as_uint(x[n][k]) & 0x7FFFFFFFu;
+                top = b > top ? b : top;
+            }
+        for (int off = 32; off > 0; off >>= 1) {
+            const uint32_t other = (uint32_t)__shfl_xor((int)top, off, 64);
+            top = other > top ? other : top;
+        }
+        if (lane == 0) s_top[wave] = top;
+        __syncthreads();                         // also: the last chunk's fragments have been read
+        for (int w = 0; w < kThreads / 64; ++w) top = s_top[w] > top ? s_top[w] : top;
+        top = (uint32_t)__builtin_amdgcn_readfirstlane((int)top);
+        if (top >= 0x7F800000u) bad = true;
+        if (top != 0 && !bad) {
+            // the largest element lands in [2^14, 2^15)
+            const int e = (int)ilogbf(__uint_as_float(top)) - 14;
+            if (e > run) {
+                const int down = run < INT_MIN / 8 ? 0 : 2 * (run - e);
+#pragma unroll
+                for (int k = 0; k < kOwn; ++k)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) acc[k][q] = ldexpf(acc[k][q], down);
+                run = e;
+            }
+        }
+        const int shift = run < INT_MIN / 8 ? 0 : -run;
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+            h8 h, g;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float y = ldexpf(x[n][k], shift);
+                h[k] = (_Float16)y;
+                g[k] = (_Float16)(y - (float)h[k]);
+            }
+            const Vector<SP> v(m, 0, n);
+            const uint32_t at = tall ? v.c * (SP * 2) + (((v.r >> 4) ^ tall_order<SP>(v.c)) << 5) + (v.r & 8) * 2
+                                     : v.r * (H::kLC * 2) + (((v.c >> 3) ^ (v.r & 15)) << 4);
+            *reinterpret_cast<h8*>(smem + at) = h;
+            if (two) *reinterpret_cast<h8*>(smem + kChunkElements * 2 + at) = g;
+        }
+        __syncthreads();
+        const auto product = [&](f32x4& into, const h8& ih, const h8& il, const h8& jh, const h8& jl) {
+            into = __builtin_amdgcn_mfma_f32_16x16x32_f16(ih, jh, into, 0, 0, 0);
+            if (two) {
+                into = __builtin_amdgcn_mfma_f32_16x16x32_f16(ih, jl, into, 0, 0, 0);
+                into = __builtin_amdgcn_mfma_f32_16x16x32_f16(il, jh, into, 0, 0, 0);
+            }
+        };
+        if constexpr (SP == 128) {
+            for (int kk = 0; kk < H::kLC / 32; ++kk) {
+                const h8 ah = chunk_fragment<SP>(hi, tall, wave, kk, lane), bh = chunk_fragment<SP>(hi, tall, 7 - wave, kk, lane);
+                h8 al{}, bl{};
+                if (two) {
+                    al = chunk_fragment<SP>(lo, tall, wave, kk, lane);
+                    bl = chunk_fragment<SP>(lo, tall, 7 - wave, kk, lane);
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    if (j > 7 - wave) continue;
+                    const h8 jh = chunk_fragment<SP>(hi, tall, j, kk, lane);
+                    const h8 jl = two ? chunk_fragment<SP>(lo, tall, j, kk, lane) : h8{};
+                    product(acc[4 + j], bh, bl, jh, jl);
+                    if (j < 4 && j <= wave) product(acc[j], ah, al, jh, jl);
+                }
+            }
+        } else {
+            for (int kk = wave; kk < H::kLC / 32; kk += kThreads / 64) {
+                h8 fh[R], fl[R];
+#pragma unroll
+                for (int i = 0; i < R; ++i) {
+                    fh[i] = chunk_fragment<SP>(hi, tall, i, kk, lane);
+                    fl[i] = two ? chunk_fragment<SP>(lo, tall, i, kk, lane) : h8{};
+                }
+#pragma unroll
+                for (int i = 0; i < R; ++i)
+#pragma unroll
+                    for (int j = 0; j <= i; ++j) product(acc[i * (i + 1) / 2 + j], fh[i], fl[i], fh[j], fl[j]);
+            }
+        }
+    }
+    float* out = reinterpret_cast<float*>(ref.ws + m.parts) + (int64_t)part * H::kTiles * 256;
+    if constexpr (SP == 128) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if (j <= 7 - wave) reinterpret_cast<f32x4*>(out + pair_index(7 - wave, j) * 256)[lane] = acc[4 + j];
+            if (j < 4 && j <= wave) reinterpret_cast<f32x4*>(out + pair_index(wave, j) * 256)[lane] = acc[j];
+        }
+    } else {
+        // the four waves' sums, added in their order
+        __syncthreads();
+        f32x4* all = reinterpret_cast<f32x4*>(smem);
+#pragma unroll
+        for (int k = 0; k < H::kTiles; ++k) all[(wave * H::kTiles + k) * 64 + lane] = acc[k];
+        __syncthreads();
+        for (int k = threadIdx.x; k < H::kTiles * 64; k += kThreads) {
+            f32x4 sum = all[k];
+            for (int w = 1; w < kThreads / 64; ++w) sum += all[w * H::kTiles * 64 + k];
+            reinterpret_cast<f32x4*>(out)[k] = sum;
+        }
+    }
+    if (threadIdx.x == 0) reinterpret_cast<int32_t*>(ref.ws + m.exponents)[part] = bad ? INT_MAX : run;
+}
+
+// ---------------------------------------------------------------- second kernel: the steps' polynomials
+
+// [SP][SP] halves, the 16-byte pieces of row r in an order by r: 16 lanes that
+// read one piece of 16 rows meet all banks.
+template <int SP>
+__device__ __forceinline__ uint32_t square_piece(int r, int piece) {
+    const int order = SP == 128 ? r & 15 : SP == 64 ? (r >> 1) & 7 : (r >> 2) & 3;
+    return r * (SP * 2) + ((piece ^ order) << 4);
+}
+
+// A tile's values (rows 16 i + 4 g + e, column 16 j + c) into a symmetric
+// matrix of two fp16: hi at `at`, lo behind it.
+template <int SP>
+__device__ __forceinline__ void put_square(char* at, int i, int j, int lane, const f32x4& v) {
+    constexpr int kLo = SP * SP * 2;
+    const int g = lane >> 4, c = lane & 15;
+    h4 h, l;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        h[e] = (_Float16)v[e];
+        l[e] = (_Float16)(v[e] - (float)h[e]);
+    }
+    char* row = at + square_piece<SP>(16 * j + c, 2 * i + (g >> 1)) + (g & 1) * 8;
+    *reinterpret_cast<h4*>(row) = h;
+    *reinterpret_cast<h4*>(row + kLo) = l;
+    if (i != j) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            char* to = at + square_piece<SP>(16 * i + 4 * g + e, 2 * j + (c >> 3)) + (c & 7) * 2;
+            *reinterpret_cast<_Float16*>(to) = h[e];
+            *reinterpret_cast<_Float16*>(to + kLo) = l[e];
+        }
+    }
+}
+
+// The tile (i, j) of the product of two symmetric matrices that commute.
+template <int SP>
+__device__ __forceinline__ f32x4 square_product(uint32_t a, uint32_t b, int i, int j, int lane) {
+    constexpr int kLo = SP * SP * 2;
+    f32x4 sum{};
+    const int ri = 16 * i + (lane & 15), rj = 16 * j + (lane & 15);
+#pragma unroll
+    for (int kk = 0; kk < SP / 32; ++kk) {
+        const uint32_t pa = a + square_piece<SP>(ri, kk * 4 + (lane >> 4)), pb = b + square_piece<SP>(rj, kk * 4 + (lane >> 4));
+        const h8 ah = lds_h8(pa), al = lds_h8(pa + kLo), bh = lds_h8(pb), bl = lds_h8(pb + kLo);
+        sum = __builtin_amdgcn_mfma_f32_16x16x32_f16(ah, bh, sum, 0, 0, 0);
+        sum = __builtin_amdgcn_mfma_f32_16x16x32_f16(ah, bl, sum, 0, 0, 0);
+        sum = __builtin_amdgcn_mfma_f32_16x16x32_f16(al, bh, sum, 0, 0, 0);
+    }
+    return sum;
+}
+
+// A tile of B for the third kernel, as its fragments: [i][k / 32][lane][8] halves
+// with the inner elements of a lane in the order 4 g .. + 3 of two tiles of 16.
+template <int SP>
+__device__ __forceinline__ void put_fragments(_Float16* to, int i, int j, int lane, const f32x4& v) {
+    const int g = lane >> 4, c = lane & 15;
+    h4 h, l;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        h[e] = (_Float16)v[e];
+        l[e] = (_Float16)(v[e] - (float)h[e]);
+    }
+    _Float16* at = to + (((j * (SP / 32) + i / 2) * 64 + g * 16 + c) * 8 + (i & 1) * 4);
+    *reinterpret_cast<h4*>(at) = h;
+    if (Thin<SP>::kTwo) *reinterpret_cast<h4*>(at + SP * SP) = l;
+    if (i != j) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            at = to + (((i * (SP / 32) + j / 2) * 64 + (c >> 2) * 16 + 4 * g + e) * 8 + (j & 1) * 4 + (c & 3));
+            at[0] = h[e];
+            if (Thin<SP>::kTwo) at[SP * SP] = l[e];
+        }
+    }
+}
+
+template <int SP>
+__global__ __launch_bounds__(64 * Thin<SP>::kWaves2) void thin_steps(NsRef ref, int64_t first_item, ThinSteps steps, double eps) {
+    using H = Thin<SP>;
+    constexpr int kOwn = H::kOwn;
+    if (ref.skipped()) return;
+    __shared__ __attribute__((aligned(1024))) char smem[4 * SP * SP * 2];     // A and B, two fp16 each
+    __shared__ double s_diag[SP];
+    const ZS_CONSTANT ThinItem& m = ((const ZS_CONSTANT ThinItem*)ref.items)[first_item + blockIdx.x];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int32_t* exponents = reinterpret_cast<const int32_t*>(ref.ws + m.exponents);
+    int top = INT_MIN;
+    for (int p = 0; p < m.n_parts; ++p) top = exponents[p] > top ? exponents[p] : top;
+    const bool bad = top == INT_MAX;
+    int ti[kOwn], tj[kOwn];
+    f32x4 A[kOwn];
+#pragma unroll
+    for (int k = 0; k < kOwn; ++k) {
+        const int tile = wave * kOwn + k;
+        int i = 0;
+        while ((i + 1) * (i + 2) / 2 <= tile) ++i;
+        ti[k] = i;
+        tj[k] = tile - i * (i + 1) / 2;
+        A[k] = f32x4{};
+    }
+    for (int p = 0; p < m.n_parts; ++p) {
+        const f32x4* part = reinterpret_cast<const f32x4*>(ref.ws + m.parts) + (int64_t)p * H::kTiles * 64;
+        const int down = exponents[p] < INT_MIN / 8 ? 0 : 2 * (exponents[p] - top);
+#pragma unroll
+        for (int k = 0; k < kOwn; ++k) {
+            const f32x4 v = part[(wave * kOwn + k) * 64 + lane];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) A[k][e] += ldexpf(v[e], bad ? 0 : down);
+        }
+    }
+    // |U|^2 = the trace
+#pragma unroll
+    for (int k = 0; k < kOwn; ++k)
+        if (ti[k] == tj[k] && (lane & 15) >> 2 == lane >> 4) {
+            const int e = lane & 3;
+            s_diag[16 * ti[k] + (lane & 15)] = (double)(e == 0 ? A[k][0] : e == 1 ? A[k][1] : e == 2 ? A[k][2] : A[k][3]);
+        }
+    __syncthreads();
+    double trace = 0.0;
+    for (int k = 0; k < SP; ++k) trace += s_diag[k];
+    const int up = top < INT_MIN / 8 || bad ? 0 : top;
+    const double norm = ldexp(sqrt(trace), up);
+    const double by = norm > eps ? norm : eps;
+    const double factor = bad ? NAN : by > 0.0 ? 1.0 / by : 0.0;
+    if (threadIdx.x == 0) *reinterpret_cast<double*>(ref.ws + m.factor) = factor;
+    const double unit = by > 0.0 ? ldexp(1.0, up) / by : 0.0;
+    const float f = (float)ldexp(unit * unit, kLog2A);
+#pragma unroll
+    for (int k = 0; k < kOwn; ++k) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) A[k][e] *= f;
+        put_square<SP>(smem, ti[k], tj[k], lane, A[k]);
+    }
+    __syncthreads();
+    const uint32_t a = lds_address(smem), b = a + 2 * SP * SP * 2;
+    char* const b_at = smem + 2 * SP * SP * 2;
+    constexpr float kDown = 1.0f / (1 << kLog2A);
+    for (int step = 0; step < steps.n; ++step) {
+        _Float16* q = reinterpret_cast<_Float16*>(ref.ws + m.q) + (int64_t)step * H::kB;
+#pragma unroll
+        for (int k = 0; k < kOwn; ++k) {
+            const f32x4 square = square_product<SP>(a, a, ti[k], tj[k], lane);
+            f32x4 B;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) B[e] = fmaf(steps.b[step], A[k][e], steps.c[step] * (square[e] * kDown));
+            put_fragments<SP>(q, ti[k], tj[k], lane, B);
+            put_square<SP>(b_at, ti[k], tj[k], lane, B);
+        }
+        if (step + 1 == steps.n) break;
+        // twice A <- a A + B A
+#pragma unroll
+        for (int twice = 0; twice < 2; ++twice) {
+            __syncthreads();
+            f32x4 next[kOwn];
+#pragma unroll
+            for (int k = 0; k < kOwn; ++k) {
+                const f32x4 v = square_product<SP>(b, a, ti[k], tj[k], lane);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) next[k][e] = fmaf(steps.a[step], A[k][e], v[e] * kDown);
+            }
+            __syncthreads();
+#pragma unroll
+            for (int k = 0; k < kOwn; ++k) {
+                A[k] = next[k];
+                put_square<SP>(smem, ti[k], tj[k], lane, A[k]);
+            }
+        }
+        __syncthreads();
+    }
+}
+
+// ---------------------------------------------------------------- third kernel: X through all steps
+
+template <int SP, int ODT>
+__device__ __forceinline__ void store_chunk(const ZS_CONSTANT ThinItem& m, int64_t first, const float* stage, float back) {
+    using H = Thin<SP>;
+    uint16_t* out = static_cast<uint16_t*>(m.out);
+#pragma unroll
+    for (int n = 0; n < 8; ++n) {
+        const Vector<SP> v(m, first, n);
+        if (v.valid == 0) continue;
+        const float* from = stage + v.r * H::kStageLd + v.c;
+        const int step = m.tall ? H::kStageLd : 1;
+        if (v.valid == 8) {
+            float a[4], b[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                a[k] = from[k * step] * back;
+                b[k] = from[(k + 4) * step] * back;
+            }
+            st_any(pack4_16<ODT>(a), out + v.at);
+            st_any(pack4_16<ODT>(b), out + v.at + 4);
+        } else {
+            for (int k = 0; k < v.valid; ++k) global(out)[v.at + k] = (uint16_t)to16<ODT>(from[k * step] * back);
+        }
+    }
+}
+
+// One chunk of columns.  A lane holds X as the MFMA leaves it, rows 16 i + 4 g
+// .. + 3 of a column, which is how the next product takes it: with the inner
+// elements in the order of put_fragments nothing moves between lanes.
+template <int SP>
+__global__ __launch_bounds__(kThreads) void thin_apply(NsRef ref, int64_t first, ThinSteps steps) {
+    using H = Thin<SP>;
+    constexpr int R = H::kR, kStrips = H::kLC / 64, kB = H::kB, kLoads = kB / 8 / kThreads;
+    if (ref.skipped()) return;
+    __shared__ __attribute__((aligned(1024))) char smem[SP * H::kStageLd * 4];
+    static_assert(kB * 2 <= SP * H::kStageLd * 4 && kLoads * 8 * kThreads == kB, "B takes the stage's place");
+    const ZS_CONSTANT TileRef& t = ref.tile(first + blockIdx.x);
+    const ZS_CONSTANT ThinItem& m = ((const ZS_CONSTANT ThinItem*)ref.items)[t.item];
+    const int64_t column = (int64_t)t.i * H::kLC;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    float* stage = reinterpret_cast<float*>(smem);
+    {
+        float x[8][8];
+        load_chunk<SP>(m, column, x);
+        const double f = ldexp(*reinterpret_cast<const double*>(ref.ws + m.factor), m.log2_scale);
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+            const Vector<SP> v(m, column, n);
+            float* to = stage + v.r * H::kStageLd + v.c;
+            if (m.tall) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) to[k * H::kStageLd] = (float)((double)x[n][k] * f);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 8; k += 4)
+                    *reinterpret_cast<f32x4*>(to + k) = f32x4{(float)((double)x[n][k] * f), (float)((double)x[n][k + 1] * f),
+                                                              (float)((double)x[n][k + 2] * f), (float)((double)x[n][k + 3] * f)};
+            }
+        }
+    }
+    const u32x4* q = reinterpret_cast<const u32x4*>(ref.ws + m.q);
+    u32x4 ahead[kLoads];
+#pragma unroll
+    for (int k = 0; k < kLoads; ++k) ahead[k] = q[k * kThreads + threadIdx.x];
+    __syncthreads();
+    const int own = wave * (H::kLC / 4) + (lane & 15), row = (lane >> 4) * 4;
+    f32x4 X[kStrips][R];
+#pragma unroll
+    for (int y = 0; y < kStrips; ++y)
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) X[y][i][e] = stage[(i * 16 + row + e) * H::kStageLd + own + y * 16];
+    for (int step = 0; step < steps.n; ++step) {
+        __syncthreads();                                      // the stage, or the last step's B, has been read
+#pragma unroll
+        for (int k = 0; k < kLoads; ++k) reinterpret_cast<u32x4*>(smem)[k * kThreads + threadIdx.x] = ahead[k];
+        if (step + 1 < steps.n) {
+            q += kB / 8;
+#pragma unroll
+            for (int k = 0; k < kLoads; ++k) ahead[k] = q[k * kThreads + threadIdx.x];
+        }
+        __syncthreads();
+        h8 xh[kStrips][R / 2], xl[kStrips][R / 2];
+#pragma unroll
+        for (int y = 0; y < kStrips; ++y)
+#pragma unroll
+            for (int i = 0; i < R; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const _Float16 h = (_Float16)X[y][i][e];
+                    xh[y][i / 2][(i & 1) * 4 + e] = h;
+                    if (H::kTwo) xl[y][i / 2][(i & 1) * 4 + e] = (_Float16)(X[y][i][e] - (float)h);
+                }
+        const float a = steps.a[step];
+        constexpr float kDown = 1.0f / (1 << kLog2A);
+        const uint32_t b = lds_address(smem) + lane * 16;
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            f32x4 sum[kStrips];
+#pragma unroll
+            for (int y = 0; y < kStrips; ++y) sum[y] = f32x4{};
+#pragma unroll
+            for (int k = 0; k < R / 2; ++k) {
+                const h8 bh = lds_h8(b + (i * (SP / 32) + k) * 1024);
+#pragma unroll
+                for (int y = 0; y < kStrips; ++y) sum[y] = __builtin_amdgcn_mfma_f32_16x16x32_f16(bh, xh[y][k], sum[y], 0, 0, 0);
+                if (H::kTwo) {
+                    const h8 bl = lds_h8(b + SP * SP * 2 + (i * (SP / 32) + k) * 1024);
+#pragma unroll
+                    for (int y = 0; y < kStrips; ++y) {
+                        sum[y] = __builtin_amdgcn_mfma_f32_16x16x32_f16(bh, xl[y][k], sum[y], 0, 0, 0);
+                        sum[y] = __builtin_amdgcn_mfma_f32_16x16x32_f16(bl, xh[y][k], sum[y], 0, 0, 0);
+                    }
+                }
+            }
+#pragma unroll
+            for (int y = 0; y < kStrips; ++y)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) X[y][i][e] = fmaf(a, X[y][i][e], sum[y][e] * kDown);
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int y = 0; y < kStrips; ++y)
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) stage[(i * 16 + row + e) * H::kStageLd + own + y * 16] = X[y][i][e];
+    __syncthreads();
+    const float back = ldexpf(1.0f, -m.log2_scale);
+    if (m.odt == ZERO_F16) store_chunk<SP, ZERO_F16>(m, column, stage, back);
+    else store_chunk<SP, ZERO_BF16>(m, column, stage, back);
+}
+
+// ---------------------------------------------------------------- host side
+
+int padded(int64_t s) { return s <= 32 ? 32 : s <= 64 ? 64 : 128; }
+
+template <int SP>
+int launch_thin_sp(const OrthoPass& p, const NsRef& ref, const ThinSteps& steps, double eps, hipStream_t s) {
+    hipLaunchKernelGGL(thin_gram<SP>, dim3((unsigned)p.n_sym), dim3(kThreads), 0, s, ref, p.sym_first);
+    int rc = launch_status("thin_gram");
+    if (rc != ZERO_OK) return rc;
+    hipLaunchKernelGGL(thin_steps<SP>, dim3((unsigned)p.n_items), dim3(64 * Thin<SP>::kWaves2), 0, s, ref, p.first_item, steps, eps);
+    rc = launch_status("thin_steps");
+    if (rc != ZERO_OK) return rc;
+    hipLaunchKernelGGL(thin_apply<SP>, dim3((unsigned)p.n_x), dim3(kThreads), 0, s, ref, p.x_first, steps);
+    return launch_status("thin_apply");
+}
+
+}  // namespace
+
+int launch_thin(const OrthoPass& pass, const NsRef& ref, const ThinSteps& steps, double eps, hipStream_t stream) {
+    if (pass.tile == -128) return launch_thin_sp<128>(pass, ref, steps, eps, stream);
+    if (pass.tile == -64) return launch_thin_sp<64>(pass, ref, steps, eps, stream);
+    return launch_thin_sp<32>(pass, ref, steps, eps, stream);
+}
+
+int plan_thin(const std::vector<OrthoMatrix>& matrices, OrthoPlan* plan) {
+    for (const int sp : {128, 64, 32}) {
+        const int tiles = sp / 16 * (sp / 16 + 1) / 2;
+        const int64_t b_bytes = 2 * (sp == 128 ? Thin<128>::kB : sp == 64 ? Thin<64>::kB : Thin<32>::kB);
+        OrthoPass pass{};
+        int64_t at = 0;
+        size_t first = plan->items.size();
+        const auto finish = [&]() {
+            if (plan->items.size() == first) return;
+            std::vector<ThinItem> items(plan->items.size() - first);
+            std::memcpy(items.data(), plan->items.data() + first, items.size() * sizeof(ThinItem));
+            pass.tile = -sp;
+            pass.first_item = (int64_t)first;
+            pass.n_items = (int32_t)(plan->items.size() - first);
+            pass.sym_first = (int64_t)plan->tiles.size();
+            for (size_t k = first; k < plan->items.size(); ++k)
+                for (int p = 0; p < items[k - first].n_parts; ++p) plan->tiles.push_back({(uint32_t)k, (uint16_t)p, 0});
+            pass.n_sym = (int64_t)plan->tiles.size() - pass.sym_first;
+            pass.x_first = (int64_t)plan->tiles.size();
+            for (size_t k = first; k < plan->items.size(); ++k)
+                for (int c = 0; c < items[k - first].n_chunks; ++c) plan->tiles.push_back({(uint32_t)k, (uint16_t)c, 0});
+            pass.n_x = (int64_t)plan->tiles.size() - pass.x_first;
+            plan->passes.push_back(pass);
+            plan->workspace = std::max(plan->workspace, at);
+            first = plan->items.size();
+            at = 0;
+        };
+        for (const OrthoMatrix& m : matrices) {
+            const int64_t s = std::min(m.rows, m.cols), l = std::max(m.rows, m.cols);
+            if (s > kThin || padded(s) != sp) continue;
+            ThinItem it{};
+            it.in = m.in;
+            it.out = m.out;
+            it.tall = m.rows > m.cols;
+            it.s = (int32_t)s;
+            it.l = (int32_t)l;
+            it.sp = sp;
+            it.udt = m.udt;
+            it.odt = m.odt;
+            it.log2_scale = log2_scale(l);
+            it.n_chunks = (int32_t)((l + kChunkElements / sp - 1) / (kChunkElements / sp));
+            // at least sp / 32 chunks a part, and no more than 2 MB of parts: one
+            // workgroup sums them
+            const int64_t most = (int64_t(2) << 20) / (tiles * 1024);
+            it.chunks_per_part = std::max<int64_t>(sp / 32, (it.n_chunks + most - 1) / most);
+            it.n_parts = (int32_t)((it.n_chunks + it.chunks_per_part - 1) / it.chunks_per_part);
+            const int64_t need = pad_to((int64_t)it.n_parts * tiles * 1024, 256) + pad_to((int64_t)it.n_parts * 4, 256) +
+                                 ZERO_MAX_ORTHO_STEPS * b_bytes + 256;
+            if (at + need > kPassBytes || plan->items.size() - first >= 1 << 20) finish();
+            it.parts = place(&at, (int64_t)it.n_parts * tiles * 1024);
+            it.exponents = place(&at, (int64_t)it.n_parts * 4);
+            it.q = place(&at, ZERO_MAX_ORTHO_STEPS * b_bytes);
+            it.factor = place(&at, sizeof(double));
+            MatrixItem slot;
+            std::memcpy(&slot, &it, sizeof(it));
+            plan->items.push_back(slot);
+        }
+        finish();
+    }
+    return ZERO_OK;
+}
+
+}  // namespace zero_shard
