@@ -155,11 +155,57 @@ __device__ __forceinline__ h8 chunk_fragment(uint32_t lds, bool tall, int i, int
     return lds_h8(lds + r * (Thin<SP>::kLC * 2) + (((kk * 4 + (lane >> 4)) ^ (r & 15)) << 4));
 }
 
-// One part of an item: chunks_per_part chunks, summed in order.
-template <int SP>
-__global__ __launch_bounds__(kThreads) void thin_gram(NsRef ref, int64_t first) {
+// The products of a chunk.  SP 128: a wave owns tile rows `wave` and 7 - wave,
+// nine tiles.  Else: all tiles, on every fourth step of the inner dimension.
+template <int SP, bool TWO>
+__device__ __forceinline__ void chunk_products(f32x4* acc, uint32_t hi, uint32_t lo, bool tall, int wave, int lane) {
     using H = Thin<SP>;
     constexpr int R = H::kR;
+    const auto product = [&](f32x4& into, const h8& ih, const h8& il, const h8& jh, const h8& jl) {
+        into = __builtin_amdgcn_mfma_f32_16x16x32_f16(ih, jh, into, 0, 0, 0);
+        if constexpr (TWO) {
+            into = __builtin_amdgcn_mfma_f32_16x16x32_f16(ih, jl, into, 0, 0, 0);
+            into = __builtin_amdgcn_mfma_f32_16x16x32_f16(il, jh, into, 0, 0, 0);
+        }
+    };
+    const auto low = [&](int i, int kk) {
+        if constexpr (TWO) return chunk_fragment<SP>(lo, tall, i, kk, lane);
+        else return h8{};
+    };
+    if constexpr (SP == 128) {
+#pragma unroll 1
+        for (int kk = 0; kk < H::kLC / 32; ++kk) {
+            const h8 ah = chunk_fragment<SP>(hi, tall, wave, kk, lane), al = low(wave, kk);
+            const h8 bh = chunk_fragment<SP>(hi, tall, 7 - wave, kk, lane), bl = low(7 - wave, kk);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if (j > 7 - wave) continue;
+                const h8 jh = chunk_fragment<SP>(hi, tall, j, kk, lane), jl = low(j, kk);
+                product(acc[4 + j], bh, bl, jh, jl);
+                if (j < 4 && j <= wave) product(acc[j], ah, al, jh, jl);
+            }
+        }
+    } else {
+#pragma unroll 1
+        for (int kk = wave; kk < H::kLC / 32; kk += kThreads / 64) {
+            h8 fh[R], fl[R];
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                fh[i] = chunk_fragment<SP>(hi, tall, i, kk, lane);
+                fl[i] = low(i, kk);
+            }
+#pragma unroll
+            for (int i = 0; i < R; ++i)
+#pragma unroll
+                for (int j = 0; j <= i; ++j) product(acc[i * (i + 1) / 2 + j], fh[i], fl[i], fh[j], fl[j]);
+        }
+    }
+}
+
+// One part of an item: chunks_per_part chunks, summed in order.
+template <int SP>
+__global__ __launch_bounds__(kThreads, 2) void thin_gram(NsRef ref, int64_t first) {
+    using H = Thin<SP>;
     if (ref.skipped()) return;
     __shared__ __attribute__((aligned(1024))) char smem[2 * kChunkElements * 2];
     __shared__ uint32_t s_top[kThreads / 64];
@@ -168,8 +214,6 @@ __global__ __launch_bounds__(kThreads) void thin_gram(NsRef ref, int64_t first) 
     const int part = t.i, lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t hi = lds_address(smem), lo = hi + kChunkElements * 2;
     const bool two = m.udt == ZERO_F32, tall = m.tall != 0;
-    // SP 128: a wave owns tile rows `wave` and 7 - wave, nine tiles.  Else: all
-    // tiles, on every fourth step of the chunk's inner dimension.
     constexpr int kOwn = SP == 128 ? 12 : H::kTiles;
     f32x4 acc[kOwn];
 #pragma unroll
@@ -177,9 +221,9 @@ __global__ __launch_bounds__(kThreads) void thin_gram(NsRef ref, int64_t first) 
     int run = INT_MIN / 4;                       // exponent that the sums are scaled by
     bool bad = false;
     const int64_t c_end = (part + 1) * m.chunks_per_part < m.n_chunks ? (part + 1) * m.chunks_per_part : m.n_chunks;
+    float x[8][8];
+    load_chunk<SP>(m, part * m.chunks_per_part * H::kLC, x);
     for (int64_t chunk = part * m.chunks_per_part; chunk < c_end; ++chunk) {
-        float x[8][8];
-        load_chunk<SP>(m, chunk * H::kLC, x);
         uint32_t top = 0;
 #pragma unroll
         for (int n = 0; n < 8; ++n)
@@ -225,45 +269,10 @@ __global__ __launch_bounds__(kThreads) void thin_gram(NsRef ref, int64_t first) 
             *reinterpret_cast<h8*>(smem + at) = h;
             if (two) *reinterpret_cast<h8*>(smem + kChunkElements * 2 + at) = g;
         }
+        if (chunk + 1 < c_end) load_chunk<SP>(m, (chunk + 1) * H::kLC, x);      // on its way during the products
         __syncthreads();
-        const auto product = [&](f32x4& into, const h8& ih, const h8& il, const h8& jh, const h8& jl) {
-            into = __builtin_amdgcn_mfma_f32_16x16x32_f16(ih, jh, into, 0, 0, 0);
-            if (two) {
-                into = __builtin_amdgcn_mfma_f32_16x16x32_f16(ih, jl, into, 0, 0, 0);
-                into = __builtin_amdgcn_mfma_f32_16x16x32_f16(il, jh, into, 0, 0, 0);
-            }
-        };
-        if constexpr (SP == 128) {
-            for (int kk = 0; kk < H::kLC / 32; ++kk) {
-                const h8 ah = chunk_fragment<SP>(hi, tall, wave, kk, lane), bh = chunk_fragment<SP>(hi, tall, 7 - wave, kk, lane);
-                h8 al{}, bl{};
-                if (two) {
-                    al = chunk_fragment<SP>(lo, tall, wave, kk, lane);
-                    bl = chunk_fragment<SP>(lo, tall, 7 - wave, kk, lane);
-                }
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    if (j > 7 - wave) continue;
-                    const h8 jh = chunk_fragment<SP>(hi, tall, j, kk, lane);
-                    const h8 jl = two ? chunk_fragment<SP>(lo, tall, j, kk, lane) : h8{};
-                    product(acc[4 + j], bh, bl, jh, jl);
-                    if (j < 4 && j <= wave) product(acc[j], ah, al, jh, jl);
-                }
-            }
-        } else {
-            for (int kk = wave; kk < H::kLC / 32; kk += kThreads / 64) {
-                h8 fh[R], fl[R];
-#pragma unroll
-                for (int i = 0; i < R; ++i) {
-                    fh[i] = chunk_fragment<SP>(hi, tall, i, kk, lane);
-                    fl[i] = two ? chunk_fragment<SP>(lo, tall, i, kk, lane) : h8{};
-                }
-#pragma unroll
-                for (int i = 0; i < R; ++i)
-#pragma unroll
-                    for (int j = 0; j <= i; ++j) product(acc[i * (i + 1) / 2 + j], fh[i], fl[i], fh[j], fl[j]);
-            }
-        }
+        if (two) chunk_products<SP, true>(acc, hi, lo, tall, wave, lane);
+        else chunk_products<SP, false>(acc, hi, lo, tall, wave, lane);
     }
     float* out = reinterpret_cast<float*>(ref.ws + m.parts) + (int64_t)part * H::kTiles * 256;
     if constexpr (SP == 128) {
@@ -388,6 +397,7 @@ __global__ __launch_bounds__(64 * Thin<SP>::kWaves2) void thin_steps(NsRef ref, 
         tj[k] = tile - i * (i + 1) / 2;
         A[k] = f32x4{};
     }
+#pragma unroll 8
     for (int p = 0; p < m.n_parts; ++p) {
         const f32x4* part = reinterpret_cast<const f32x4*>(ref.ws + m.parts) + (int64_t)p * H::kTiles * 64;
         const int down = exponents[p] < INT_MIN / 8 ? 0 : 2 * (exponents[p] - top);
@@ -406,8 +416,8 @@ __global__ __launch_bounds__(64 * Thin<SP>::kWaves2) void thin_steps(NsRef ref, 
             s_diag[16 * ti[k] + (lane & 15)] = (double)(e == 0 ? A[k][0] : e == 1 ? A[k][1] : e == 2 ? A[k][2] : A[k][3]);
         }
     __syncthreads();
-    double trace = 0.0;
-    for (int k = 0; k < SP; ++k) trace += s_diag[k];
+    double trace = s_diag[lane % SP] + (SP == 128 ? s_diag[lane + 64] : 0.0);
+    for (int off = (SP < 64 ? SP : 64) / 2; off > 0; off >>= 1) trace += __shfl_xor(trace, off, 64);
     const int up = top < INT_MIN / 8 || bad ? 0 : top;
     const double norm = ldexp(sqrt(trace), up);
     const double by = norm > eps ? norm : eps;
@@ -495,7 +505,7 @@ __global__ __launch_bounds__(kThreads) void thin_apply(NsRef ref, int64_t first,
     constexpr int R = H::kR, kStrips = H::kLC / 64, kB = H::kB, kLoads = kB / 8 / kThreads;
     if (ref.skipped()) return;
     __shared__ __attribute__((aligned(1024))) char smem[SP * H::kStageLd * 4];
-    static_assert(kB * 2 <= SP * H::kStageLd * 4 && kLoads * 8 * kThreads == kB, "B takes the stage's place");
+    static_assert(kB * 4 <= SP * H::kStageLd * 4 && kLoads * 8 * kThreads == kB, "two steps' B take the stage's place");
     const ZS_CONSTANT TileRef& t = ref.tile(first + blockIdx.x);
     const ZS_CONSTANT ThinItem& m = ((const ZS_CONSTANT ThinItem*)ref.items)[t.item];
     const int64_t column = (int64_t)t.i * H::kLC;
@@ -504,19 +514,22 @@ __global__ __launch_bounds__(kThreads) void thin_apply(NsRef ref, int64_t first,
     {
         float x[8][8];
         load_chunk<SP>(m, column, x);
-        const double f = ldexp(*reinterpret_cast<const double*>(ref.ws + m.factor), m.log2_scale);
+        // x * factor as x * 2^e * f, f in [0.5, 1): neither the factor nor a product leaves float32
+        int e;
+        const float f = (float)frexp(*reinterpret_cast<const double*>(ref.ws + m.factor), &e);
+        e += m.log2_scale;
 #pragma unroll
         for (int n = 0; n < 8; ++n) {
             const Vector<SP> v(m, column, n);
             float* to = stage + v.r * H::kStageLd + v.c;
             if (m.tall) {
 #pragma unroll
-                for (int k = 0; k < 8; ++k) to[k * H::kStageLd] = (float)((double)x[n][k] * f);
+                for (int k = 0; k < 8; ++k) to[k * H::kStageLd] = ldexpf(x[n][k], e) * f;
             } else {
 #pragma unroll
                 for (int k = 0; k < 8; k += 4)
-                    *reinterpret_cast<f32x4*>(to + k) = f32x4{(float)((double)x[n][k] * f), (float)((double)x[n][k + 1] * f),
-                                                              (float)((double)x[n][k + 2] * f), (float)((double)x[n][k + 3] * f)};
+                    *reinterpret_cast<f32x4*>(to + k) = f32x4{ldexpf(x[n][k], e) * f, ldexpf(x[n][k + 1], e) * f,
+                                                              ldexpf(x[n][k + 2], e) * f, ldexpf(x[n][k + 3], e) * f};
             }
         }
     }
@@ -533,10 +546,12 @@ __global__ __launch_bounds__(kThreads) void thin_apply(NsRef ref, int64_t first,
         for (int i = 0; i < R; ++i)
 #pragma unroll
             for (int e = 0; e < 4; ++e) X[y][i][e] = stage[(i * 16 + row + e) * H::kStageLd + own + y * 16];
+    __syncthreads();                                          // the stage has been read
     for (int step = 0; step < steps.n; ++step) {
-        __syncthreads();                                      // the stage, or the last step's B, has been read
+        // in turn in two places: where this one goes was last read before the last barrier
+        char* const place = smem + (step & 1) * kB * 2;
 #pragma unroll
-        for (int k = 0; k < kLoads; ++k) reinterpret_cast<u32x4*>(smem)[k * kThreads + threadIdx.x] = ahead[k];
+        for (int k = 0; k < kLoads; ++k) reinterpret_cast<u32x4*>(place)[k * kThreads + threadIdx.x] = ahead[k];
         if (step + 1 < steps.n) {
             q += kB / 8;
 #pragma unroll
@@ -556,7 +571,7 @@ __global__ __launch_bounds__(kThreads) void thin_apply(NsRef ref, int64_t first,
                 }
         const float a = steps.a[step];
         constexpr float kDown = 1.0f / (1 << kLog2A);
-        const uint32_t b = lds_address(smem) + lane * 16;
+        const uint32_t b = lds_address(place) + lane * 16;
 #pragma unroll
         for (int i = 0; i < R; ++i) {
             f32x4 sum[kStrips];
