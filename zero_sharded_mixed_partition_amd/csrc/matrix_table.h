@@ -81,6 +81,7 @@ struct OrthoPass {
     int64_t first_item;
     int64_t sym_first, n_sym;           // tiles of the symmetric products, lower triangle
     int64_t x_first, n_x;               // tiles of the iterate
+    int64_t piece_first, n_pieces;      // pieces in which U is read (not of thin ones)
 };
 
 enum { kCanMomentum = 1, kCanOrtho = 2, kCanUpdate = 4 };

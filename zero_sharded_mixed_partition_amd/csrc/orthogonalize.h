@@ -56,6 +56,104 @@ __device__ __forceinline__ h4 lds_column(uint32_t a) {
     return __builtin_bit_cast(h4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4*)(uintptr_t)a));
 }
 
+// ---------------------------------------------------------------- boxes of U
+
+constexpr int kThreads = 256;
+constexpr int kChunkElements = 16384;            // of a box: 64 a thread, as eight vectors of eight
+
+// Eight consecutive elements, the first `valid` of them; whole: eight may be read.
+template <int DT>
+__device__ __forceinline__ void ld8(const void* U, int64_t e, int valid, bool whole, float v[8]) {
+    if (whole) {
+        if constexpr (DT == ZERO_F32) {
+            const f32x4 a = ld_any(static_cast<const float*>(U) + e), b = ld_any(static_cast<const float*>(U) + e + 4);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                v[k] = a[k];
+                v[k + 4] = b[k];
+            }
+        } else {
+            const u32x4 w = ld16_any(static_cast<const uint16_t*>(U) + e);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) unpack2<DT>(w[k], v[2 * k], v[2 * k + 1]);
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = k < valid ? v[k] : 0.0f;
+    } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = k < valid ? ld_grad1<DT>(U, e + k) : 0.0f;
+    }
+}
+
+// A thread's n-th vector of a box of ROWS x 16384 / ROWS elements at (r0, c0) of
+// the s x l matrix, which the caller holds transposed if it is tall: along the
+// columns of a wide matrix, along the rows of a tall one.  BAND rows of a wide
+// one come before the next columns.
+template <int ROWS, int BAND>
+struct Vector8 {
+    int r, c;                                    // in the box
+    int64_t at;                                  // of the first element, in the caller's matrix
+    int valid;
+
+    __device__ __forceinline__ Vector8(int s, int l, int tall, int r0, int64_t c0, int n) {
+        constexpr int kAcross = kChunkElements / ROWS / 8;                     // vectors along a row
+        constexpr int kBandAcross = kAcross * BAND / ROWS;                     // ... of a band of 256 / BAND vectors
+        const int v = n * kThreads + threadIdx.x;
+        if (tall) {
+            r = v % (ROWS / 8) * 8;
+            c = v / (ROWS / 8);
+            at = (c0 + c) * s + r0 + r;
+            valid = c0 + c < l ? s - r0 - r : 0;
+        } else {
+            if constexpr (BAND == ROWS) {
+                r = v / kAcross;
+                c = v % kAcross * 8;
+            } else {
+                r = v / kBandAcross % ROWS;
+                c = (v / (kBandAcross * ROWS) * kBandAcross + v % kBandAcross) * 8;
+            }
+            at = (int64_t)(r0 + r) * l + c0 + c;
+            const int64_t left = l - c0 - c;
+            valid = r0 + r < s ? (int)(left < 8 ? left : 8) : 0;
+        }
+        valid = valid < 0 ? 0 : valid > 8 ? 8 : valid;
+    }
+};
+
+template <int ROWS, int BAND, int DT>
+__device__ __forceinline__ void load_box(const void* U, int s, int l, int tall, int r0, int64_t c0, float x[8][8]) {
+    constexpr int kColumns = kChunkElements / ROWS;
+    const int64_t all = (int64_t)s * l;
+    // a vector may run over its row's end into the next row, but not over the matrix's
+    const int64_t r_last = (r0 + ROWS < s ? r0 + ROWS : s) - 1, c_last = (c0 + kColumns < l ? c0 + kColumns : l) - 1;
+    const int64_t last = tall ? c_last * s + r_last : r_last * (int64_t)l + c_last;
+    if (last + 8 <= all) {
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+            const Vector8<ROWS, BAND> v(s, l, tall, r0, c0, n);
+            ld8<DT>(U, v.valid ? v.at : 0, v.valid, true, x[n]);
+        }
+    } else {
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+            const Vector8<ROWS, BAND> v(s, l, tall, r0, c0, n);
+            ld8<DT>(U, v.valid ? v.at : 0, v.valid, v.valid > 0 && v.at + 8 <= all, x[n]);
+        }
+    }
+}
+
+template <int ROWS, int BAND>
+__device__ __forceinline__ void load_box(int dt, const void* U, int s, int l, int tall, int r0, int64_t c0, float x[8][8]) {
+    if (dt == ZERO_F16) load_box<ROWS, BAND, ZERO_F16>(U, s, l, tall, r0, c0, x);
+    else if (dt == ZERO_BF16) load_box<ROWS, BAND, ZERO_BF16>(U, s, l, tall, r0, c0, x);
+    else load_box<ROWS, BAND, ZERO_F32>(U, s, l, tall, r0, c0, x);
+}
+
+// x * f * 2^e: with f in [0.5, 1) no product leaves float32 that the result does not.
+__device__ __forceinline__ float scaled(float x, float f, int e) { return ldexpf(x, e) * f; }
+
+// ---------------------------------------------------------------- host side
+
 inline int64_t pad_to(int64_t x, int64_t t) { return (x + t - 1) / t * t; }
 
 inline int64_t place(int64_t* at, int64_t bytes) {

@@ -34,24 +34,6 @@ enum { kGram, kPoly, kApply };
 
 // ---------------------------------------------------------------- load and norm
 
-template <int DT>
-__device__ __forceinline__ void ld4(const void* U, int64_t e, int valid, float v[4]) {
-    if (valid >= 4) {
-        Grad4<DT> q;
-        q.load(U, e);
-        q.values(v);
-        return;
-    }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = k < valid ? ld_grad1<DT>(U, e + k) : 0.0f;
-}
-
-__device__ __forceinline__ void ld4(int dt, const void* U, int64_t e, int valid, float v[4]) {
-    if (dt == ZERO_F16) ld4<ZERO_F16>(U, e, valid, v);
-    else if (dt == ZERO_BF16) ld4<ZERO_BF16>(U, e, valid, v);
-    else ld4<ZERO_F32>(U, e, valid, v);
-}
-
 // Where element (r, c) of a matrix of `rows` rows is in the workspace: panels
 // of 32 columns, each with its rows end to end.  A stage of either operand of
 // any product is then made of runs of at least 1 KB.
@@ -59,36 +41,35 @@ __device__ __forceinline__ int64_t panel_at(int64_t r, int64_t c, int64_t rows) 
     return ((c / kPanel) * rows + r) * kPanel + c % kPanel;
 }
 
-// The caller's rows and columns of a tile of the iterate.
-struct TileBox {
-    int r0, c0, rows, cols;                      // the caller's matrix
-};
+// U is read in pieces of 64 rows and 256 columns (of the s x l matrix), whatever
+// the tiles: the norm's sums, and so the results, do not depend on them.
+constexpr int kPieceRows = 64, kPieceColumns = kChunkElements / kPieceRows;
 
-__device__ __forceinline__ TileBox tile_box(const ZS_CONSTANT MatrixItem& m, const ZS_CONSTANT TileRef& t, int tile) {
-    const int i = t.i * tile, j = t.j * tile;
-    return m.tall ? TileBox{j, i, m.l, m.s} : TileBox{i, j, m.s, m.l};
+template <int D>
+__device__ __forceinline__ void load_piece(const ZS_CONSTANT MatrixItem& m, int r0, int c0, float x[8][8]) {
+    load_box<kPieceRows, D>(m.udt, m.in, m.s, m.l, m.tall, r0, c0, x);
 }
 
-// One tile's sum of squares into its slot.
-__global__ __launch_bounds__(kBlock) void ortho_squares(NsRef ref, int64_t first, int tile) {
+// One piece's sum of squares into its slot.
+__global__ __launch_bounds__(kBlock) void ortho_squares(NsRef ref, int64_t first) {
     if (ref.skipped()) return;
     __shared__ double s_sq[kWaves];
     __shared__ uint32_t s_bad[kWaves];
     const ZS_CONSTANT TileRef& t = ref.tile(first + blockIdx.x);
     const ZS_CONSTANT MatrixItem& m = ref.item(t.item);
-    const TileBox box = tile_box(m, t, tile);
+    const int r0 = t.i * kPieceRows, c0 = t.j * kPieceColumns;
+    if (r0 >= m.s || c0 >= m.l) return;                      // padding alone
+    float x[8][8];
+    load_piece<kPieceRows>(m, r0, c0, x);
     double acc = 0.0;
-    for (int k = threadIdx.x; k < tile * tile / 4; k += kBlock) {
-        const int r = box.r0 + k / (tile / 4), c = box.c0 + k % (tile / 4) * 4;
-        if (r >= box.rows || c >= box.cols) continue;
-        float v[4];
-        ld4(m.udt, m.in, (int64_t)r * box.cols + c, box.cols - c, v);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc = fma((double)v[e], (double)v[e], acc);
-    }
+    for (int n = 0; n < 8; ++n)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) acc = fma((double)x[n][k], (double)x[n][k], acc);
     uint32_t none = 0;
     block_reduce(acc, none, s_sq, s_bad);
-    if (threadIdx.x == 0) reinterpret_cast<double*>(ref.ws + m.slots)[t.i * (m.lp / tile) + t.j] = acc;
+    if (threadIdx.x == 0)
+        reinterpret_cast<double*>(ref.ws + m.slots)[(int64_t)t.i * ((m.l + kPieceColumns - 1) / kPieceColumns) + t.j] = acc;
 }
 
 // The factor 2^log2_scale / max(|U|_F, eps); NaN if U is not finite, so that all of the result is.
@@ -107,37 +88,46 @@ __device__ __forceinline__ double norm_factor(const ZS_CONSTANT MatrixItem& m, c
     return by > 0.0 ? ldexp(1.0, m.log2_scale) / by : 0.0;
 }
 
-// The tile of X = U * factor, with its padding, in 64 x 64 blocks.
-__global__ __launch_bounds__(kBlock) void ortho_load(NsRef ref, int64_t first, int tile, double eps) {
+// A piece of X = U * factor, with its padding.
+__global__ __launch_bounds__(kBlock) void ortho_load(NsRef ref, int64_t first, double eps) {
     if (ref.skipped()) return;
     __shared__ double s_sq[kWaves];
     __shared__ uint32_t s_bad[kWaves];
-    __shared__ _Float16 block[64][68];
+    __shared__ __attribute__((aligned(16))) _Float16 block[kPieceRows][kPieceColumns + 8];
     const ZS_CONSTANT TileRef& t = ref.tile(first + blockIdx.x);
     const ZS_CONSTANT MatrixItem& m = ref.item(t.item);
-    const double f = norm_factor(m, ref.ws, eps, s_sq, s_bad);
-    const TileBox box = tile_box(m, t, tile);
-    _Float16* X = reinterpret_cast<_Float16*>(ref.ws + m.x0);
-    const int p = threadIdx.x / 16, q = threadIdx.x % 16 * 4;
-    for (int sub = 0; sub < (tile / 64) * (tile / 64); ++sub) {
-        const int r0 = box.r0 + sub / (tile / 64) * 64, c0 = box.c0 + sub % (tile / 64) * 64;
-        for (int k = p; k < 64; k += 16) {
-            const int r = r0 + k, c = c0 + q;
-            float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            if (r < box.rows && c < box.cols) ld4(m.udt, m.in, (int64_t)r * box.cols + c, box.cols - c, v);
-            h4 h;
+    const int r0 = t.i * kPieceRows, c0 = t.j * kPieceColumns;
+    float x[8][8];
+    if (r0 < m.s && c0 < m.l) {
+        load_piece<8>(m, r0, c0, x);
+    } else {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) h[e] = r < box.rows && c + e < box.cols ? (_Float16)(float)((double)v[e] * f) : (_Float16)0;
-            if (m.tall) *reinterpret_cast<h4*>(&block[k][q]) = h;
-            else *reinterpret_cast<h4*>(X + panel_at(r, c, m.sp)) = h;
+        for (int n = 0; n < 8; ++n)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) x[n][k] = 0.0f;
+    }
+    int e;
+    const float f = (float)frexp(norm_factor(m, ref.ws, eps, s_sq, s_bad), &e);
+    _Float16* X = reinterpret_cast<_Float16*>(ref.ws + m.x0);
+#pragma unroll
+    for (int n = 0; n < 8; ++n) {
+        const Vector8<kPieceRows, 8> v(m.s, m.l, m.tall, r0, c0, n);
+        h8 h;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) h[k] = k < v.valid ? (_Float16)scaled(x[n][k], f, e) : (_Float16)0;
+        if (m.tall) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) block[v.r + k][v.c] = h[k];
+        } else if (c0 + v.c < m.lp) {
+            *reinterpret_cast<h8*>(X + panel_at(r0 + v.r, c0 + v.c, m.sp)) = h;
         }
-        if (!m.tall) continue;
-        __syncthreads();
-        for (int k = p; k < 64; k += 16) {
-            const h4 h = {block[q][k], block[q + 1][k], block[q + 2][k], block[q + 3][k]};
-            *reinterpret_cast<h4*>(X + panel_at(c0 + k, r0 + q, m.sp)) = h;
-        }
-        __syncthreads();
+    }
+    if (!m.tall) return;
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < 8; ++n) {
+        const Vector8<kPieceRows, 8> v(m.s, m.l, 0, r0, c0, n);
+        if (c0 + v.c < m.lp) *reinterpret_cast<h8*>(X + panel_at(r0 + v.r, c0 + v.c, m.sp)) = *reinterpret_cast<const h8*>(&block[v.r][v.c]);
     }
 }
 
@@ -406,7 +396,35 @@ __global__ __launch_bounds__(64 * WM * WN) void ortho_product(NsRef ref, int64_t
 
 // ---------------------------------------------------------------- host side
 
-int tile_of(int64_t s) { return s >= 1024 ? 256 : s > 256 ? 128 : 64; }
+// What one step of the products is taken to cost with tiles of this size, in
+// microseconds: per product the larger of one tile's chain of stages and of all
+// tiles over the CUs.  A tile costs c0 besides its stages (start, first loads,
+// stores), and a chain of stages alone in its CU is slower than several (c1
+// against c1_full).  Measured with every size (64, 128, 256) on 19 lists: one of
+// 512 x 512 takes 86, 166 and 364 us, 64 of 512 x 2048 1427, 1310 and 1267, one
+// of 4096 x 4096 2109, 1693 and 1589, 4 of 1024 x 4096 578, 558 and 840; the
+// size that this picks is within 8% of the fastest on all of them.
+double step_cost(const std::vector<OrthoMatrix>& matrices, int tile) {
+    const double c0 = tile == 256 ? 21.0 : tile == 128 ? 4.8 : 0.82, first = tile == 256 ? 13.5 : tile == 128 ? 5.0 : 2.1;
+    const double c1 = tile == 256 ? 0.68 : tile == 128 ? 0.30 : 0.20, c1_full = tile == 256 ? 0.68 : tile == 128 ? 0.32 : 0.105;
+    double cost = 0.0;
+    for (int product = 0; product < 3; ++product) {
+        double tiles = 0.0, work = 0.0, deepest = 0.0;
+        for (const OrthoMatrix& m : matrices) {
+            const int64_t s = std::min(m.rows, m.cols), l = std::max(m.rows, m.cols);
+            if (s <= kThin) continue;
+            const double n = (double)((s + tile - 1) / tile), nl = (double)((l + tile - 1) / tile);
+            const double k = product == kApply ? n * nl : n * (n + 1) / 2, depth = stages_of((int)(product == kGram ? l : s));
+            tiles += k;
+            work += k * depth;
+            deepest = std::max(deepest, depth);
+        }
+        double full = (work * c1_full + tiles * c0) / 256;
+        if (tile == 256) full *= std::ceil(tiles / 256) / (tiles / 256);       // one tile a CU
+        cost += std::max(first + c1 * deepest, full);
+    }
+    return cost;
+}
 
 // Blocks go to the eight XCDs in turn.  A run of tiles of equal depth is dealt
 // out so that each XCD takes a part of it whose tiles share their operands in
@@ -492,57 +510,64 @@ int check_coefs(const double* coefs, int32_t n_steps) {
 }  // namespace
 
 int plan_ortho(const std::vector<OrthoMatrix>& matrices, OrthoPlan* plan) {
-    for (const int tile : {256, 128, 64}) {
-        std::vector<MatrixItem> mine;
-        int64_t total = 0;
-        for (const OrthoMatrix& m : matrices) {
-            if (std::min(m.rows, m.cols) <= kThin || tile_of(std::min(m.rows, m.cols)) != tile) continue;
-            MatrixItem it{};
-            it.in = m.in;
-            it.out = m.out;
-            it.tall = m.rows > m.cols;
-            it.s = (int32_t)std::min(m.rows, m.cols);
-            it.l = (int32_t)std::max(m.rows, m.cols);
-            it.sp = (int32_t)pad_to(it.s, tile);
-            it.lp = (int32_t)pad_to(it.l, tile);
-            it.udt = m.udt;
-            it.odt = m.odt;
-            it.log2_scale = log2_scale(it.l);
-            const int64_t n_tiles = (int64_t)(it.sp / tile) * (it.lp / tile);
-            if (n_tiles > INT32_MAX) return fail(ZERO_ERANGE, "a matrix of %d x %d is too large", it.s, it.l);
-            it.n_slots = (int32_t)n_tiles;
-            place_item(&it, &total);
-            mine.push_back(it);
+    std::vector<MatrixItem> mine;
+    int tile = 64;
+    for (const int other : {128, 256})
+        if (step_cost(matrices, other) < step_cost(matrices, tile)) tile = other;
+    int64_t total = 0;
+    for (const OrthoMatrix& m : matrices) {
+        if (std::min(m.rows, m.cols) <= kThin) continue;
+        MatrixItem it{};
+        it.in = m.in;
+        it.out = m.out;
+        it.tall = m.rows > m.cols;
+        it.s = (int32_t)std::min(m.rows, m.cols);
+        it.l = (int32_t)std::max(m.rows, m.cols);
+        it.sp = (int32_t)pad_to(it.s, tile);
+        it.lp = (int32_t)pad_to(it.l, tile);
+        it.udt = m.udt;
+        it.odt = m.odt;
+        it.log2_scale = log2_scale(it.l);
+        const int64_t n_slots = pad_to(it.s, kPieceRows) / kPieceRows * (pad_to(it.l, kPieceColumns) / kPieceColumns);
+        if (n_slots > INT32_MAX) return fail(ZERO_ERANGE, "a matrix of %d x %d is too large", it.s, it.l);
+        it.n_slots = (int32_t)n_slots;
+        place_item(&it, &total);
+        mine.push_back(it);
+    }
+    // as many passes as the workspace takes, of about equal size; in each the deepest products first
+    const int64_t share = total / ((total + kPassBytes - 1) / kPassBytes + !total) + 1;
+    for (size_t done = 0; done < mine.size();) {
+        OrthoPass pass{};
+        pass.tile = tile;
+        int64_t at = 0;
+        size_t end = done;
+        while (end < mine.size() && (end == done || at < share)) {
+            int64_t after = at;
+            place_item(&mine[end], &after);
+            if (end > done && after > kPassBytes) break;
+            at = after;
+            ++end;
         }
-        // as many passes as the workspace takes, of about equal size; in each the deepest products first
-        const int64_t share = total / ((total + kPassBytes - 1) / kPassBytes + !total) + 1;
-        for (size_t done = 0; done < mine.size();) {
-            OrthoPass pass{};
-            pass.tile = tile;
-            int64_t at = 0;
-            size_t end = done;
-            while (end < mine.size() && (end == done || at < share)) {
-                int64_t after = at;
-                place_item(&mine[end], &after);
-                if (end > done && after > kPassBytes) break;
-                at = after;
-                ++end;
-            }
-            plan->workspace = std::max(plan->workspace, at);
-            const size_t first_item = plan->items.size();
-            plan->items.insert(plan->items.end(), mine.begin() + done, mine.begin() + end);
-            pass.first_item = (int64_t)first_item;
-            pass.n_items = (int32_t)(end - done);
-            done = end;
-            pass.sym_first = (int64_t)plan->tiles.size();
-            add_tiles(plan, first_item, tile, true);
-            pass.n_sym = (int64_t)plan->tiles.size() - pass.sym_first;
-            pass.x_first = (int64_t)plan->tiles.size();
-            add_tiles(plan, first_item, tile, false);
-            pass.n_x = (int64_t)plan->tiles.size() - pass.x_first;
-            if (std::max(pass.n_x, pass.n_sym) > INT32_MAX) return fail(ZERO_ERANGE, "the list is too long");
-            plan->passes.push_back(pass);
-        }
+        plan->workspace = std::max(plan->workspace, at);
+        const size_t first_item = plan->items.size();
+        plan->items.insert(plan->items.end(), mine.begin() + done, mine.begin() + end);
+        pass.first_item = (int64_t)first_item;
+        pass.n_items = (int32_t)(end - done);
+        done = end;
+        pass.sym_first = (int64_t)plan->tiles.size();
+        add_tiles(plan, first_item, tile, true);
+        pass.n_sym = (int64_t)plan->tiles.size() - pass.sym_first;
+        pass.x_first = (int64_t)plan->tiles.size();
+        add_tiles(plan, first_item, tile, false);
+        pass.n_x = (int64_t)plan->tiles.size() - pass.x_first;
+        pass.piece_first = (int64_t)plan->tiles.size();
+        for (size_t k = first_item; k < plan->items.size(); ++k)
+            for (int i = 0; i < plan->items[k].sp / kPieceRows; ++i)
+                for (int j = 0; j < (int)(pad_to(plan->items[k].lp, kPieceColumns) / kPieceColumns); ++j)
+                    plan->tiles.push_back({(uint32_t)k, (uint16_t)i, (uint16_t)j});
+        pass.n_pieces = (int64_t)plan->tiles.size() - pass.piece_first;
+        if (std::max({pass.n_x, pass.n_sym, pass.n_pieces}) > INT32_MAX) return fail(ZERO_ERANGE, "the list is too long");
+        plan->passes.push_back(pass);
     }
     return plan_thin(matrices, plan);
 }
@@ -600,10 +625,10 @@ int zero_multi_orthogonalize(const void* table, const void* d_table, const doubl
             if (rc != ZERO_OK) return rc;
             continue;
         }
-        hipLaunchKernelGGL(ortho_squares, dim3((unsigned)pass.n_x), dim3(kBlock), 0, s, ref, pass.x_first, pass.tile);
+        hipLaunchKernelGGL(ortho_squares, dim3((unsigned)pass.n_pieces), dim3(kBlock), 0, s, ref, pass.piece_first);
         rc = launch_status("ortho_squares");
         if (rc != ZERO_OK) return rc;
-        hipLaunchKernelGGL(ortho_load, dim3((unsigned)pass.n_x), dim3(kBlock), 0, s, ref, pass.x_first, pass.tile, eps);
+        hipLaunchKernelGGL(ortho_load, dim3((unsigned)pass.n_pieces), dim3(kBlock), 0, s, ref, pass.piece_first, eps);
         rc = launch_status("ortho_load");
         for (int k = 0; k < n_steps && rc == ZERO_OK; ++k) {
             const NsStep step{(float)coefs[3 * k], (float)coefs[3 * k + 1], (float)coefs[3 * k + 2], k & 1, k + 1 == n_steps};

@@ -31,8 +31,6 @@
 namespace zero_shard {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kChunkElements = 16384;            // padded elements of U per chunk: 64 a thread
 
 template <int SP>
 struct Thin {
@@ -50,83 +48,12 @@ __device__ __forceinline__ int pair_index(int i, int j) { return i * (i + 1) / 2
 
 // ---------------------------------------------------------------- a chunk of U
 
-// Eight consecutive elements, the first `valid` of them; whole: eight may be read.
-template <int DT>
-__device__ __forceinline__ void ld8(const void* U, int64_t e, int valid, bool whole, float v[8]) {
-    if (whole) {
-        if constexpr (DT == ZERO_F32) {
-            const f32x4 a = ld_any(static_cast<const float*>(U) + e), b = ld_any(static_cast<const float*>(U) + e + 4);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                v[k] = a[k];
-                v[k + 4] = b[k];
-            }
-        } else {
-            const u32x4 w = ld16_any(static_cast<const uint16_t*>(U) + e);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) unpack2<DT>(w[k], v[2 * k], v[2 * k + 1]);
-        }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = k < valid ? v[k] : 0.0f;
-    } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = k < valid ? ld_grad1<DT>(U, e + k) : 0.0f;
-    }
-}
-
-// The caller's place of a thread's n-th vector of eight of a chunk: along the
-// long side for a wide matrix, along the short one for a tall one.
 template <int SP>
-struct Vector {
-    int r, c;                                    // in X: row, and column from the chunk's first
-    int64_t at;                                  // of its first element in the matrix
-    int valid;
-
-    __device__ __forceinline__ Vector(const ZS_CONSTANT ThinItem& m, int64_t first, int n) {
-        const int v = n * kThreads + threadIdx.x;
-        if (m.tall) {
-            r = v % (SP / 8) * 8;
-            c = v / (SP / 8);
-            at = (first + c) * m.s + r;
-            valid = first + c < m.l ? m.s - r : 0;
-        } else {
-            r = v / (Thin<SP>::kLC / 8);
-            c = v % (Thin<SP>::kLC / 8) * 8;
-            at = r * (int64_t)m.l + first + c;
-            const int64_t left = m.l - first - c;
-            valid = r < m.s ? (int)(left < 8 ? left : 8) : 0;
-        }
-        valid = valid < 0 ? 0 : valid > 8 ? 8 : valid;
-    }
-};
-
-template <int SP, int DT>
-__device__ __forceinline__ void load_chunk(const ZS_CONSTANT ThinItem& m, int64_t first, float x[8][8]) {
-    const int64_t all = (int64_t)m.s * m.l;
-    // a vector may run over its row's end into the next row, but not over the matrix's
-    const int64_t last = m.tall ? (first + Thin<SP>::kLC < m.l ? (first + Thin<SP>::kLC) * m.s : all)
-                                : (m.s - 1) * (int64_t)m.l + (first + Thin<SP>::kLC < m.l ? first + Thin<SP>::kLC : m.l);
-    if (last + 8 <= all) {
-#pragma unroll
-        for (int n = 0; n < 8; ++n) {
-            const Vector<SP> v(m, first, n);
-            ld8<DT>(m.in, v.valid ? v.at : 0, v.valid, true, x[n]);
-        }
-    } else {
-#pragma unroll
-        for (int n = 0; n < 8; ++n) {
-            const Vector<SP> v(m, first, n);
-            const bool whole = v.at + 8 <= all;
-            ld8<DT>(m.in, v.valid ? v.at : 0, v.valid, v.valid > 0 && whole, x[n]);
-        }
-    }
-}
+using ChunkVector = Vector8<SP, SP>;
 
 template <int SP>
 __device__ __forceinline__ void load_chunk(const ZS_CONSTANT ThinItem& m, int64_t first, float x[8][8]) {
-    if (m.udt == ZERO_F16) load_chunk<SP, ZERO_F16>(m, first, x);
-    else if (m.udt == ZERO_BF16) load_chunk<SP, ZERO_BF16>(m, first, x);
-    else load_chunk<SP, ZERO_F32>(m, first, x);
+    load_box<SP, SP>(m.udt, m.in, m.s, m.l, m.tall, 0, first, x);
 }
 
 // ---------------------------------------------------------------- first kernel: parts of U U^T
@@ -263,7 +190,7 @@ __global__ __launch_bounds__(kThreads, 2) void thin_gram(NsRef ref, int64_t firs
                 h[k] = (_Float16)y;
                 g[k] = (_Float16)(y - (float)h[k]);
             }
-            const Vector<SP> v(m, 0, n);
+            const ChunkVector<SP> v(m.s, m.l, m.tall, 0, 0, n);
             const uint32_t at = tall ? v.c * (SP * 2) + (((v.r >> 4) ^ tall_order<SP>(v.c)) << 5) + (v.r & 8) * 2
                                      : v.r * (H::kLC * 2) + (((v.c >> 3) ^ (v.r & 15)) << 4);
             *reinterpret_cast<h8*>(smem + at) = h;
@@ -477,7 +404,7 @@ __device__ __forceinline__ void store_chunk(const ZS_CONSTANT ThinItem& m, int64
     uint16_t* out = static_cast<uint16_t*>(m.out);
 #pragma unroll
     for (int n = 0; n < 8; ++n) {
-        const Vector<SP> v(m, first, n);
+        const ChunkVector<SP> v(m.s, m.l, m.tall, 0, first, n);
         if (v.valid == 0) continue;
         const float* from = stage + v.r * H::kStageLd + v.c;
         const int step = m.tall ? H::kStageLd : 1;
@@ -520,16 +447,16 @@ __global__ __launch_bounds__(kThreads) void thin_apply(NsRef ref, int64_t first,
         e += m.log2_scale;
 #pragma unroll
         for (int n = 0; n < 8; ++n) {
-            const Vector<SP> v(m, column, n);
+            const ChunkVector<SP> v(m.s, m.l, m.tall, 0, column, n);
             float* to = stage + v.r * H::kStageLd + v.c;
             if (m.tall) {
 #pragma unroll
-                for (int k = 0; k < 8; ++k) to[k * H::kStageLd] = ldexpf(x[n][k], e) * f;
+                for (int k = 0; k < 8; ++k) to[k * H::kStageLd] = scaled(x[n][k], f, e);
             } else {
 #pragma unroll
                 for (int k = 0; k < 8; k += 4)
-                    *reinterpret_cast<f32x4*>(to + k) = f32x4{ldexpf(x[n][k], e) * f, ldexpf(x[n][k + 1], e) * f,
-                                                              ldexpf(x[n][k + 2], e) * f, ldexpf(x[n][k + 3], e) * f};
+                    *reinterpret_cast<f32x4*>(to + k) = f32x4{scaled(x[n][k], f, e), scaled(x[n][k + 1], f, e),
+                                                              scaled(x[n][k + 2], f, e), scaled(x[n][k + 3], f, e)};
             }
         }
     }
