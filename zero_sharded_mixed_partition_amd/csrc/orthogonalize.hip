@@ -198,9 +198,25 @@ struct NsStep {
     int32_t last;
 };
 
+// Four neighbours of a row of X into the caller's matrix.
 template <int DT>
-__device__ __forceinline__ void st_ortho(void* out, int64_t e, float v) {
-    global(static_cast<uint16_t*>(out))[e] = (uint16_t)to16<DT>(v);
+__device__ __forceinline__ void store_ortho(const ZS_CONSTANT MatrixItem& m, int64_t row, int64_t col, const float v[4]) {
+    uint16_t* out = static_cast<uint16_t*>(m.out);
+    if (!m.tall && col + 4 <= m.l) {
+        st_any(pack4_16<DT>(v), out + row * m.l + col);
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        if (col + e >= m.l) break;
+        global(out)[m.tall ? (col + e) * m.s + row : row * m.l + col + e] = (uint16_t)to16<DT>(v[e]);
+    }
+}
+
+// Byte offset in a row of a mirrored tile of the 16-byte piece that holds column c.
+template <int WIDE>
+__device__ __forceinline__ int mirror_piece(int r, int c) {
+    return (((c % WIDE) >> 3) ^ (WIDE == 32 ? (r >> 2) & 3 : (r >> 2) & (WIDE / 8 - 1))) << 4;
 }
 
 // Waits until no more than N of this wave's loads are on their way, then for the other waves.
@@ -242,7 +258,7 @@ __global__ __launch_bounds__(64 * WM * WN) void ortho_product(NsRef ref, int64_t
         const char* from = MODE == kGram ? X : A;
         pm = from + ti * (T * 64);
         pn = from + tj * (T * 64);
-        n = stages_of(MODE == kGram ? m.l : m.s);
+        n = MODE == kPoly && step.c == 0.0f ? 0 : stages_of(MODE == kGram ? m.l : m.s);
     }
     uint32_t on[L];
     const char* cm[MODE == kApply ? L : 1];
@@ -281,11 +297,23 @@ __global__ __launch_bounds__(64 * WM * WN) void ortho_product(NsRef ref, int64_t
         }
     };
 
+    // The sums start with the product's other term, in their units: a X for
+    // kApply, (b / c) A for kPoly (or b A alone).  Its loads are on their way with
+    // the first stages'.  A lane holds four neighbours along M of one N.
+    const float unit = MODE == kApply ? step.a * (1 << kLog2A) : step.c != 0.0f ? step.b / step.c * (1 << kLog2A) : step.b;
+    h4 other[MODE == kGram ? 1 : UM][UN];
+    const int im = wm + (lane >> 4) * 4, in = wn + (lane & 15);
+    const int64_t at0 = MODE == kApply ? panel_at((int64_t)ti * T + in, (int64_t)tj * T + im, sp)
+                                       : panel_at((int64_t)tj * T + in, (int64_t)ti * T + im, sp);
+    const auto at = [&](int x, int y) { return at0 + (x >> 1) * sp * kPanel + (x & 1) * 16 + y * 16 * kPanel; };
+    if constexpr (MODE != kGram) {
+        const _Float16* from = reinterpret_cast<const _Float16*>(MODE == kApply ? X : A);
+#pragma unroll
+        for (int x = 0; x < UM; ++x)
+#pragma unroll
+            for (int y = 0; y < UN; ++y) other[x][y] = *reinterpret_cast<const h4*>(from + at(x, y));
+    }
     f32x4 acc[UM][UN];
-#pragma unroll
-    for (int x = 0; x < UM; ++x)
-#pragma unroll
-        for (int y = 0; y < UN; ++y) acc[x][y] = f32x4{};
     h8 fm[UM], fn[2][UN];
     const uint32_t an = lds + P::kOperand + P::row_read(lane, wn);
     const uint32_t am = lds + (MODE == kApply ? 0u : P::row_read(lane, wm));
@@ -305,6 +333,12 @@ __global__ __launch_bounds__(64 * WM * WN) void ortho_product(NsRef ref, int64_t
     for (int k = 0; k < S - 1; ++k)
 #pragma unroll
         for (int q = 0; q < NL; ++q) load(q);
+#pragma unroll
+    for (int x = 0; x < UM; ++x)
+#pragma unroll
+        for (int y = 0; y < UN; ++y)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[x][y][e] = MODE == kGram ? 0.0f : (float)other[x][y][e] * unit;
     wait_stage<(S - 2) * NL>();
 #pragma unroll
     for (int y = 0; y < UN; ++y) fn[0][y] = lds_h8(an + y * 1024);
@@ -341,57 +375,60 @@ __global__ __launch_bounds__(64 * WM * WN) void ortho_product(NsRef ref, int64_t
     }
     wait_stage<0>();                               // nothing may land once the LDS is another workgroup's
 
-    // a lane holds four neighbours along M of one N
+    if constexpr (MODE == kApply) {
+        const float scale = step.last ? ldexpf(1.0f, -kLog2A - m.log2_scale) : ldexpf(1.0f, -kLog2A);
+        _Float16* out = reinterpret_cast<_Float16*>(ref.ws + (step.odd ? m.x0 : m.x1));
 #pragma unroll
-    for (int x = 0; x < UM; ++x)
+        for (int x = 0; x < UM; ++x)
 #pragma unroll
-        for (int y = 0; y < UN; ++y) {
-            const int im = wm + x * 16 + (lane >> 4) * 4, in = wn + y * 16 + (lane & 15);
-            float v[4];
+            for (int y = 0; y < UN; ++y) {
+                float v[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = acc[x][y][e];
-            if constexpr (MODE == kApply) {
-                const int64_t row = (int64_t)ti * T + in, col = (int64_t)tj * T + im, at = panel_at(row, col, sp);
-                const h4 old = *reinterpret_cast<const h4*>(X + at * 2);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = fmaf(step.a, (float)old[e], ldexpf(v[e], -kLog2A));
+                for (int e = 0; e < 4; ++e) v[e] = acc[x][y][e] * scale;
                 if (!step.last) {
-                    h4 h;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) h[e] = (_Float16)v[e];
-                    *reinterpret_cast<h4*>(ref.ws + (step.odd ? m.x0 : m.x1) + at * 2) = h;
-                } else if (row < m.s) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        if (col + e >= m.l) break;
-                        const int64_t to = m.tall ? (col + e) * m.s + row : row * m.l + col + e;
-                        const float o = ldexpf(v[e], -m.log2_scale);
-                        if (m.odt == ZERO_F16) st_ortho<ZERO_F16>(m.out, to, o);
-                        else st_ortho<ZERO_BF16>(m.out, to, o);
-                    }
+                    *reinterpret_cast<h4*>(out + at(x, y)) = h4{(_Float16)v[0], (_Float16)v[1], (_Float16)v[2], (_Float16)v[3]};
+                    continue;
                 }
-            } else {
-                // symmetric: (c, r .. r + 3) is what the lane holds, (r .. r + 3, c) its mirror
-                const int64_t r = (int64_t)ti * T + im, c = (int64_t)tj * T + in, at = panel_at(c, r, sp);
+                const int64_t row = (int64_t)ti * T + in + y * 16, col = (int64_t)tj * T + im + x * 16;
+                if (row >= m.s) continue;
+                if (m.odt == ZERO_F16) store_ortho<ZERO_F16>(m, row, col, v);
+                else store_ortho<ZERO_BF16>(m, row, col, v);
+            }
+    } else {
+        // (c, r .. r + 3) is what a lane holds of the symmetric result; its mirror
+        // (r .. r + 3, c) goes through the LDS to leave in whole rows of a panel
+        const float scale = MODE == kGram ? ldexpf(1.0f, kLog2A - 2 * m.log2_scale)
+                                          : step.c != 0.0f ? step.c * ldexpf(1.0f, -kLog2A) : 1.0f;
+        _Float16* out = reinterpret_cast<_Float16*>(MODE == kGram ? A : B);
+        constexpr int kRows = T / WM, kColumns = T / WN, kWide = kColumns < kPanel ? kColumns : kPanel;
+        static_assert(kRows * kColumns * 2 * P::kWaves <= S * P::kStage, "the mirrored tile fits the stages' place");
+        char* mine_at = smem + wave * (kRows * kColumns * 2);
+        const bool mirror = ti != tj;
+#pragma unroll
+        for (int x = 0; x < UM; ++x)
+#pragma unroll
+            for (int y = 0; y < UN; ++y) {
                 h4 h;
-                if constexpr (MODE == kGram) {
-                    const int shift = kLog2A - 2 * m.log2_scale;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) h[e] = (_Float16)ldexpf(v[e], shift);
-                } else {
-                    const h4 old = *reinterpret_cast<const h4*>(A + at * 2);
+                for (int e = 0; e < 4; ++e) h[e] = (_Float16)(acc[x][y][e] * scale);
+                *reinterpret_cast<h4*>(out + at(x, y)) = h;
+                if (!mirror) continue;
+                const int r = x * 16 + (lane >> 4) * 4, c = y * 16 + (lane & 15);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) h[e] = (_Float16)fmaf(step.b, (float)old[e], step.c * ldexpf(v[e], -kLog2A));
-                }
-                _Float16* out = reinterpret_cast<_Float16*>(MODE == kGram ? A : B);
-                *reinterpret_cast<h4*>(out + at) = h;
-                if (ti != tj) {
-                    const int64_t mirror = panel_at(r, c, sp);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) out[mirror + e * kPanel] = h[e];
-                }
+                for (int e = 0; e < 4; ++e)
+                    *reinterpret_cast<_Float16*>(mine_at + ((c / kWide) * kRows + r + e) * (kWide * 2) + mirror_piece<kWide>(r, c) + (c & 7) * 2) = h[e];
+            }
+        if (mirror) {
+            // a wave reads what it wrote
+            __asm__ volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            constexpr int kPieces = kWide / 8;
+            for (int k = lane; k < kRows * kColumns / 8; k += 64) {
+                const int r = k / kPieces % kRows, c = k / (kPieces * kRows) * kWide + k % kPieces * 8;
+                const h8 h = *reinterpret_cast<const h8*>(mine_at + ((c / kWide) * kRows + r) * (kWide * 2) + mirror_piece<kWide>(r, c));
+                *reinterpret_cast<h8*>(out + panel_at((int64_t)ti * T + wm + r, (int64_t)tj * T + wn + c, sp)) = h;
             }
         }
+    }
 }
 
 // ---------------------------------------------------------------- host side
@@ -631,7 +668,9 @@ int zero_multi_orthogonalize(const void* table, const void* d_table, const doubl
         hipLaunchKernelGGL(ortho_load, dim3((unsigned)pass.n_pieces), dim3(kBlock), 0, s, ref, pass.piece_first, eps);
         rc = launch_status("ortho_load");
         for (int k = 0; k < n_steps && rc == ZERO_OK; ++k) {
-            const NsStep step{(float)coefs[3 * k], (float)coefs[3 * k + 1], (float)coefs[3 * k + 2], k & 1, k + 1 == n_steps};
+            // the square's sums start with (b / c) A, which has to stay in float32
+            const float b = steps.b[k], c = std::fabs(steps.c[k]) > std::fabs(b) * 0x1p-40f ? steps.c[k] : 0.0f;
+            const NsStep step{steps.a[k], b, c, k & 1, k + 1 == n_steps};
             rc = launch_product<kGram>(pass, ref, step, s);
             if (rc == ZERO_OK) rc = launch_product<kPoly>(pass, ref, step, s);
             if (rc == ZERO_OK) rc = launch_product<kApply>(pass, ref, step, s);
