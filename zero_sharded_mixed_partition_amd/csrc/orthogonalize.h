@@ -51,6 +51,13 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
 
 __device__ __forceinline__ h8 lds_h8(uint32_t a) { return *(__attribute__((address_space(3))) h8*)(uintptr_t)a; }
 
+// The order of the four 16-byte pieces of 64-byte rows for reads of 16 bytes of
+// which lane l takes row l % 16, piece l / 16.  The hardware serves lanes 0-3,
+// 12-15 and 20-27 at once, then 4-11, 16-19 and 28-31, and the upper half alike:
+// rows 4 q .. 4 q + 3 of one piece with others of the next.  0, 2, 3, 1 by q
+// keeps them apart in both.
+__device__ __forceinline__ int row_order(int r) { return (((r >> 2) ^ (r >> 3)) & 1) * 2 + ((r >> 3) & 1); }
+
 // Four values down a column of 4 x 16 blocks (a lane of 16 gives the address of a fourth of a row).
 __device__ __forceinline__ h4 lds_column(uint32_t a) {
     return __builtin_bit_cast(h4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4*)(uintptr_t)a));

@@ -152,8 +152,9 @@ __device__ __forceinline__ void load_lds(const void* base, uint32_t offset, uint
 // Operands in the LDS, as the 16 x 16 x 32 MFMA takes them (lane l: row or
 // column l % 16, inner elements 8 (l / 16) .. + 7):
 //  rows:     of a matrix whose inner dimension runs along the panel's columns.
-//            The 16-byte pieces of row r lie in the order piece ^ (r / 4) % 4,
-//            so that 16 lanes which read one piece of 16 rows meet all 64 banks.
+//            The 16-byte pieces of row r lie in the order piece ^ row_order(r):
+//            the 16 lanes that a 16-byte read serves at a time then meet all 64
+//            banks (with piece ^ (r / 4) % 4 two and two of them meet).
 //  columns:  the inner dimension runs down the panel's rows, read through the
 //            transposing load: 16 lanes take 4 rows of 16 elements.  The 32-byte
 //            halves of rows 8 to 15 of 16 are swapped, so that the two groups
@@ -171,7 +172,7 @@ struct Product {
     // Where this lane reads its n-th piece of an operand of rows, from the first.
     __device__ static __forceinline__ uint32_t row_offset(int wave, int lane, int n) {
         const int r = (wave * kLoads + n) * 16 + lane / 4;
-        return (uint32_t)(r * 64 + ((lane & 3) ^ ((r >> 2) & 3)) * 16);
+        return (uint32_t)(r * 64 + ((lane & 3) ^ row_order(r)) * 16);
     }
     // ... of an operand of columns: T / 32 panels of 32 rows, panel_bytes apart
     __device__ static __forceinline__ int64_t column_offset(int wave, int lane, int n, int64_t panel_bytes) {
@@ -181,7 +182,7 @@ struct Product {
     // Where it finds its part of rows 0 .. 15, or of columns 0 .. 15, in the LDS.
     __device__ static __forceinline__ uint32_t row_read(int lane, int first) {
         const int r = first + (lane & 15);
-        return (uint32_t)(r * 64 + (((lane >> 4) ^ (r >> 2)) & 3) * 16);
+        return (uint32_t)(r * 64 + ((lane >> 4) ^ row_order(r)) * 16);
     }
     __device__ static __forceinline__ uint32_t column_read(int lane, int first) {
         const int r = (lane >> 4) * 8 + ((lane & 15) >> 2), half = (first >> 4) & 1;

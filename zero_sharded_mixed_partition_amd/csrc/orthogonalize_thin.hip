@@ -230,7 +230,7 @@ __global__ __launch_bounds__(kThreads, 2) void thin_gram(NsRef ref, int64_t firs
 // read one piece of 16 rows meet all banks.
 template <int SP>
 __device__ __forceinline__ uint32_t square_piece(int r, int piece) {
-    const int order = SP == 128 ? r & 15 : SP == 64 ? (r >> 1) & 7 : (r >> 2) & 3;
+    const int order = SP == 128 ? r & 15 : SP == 64 ? (r >> 1) & 7 : row_order(r);
     return r * (SP * 2) + ((piece ^ order) << 4);
 }
 
