@@ -50,7 +50,7 @@ def rounded(u, coefs=COEFS, eps=1e-7):
     x = _half(x, 2.0 ** k)
     for i, (a, b, c) in enumerate(coefs):
         g = _half(x @ x.T, 1024.0)
-        x = a * x + _half(b * g + c * (g @ g), 1024.0) @ x
+        x = _half(a * np.eye(len(g)) + b * g + c * (g @ g), 1024.0) @ x
         if i + 1 < len(coefs):
             x = _half(x, 2.0 ** k)
     return x.T if tall else x

@@ -144,10 +144,10 @@ __device__ __forceinline__ void load_lds(const void* base, uint32_t offset, uint
 // A wave's share of a T x T tile of a product, WM x WN waves.
 //
 // A stage is 32 inner elements of both operands, 64 bytes a row: 16 rows for
-// each 1 KB that a wave loads at a time, straight into the LDS.  S stages lie
-// there; S - 2 are on their way while one is multiplied, since a load that
-// misses the L2 takes longer than a stage.  One barrier a stage: behind it the
-// next stage has landed for all waves, and the last one's place is free.
+// each 1 KB that a wave loads at a time, straight into the LDS.  Four stages lie
+// there; two are on their way while one is multiplied, since a load that misses
+// the L2 takes longer than a stage.  One barrier a stage: behind it the next
+// stage has landed for all waves, and the last one's place is free.
 //
 // Operands in the LDS, as the 16 x 16 x 32 MFMA takes them (lane l: row or
 // column l % 16, inner elements 8 (l / 16) .. + 7):
@@ -165,19 +165,21 @@ struct Product {
     static constexpr int kUM = T / WM / 16, kUN = T / WN / 16;       // 16 x 16 results per wave
     static constexpr int kOperand = T * kPanel * 2;                  // bytes of a stage
     static constexpr int kLoads = kOperand / 1024 / kWaves;          // per wave and operand
-    static constexpr int kStages = 5;
+    static constexpr int kStages = 4;
     static constexpr int kStage = 2 * kOperand;
-    static_assert(kLoads >= 1 && kStages * kStage <= 160 * 1024, "stages do not fit the LDS");
+    static constexpr int kMirror = 2 * 16 * (T / WN) * 2;            // of a wave: 32 rows of its mirrored results
+    static constexpr int kLds = kStages * kStage + kWaves * kMirror;
+    static_assert(kLoads >= 1 && kLds <= 160 * 1024, "stages do not fit the LDS");
 
     // Where this lane reads its n-th piece of an operand of rows, from the first.
     __device__ static __forceinline__ uint32_t row_offset(int wave, int lane, int n) {
         const int r = (wave * kLoads + n) * 16 + lane / 4;
         return (uint32_t)(r * 64 + ((lane & 3) ^ row_order(r)) * 16);
     }
-    // ... of an operand of columns: T / 32 panels of 32 rows, panel_bytes apart
-    __device__ static __forceinline__ int64_t column_offset(int wave, int lane, int n, int64_t panel_bytes) {
-        const int k = wave * kLoads + n, r = (k & 1) * 16 + lane / 4;
-        return (k >> 1) * panel_bytes + r * 64 + ((lane & 3) ^ ((r >> 2) & 2)) * 16;
+    // ... of an operand of columns, T / 32 panels of 32 rows, from the wave's first panel
+    __device__ static __forceinline__ uint32_t column_offset(int wave, int lane, int n) {
+        const int r = ((wave * kLoads + n) & 1) * 16 + lane / 4;
+        return (uint32_t)(r * 64 + ((lane & 3) ^ ((r >> 2) & 2)) * 16);
     }
     // Where it finds its part of rows 0 .. 15, or of columns 0 .. 15, in the LDS.
     __device__ static __forceinline__ uint32_t row_read(int lane, int first) {
@@ -214,11 +216,8 @@ __device__ __forceinline__ void store_ortho(const ZS_CONSTANT MatrixItem& m, int
     }
 }
 
-// Byte offset in a row of a mirrored tile of the 16-byte piece that holds column c.
-template <int WIDE>
-__device__ __forceinline__ int mirror_piece(int r, int c) {
-    return (((c % WIDE) >> 3) ^ (WIDE == 32 ? (r >> 2) & 3 : (r >> 2) & (WIDE / 8 - 1))) << 4;
-}
+// Byte offset in a row of 32 mirrored results of the 16-byte piece that holds column c.
+__device__ __forceinline__ int mirror_piece(int r, int c) { return (((c & 31) >> 3) ^ ((r >> 2) & 3)) << 4; }
 
 // Waits until no more than N of this wave's loads are on their way, then for the other waves.
 template <int N>
@@ -226,94 +225,75 @@ __device__ __forceinline__ void wait_stage() {
     __asm__ volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
-// One tile of a product.  M runs over the tile's rows for kGram and kPoly and
-// over its columns for kApply, so that a lane ends with four neighbours of a
-// stored row: rows of X for kApply, of the transposed tile for the others.
+// What a wave loads for a tile: where its operands begin, how far a stage moves
+// them, and the stages.
+struct Source {
+    const char *m, *n;
+    int64_t move_m, move_n;
+    int stages;
+};
+
 template <int T, int WM, int WN, int MODE>
-__global__ __launch_bounds__(64 * WM * WN) void ortho_product(NsRef ref, int64_t first, NsStep step) {
+__device__ __forceinline__ Source source_of(const NsRef& ref, const TileRef tile, const NsStep& step, int wave) {
+    using P = Product<T, WM, WN>;
+    const ZS_CONSTANT MatrixItem& m = ref.item(tile.item);
+    const char* X = ref.ws + (step.odd ? m.x1 : m.x0);
+    const int64_t panel = (int64_t)m.sp * 64;
+    if constexpr (MODE == kApply) {
+        return Source{X + ((int64_t)tile.j * (T / kPanel) + ((wave * P::kLoads) >> 1)) * panel, ref.ws + m.b + tile.i * (T * 64),
+                      kPanel * 64, panel, stages_of(m.s)};
+    } else {
+        const char* from = MODE == kGram ? X : ref.ws + m.a;
+        return Source{from + tile.i * (T * 64), from + tile.j * (T * 64), panel, panel, stages_of(MODE == kGram ? m.l : m.s)};
+    }
+}
+
+// The tiles of a product, block b taking tiles b, b + blocks, ...  M runs over a
+// tile's rows for kGram and kPoly and over its columns for kApply, so that a
+// lane ends with four neighbours of a stored row: rows of X for kApply, of the
+// transposed tile for the others.
+//
+// The loads run on from tile to tile: the next one's first stages land while
+// this one's last are multiplied and its results leave.  (With a block per tile
+// and one block a CU, all CUs loaded, multiplied and stored in step: 23 us a
+// tile besides its stages at T 256, of 116 with 128 stages.)
+template <int T, int WM, int WN, int MODE>
+__global__ __launch_bounds__(64 * WM * WN) void ortho_product(NsRef ref, int64_t first, int64_t n_tiles, NsStep step) {
     using P = Product<T, WM, WN>;
     constexpr int UM = P::kUM, UN = P::kUN, L = P::kLoads, S = P::kStages, NL = 2 * L;
     if (ref.skipped()) return;
-    __shared__ __attribute__((aligned(1024))) char smem[S * P::kStage];
-    const ZS_CONSTANT TileRef& t = ref.tile(first + blockIdx.x);
-    const ZS_CONSTANT MatrixItem& m = ref.item(t.item);
-    const int ti = t.i, tj = t.j;
-    const int64_t sp = m.sp;
+    __shared__ __attribute__((aligned(1024))) char smem[P::kLds];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int wm = wave / WN * (T / WM), wn = wave % WN * (T / WN);
-    const char* X = ref.ws + (step.odd ? m.x1 : m.x0);
-    char* A = ref.ws + m.a;
-    char* B = ref.ws + m.b;
-
-    // the M operand, the N operand, and how far a stage moves the first
-    const char *pm, *pn;
-    int64_t move_m = sp * 64;
-    const int64_t move_n = sp * 64;
-    int n;
-    if constexpr (MODE == kApply) {
-        pm = X + (int64_t)tj * (T / kPanel) * sp * 64;
-        pn = B + ti * (T * 64);
-        move_m = kPanel * 64;
-        n = stages_of(m.s);
-    } else {
-        const char* from = MODE == kGram ? X : A;
-        pm = from + ti * (T * 64);
-        pn = from + tj * (T * 64);
-        n = MODE == kPoly && step.c == 0.0f ? 0 : stages_of(MODE == kGram ? m.l : m.s);
-    }
-    uint32_t on[L];
-    const char* cm[MODE == kApply ? L : 1];
+    const auto tile_at = [&](int64_t i) {
+        const ZS_CONSTANT TileRef& t = ref.tile(first + i);
+        return TileRef{t.item, t.i, t.j};
+    };
+    uint32_t om[L], on[L];
 #pragma unroll
     for (int q = 0; q < L; ++q) {
         on[q] = P::row_offset(wave, lane, q);
-        if constexpr (MODE == kApply) cm[q] = pm + P::column_offset(wave, 0, q, sp * 64);
-    }
-    // the lane's part of the column offset is the same for all pieces: rows of 16 from an even or an odd half
-    uint32_t oc[MODE == kApply ? L : 1];
-    if constexpr (MODE == kApply) {
-#pragma unroll
-        for (int q = 0; q < L; ++q)
-            oc[q] = (uint32_t)(P::column_offset(wave, lane, q, 0) - P::column_offset(wave, 0, q, 0));
+        om[q] = MODE == kApply ? P::column_offset(wave, lane, q) : on[q];
     }
     const uint32_t lds = lds_address(smem), mine = lds + wave * L * 1024;
+    TileRef tile = tile_at(blockIdx.x);
+    Source now = source_of<T, WM, WN, MODE>(ref, tile, step, wave), then = now;
+    int n = now.stages, left = n;
     uint32_t put = 0;
-    int left = n;
     const auto load = [&](int q) {                 // the q-th load of a stage
-        if (q < L) {
-            if constexpr (MODE == kApply) load_lds(cm[q], oc[q], mine + put + q * 1024);
-            else load_lds(pm, on[q], mine + put + q * 1024);
-        } else {
-            load_lds(pn, on[q - L], mine + put + P::kOperand + (q - L) * 1024);
-        }
+        if (q < L) load_lds(now.m, om[q], mine + put + q * 1024);
+        else load_lds(now.n, on[q - L], mine + put + P::kOperand + (q - L) * 1024);
         if (q == NL - 1) {
-            const bool more = --left > 0;
-            if constexpr (MODE == kApply) {
-#pragma unroll
-                for (int k = 0; k < L; ++k) cm[k] += more ? move_m : 0;
-            } else {
-                pm += more ? move_m : 0;
-            }
-            pn += more ? move_n : 0;
+            const bool over = --left == 0;
+            now.m = over ? then.m : now.m + now.move_m;
+            now.n = over ? then.n : now.n + now.move_n;
+            now.move_m = over ? then.move_m : now.move_m;
+            now.move_n = over ? then.move_n : now.move_n;
+            left = over ? then.stages : left;
             put = put == (S - 1) * P::kStage ? 0 : put + P::kStage;
         }
     };
 
-    // The sums start with the product's other term, in their units: a X for
-    // kApply, (b / c) A for kPoly (or b A alone).  Its loads are on their way with
-    // the first stages'.  A lane holds four neighbours along M of one N.
-    const float unit = MODE == kApply ? step.a * (1 << kLog2A) : step.c != 0.0f ? step.b / step.c * (1 << kLog2A) : step.b;
-    h4 other[MODE == kGram ? 1 : UM][UN];
-    const int im = wm + (lane >> 4) * 4, in = wn + (lane & 15);
-    const int64_t at0 = MODE == kApply ? panel_at((int64_t)ti * T + in, (int64_t)tj * T + im, sp)
-                                       : panel_at((int64_t)tj * T + in, (int64_t)ti * T + im, sp);
-    const auto at = [&](int x, int y) { return at0 + (x >> 1) * sp * kPanel + (x & 1) * 16 + y * 16 * kPanel; };
-    if constexpr (MODE != kGram) {
-        const _Float16* from = reinterpret_cast<const _Float16*>(MODE == kApply ? X : A);
-#pragma unroll
-        for (int x = 0; x < UM; ++x)
-#pragma unroll
-            for (int y = 0; y < UN; ++y) other[x][y] = *reinterpret_cast<const h4*>(from + at(x, y));
-    }
     f32x4 acc[UM][UN];
     h8 fm[UM], fn[2][UN];
     const uint32_t an = lds + P::kOperand + P::row_read(lane, wn);
@@ -328,24 +308,7 @@ __global__ __launch_bounds__(64 * WM * WN) void ortho_product(NsRef ref, int64_t
             return lds_h8(am + stage + x * 1024);
         }
     };
-
-    // Loads past the last stage read it again, into places that nothing reads any
-    // more: the loop has no other end to it, and its waits are constants.
-    for (int k = 0; k < S - 1; ++k)
-#pragma unroll
-        for (int q = 0; q < NL; ++q) load(q);
-#pragma unroll
-    for (int x = 0; x < UM; ++x)
-#pragma unroll
-        for (int y = 0; y < UN; ++y)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[x][y][e] = MODE == kGram ? 0.0f : (float)other[x][y][e] * unit;
-    wait_stage<(S - 2) * NL>();
-#pragma unroll
-    for (int y = 0; y < UN; ++y) fn[0][y] = lds_h8(an + y * 1024);
-#pragma unroll
-    for (int x = 0; x < UM; ++x) fm[x] = read_m(0, x);
-    uint32_t next = P::kStage;
+    uint32_t next = 0;
     // One stage's products.  Between them, in this order, the loads of the stage
     // S - 1 ahead and the reads of the next one: a row of M is read as soon as
     // its products are issued, N into the other half of fn.
@@ -368,68 +331,119 @@ __global__ __launch_bounds__(64 * WM * WN) void ortho_product(NsRef ref, int64_t
         }
         next = next == (S - 1) * P::kStage ? 0 : next + P::kStage;
     };
-    for (int k = 0; k < n; k += 2) {
-        wait_stage<(S - 3) * NL>();
-        multiply(std::integral_constant<int, 0>{});
-        wait_stage<(S - 3) * NL>();
-        multiply(std::integral_constant<int, 1>{});
-    }
-    wait_stage<0>();                               // nothing may land once the LDS is another workgroup's
 
-    if constexpr (MODE == kApply) {
-        const float scale = step.last ? ldexpf(1.0f, -kLog2A - m.log2_scale) : ldexpf(1.0f, -kLog2A);
-        _Float16* out = reinterpret_cast<_Float16*>(ref.ws + (step.odd ? m.x0 : m.x1));
+    for (int k = 0; k < S - 1; ++k)                // no tile has fewer stages
+#pragma unroll
+        for (int q = 0; q < NL; ++q) load(q);
+    wait_stage<(S - 2) * NL>();
+#pragma unroll
+    for (int y = 0; y < UN; ++y) fn[0][y] = lds_h8(an + y * 1024);
+#pragma unroll
+    for (int x = 0; x < UM; ++x) fm[x] = read_m(0, x);
+    next = P::kStage;
+    int landed = 0;                                // stages of this tile that need no wait
+    for (int64_t index = blockIdx.x; index < n_tiles; index += gridDim.x) {
+        // behind the last tile its first stage is read again, into places that nothing reads any more
+        TileRef following = tile;
+        if (index + (int64_t)gridDim.x < n_tiles) {
+            following = tile_at(index + gridDim.x);
+            then = source_of<T, WM, WN, MODE>(ref, following, step, wave);
+        } else {
+            then = Source{now.m, now.n, 0, 0, INT32_MAX};
+        }
 #pragma unroll
         for (int x = 0; x < UM; ++x)
 #pragma unroll
-            for (int y = 0; y < UN; ++y) {
-                float v[4];
+            for (int y = 0; y < UN; ++y) acc[x][y] = f32x4{};
+        for (int k = 0; k < n; k += 2) {
+            if (k >= landed) wait_stage<(S - 3) * NL>();
+            else __asm__ volatile("s_barrier" ::: "memory");
+            multiply(std::integral_constant<int, 0>{});
+            if (k >= landed) wait_stage<(S - 3) * NL>();
+            else __asm__ volatile("s_barrier" ::: "memory");
+            multiply(std::integral_constant<int, 1>{});
+        }
+        // What is on its way has had a stage's time: with it landed, the stores below
+        // are the oldest that a later wait waits for.
+        __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        landed = S - 2;
+
+        const ZS_CONSTANT MatrixItem& m = ref.item(tile.item);
+        const int64_t sp = m.sp;
+        const int ti = tile.i, tj = tile.j;
+        // a lane holds four neighbours along M of one N
+        const int im = wm + (lane >> 4) * 4, in = wn + (lane & 15);
+        const int64_t at0 = MODE == kApply ? panel_at((int64_t)ti * T + in, (int64_t)tj * T + im, sp)
+                                           : panel_at((int64_t)tj * T + in, (int64_t)ti * T + im, sp);
+        const auto at = [&](int x, int y) { return at0 + (x >> 1) * sp * kPanel + (x & 1) * 16 + y * 16 * kPanel; };
+        if constexpr (MODE == kApply) {
+            const float scale = step.last ? ldexpf(1.0f, -kLog2A - m.log2_scale) : ldexpf(1.0f, -kLog2A);
+            _Float16* out = reinterpret_cast<_Float16*>(ref.ws + (step.odd ? m.x0 : m.x1));
 #pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = acc[x][y][e] * scale;
-                if (!step.last) {
-                    *reinterpret_cast<h4*>(out + at(x, y)) = h4{(_Float16)v[0], (_Float16)v[1], (_Float16)v[2], (_Float16)v[3]};
-                    continue;
+            for (int x = 0; x < UM; ++x)
+#pragma unroll
+                for (int y = 0; y < UN; ++y) {
+                    float v[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[e] = acc[x][y][e] * scale;
+                    if (!step.last) {
+                        *reinterpret_cast<h4*>(out + at(x, y)) = h4{(_Float16)v[0], (_Float16)v[1], (_Float16)v[2], (_Float16)v[3]};
+                        continue;
+                    }
+                    const int64_t row = (int64_t)ti * T + in + y * 16, col = (int64_t)tj * T + im + x * 16;
+                    if (row >= m.s) continue;
+                    if (m.odt == ZERO_F16) store_ortho<ZERO_F16>(m, row, col, v);
+                    else store_ortho<ZERO_BF16>(m, row, col, v);
                 }
-                const int64_t row = (int64_t)ti * T + in + y * 16, col = (int64_t)tj * T + im + x * 16;
-                if (row >= m.s) continue;
-                if (m.odt == ZERO_F16) store_ortho<ZERO_F16>(m, row, col, v);
-                else store_ortho<ZERO_BF16>(m, row, col, v);
-            }
-    } else {
-        // (c, r .. r + 3) is what a lane holds of the symmetric result; its mirror
-        // (r .. r + 3, c) goes through the LDS to leave in whole rows of a panel
-        const float scale = MODE == kGram ? ldexpf(1.0f, kLog2A - 2 * m.log2_scale)
-                                          : step.c != 0.0f ? step.c * ldexpf(1.0f, -kLog2A) : 1.0f;
-        _Float16* out = reinterpret_cast<_Float16*>(MODE == kGram ? A : B);
-        constexpr int kRows = T / WM, kColumns = T / WN, kWide = kColumns < kPanel ? kColumns : kPanel;
-        static_assert(kRows * kColumns * 2 * P::kWaves <= S * P::kStage, "the mirrored tile fits the stages' place");
-        char* mine_at = smem + wave * (kRows * kColumns * 2);
-        const bool mirror = ti != tj;
+        } else {
+            // (c, r .. r + 3) is what a lane holds of the symmetric result; its mirror
+            // (r .. r + 3, c) goes through the LDS, 32 rows at a time, to leave in
+            // whole rows of a panel
+            const float scale = MODE == kGram ? ldexpf(1.0f, kLog2A - 2 * m.log2_scale) : step.c * ldexpf(1.0f, -kLog2A);
+            const float diagonal = step.a * (1 << kLog2A);
+            const _Float16* old = reinterpret_cast<const _Float16*>(ref.ws + m.a);
+            _Float16* out = reinterpret_cast<_Float16*>(ref.ws + (MODE == kGram ? m.a : m.b));
+            char* mirror_at = smem + S * P::kStage + wave * P::kMirror;
 #pragma unroll
-        for (int x = 0; x < UM; ++x)
+            for (int x = 0; x < UM; x += 2) {
 #pragma unroll
-            for (int y = 0; y < UN; ++y) {
-                h4 h;
+                for (int z = 0; z < 2; ++z)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) h[e] = (_Float16)(acc[x][y][e] * scale);
-                *reinterpret_cast<h4*>(out + at(x, y)) = h;
-                if (!mirror) continue;
-                const int r = x * 16 + (lane >> 4) * 4, c = y * 16 + (lane & 15);
+                    for (int y = 0; y < UN; ++y) {
+                        const int r = z * 16 + (lane >> 4) * 4, c = y * 16 + (lane & 15);
+                        h4 h;
+                        if constexpr (MODE == kGram) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    *reinterpret_cast<_Float16*>(mine_at + ((c / kWide) * kRows + r + e) * (kWide * 2) + mirror_piece<kWide>(r, c) + (c & 7) * 2) = h[e];
-            }
-        if (mirror) {
-            // a wave reads what it wrote
-            __asm__ volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-            constexpr int kPieces = kWide / 8;
-            for (int k = lane; k < kRows * kColumns / 8; k += 64) {
-                const int r = k / kPieces % kRows, c = k / (kPieces * kRows) * kWide + k % kPieces * 8;
-                const h8 h = *reinterpret_cast<const h8*>(mine_at + ((c / kWide) * kRows + r) * (kWide * 2) + mirror_piece<kWide>(r, c));
-                *reinterpret_cast<h8*>(out + panel_at((int64_t)ti * T + wm + r, (int64_t)tj * T + wn + c, sp)) = h;
+                            for (int e = 0; e < 4; ++e) h[e] = (_Float16)(acc[x + z][y][e] * scale);
+                        } else {
+                            const h4 a = *reinterpret_cast<const h4*>(old + at(x + z, y));
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const float v = fmaf(step.b, (float)a[e], acc[x + z][y][e] * scale);
+                                h[e] = (_Float16)(ti == tj && im + (x + z) * 16 + e == in + y * 16 ? v + diagonal : v);
+                            }
+                        }
+                        *reinterpret_cast<h4*>(out + at(x + z, y)) = h;
+                        if (ti == tj) continue;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            *reinterpret_cast<_Float16*>(mirror_at + ((c / kPanel) * 32 + r + e) * 64 + mirror_piece(r, c) + (c & 7) * 2) = h[e];
+                    }
+                if (ti == tj) continue;
+                __asm__ volatile("s_waitcnt lgkmcnt(0)" ::: "memory");     // a wave reads what it wrote
+#pragma unroll
+                for (int k = 0; k < P::kMirror / 1024; ++k) {
+                    const int piece = k * 64 + lane, r = piece / 4 % 32, c = piece / 128 * kPanel + (piece & 3) * 8;
+                    const h8 h = *reinterpret_cast<const h8*>(mirror_at + ((c / kPanel) * 32 + r) * 64 + mirror_piece(r, c));
+                    *reinterpret_cast<h8*>(out + panel_at((int64_t)ti * T + wm + x * 16 + r, (int64_t)tj * T + wn + c, sp)) = h;
+                }
+                __asm__ volatile("s_waitcnt lgkmcnt(0)" ::: "memory");     // before the next 32 rows
             }
         }
+        tile = following;
+        n = then.stages;
     }
+    wait_stage<0>();                               // nothing may land once the LDS is another workgroup's
 }
 
 // ---------------------------------------------------------------- host side
@@ -508,15 +522,19 @@ void add_tiles(OrthoPlan* plan, size_t first, int tile, bool symmetric) {
     }
 }
 
+constexpr int64_t kCUs = 256;
+
 template <int MODE>
 int launch_product(const OrthoPass& p, const NsRef& ref, const NsStep& step, hipStream_t s) {
     const int64_t first = MODE == kApply ? p.x_first : p.sym_first, n = MODE == kApply ? p.n_x : p.n_sym;
+    // as many blocks as the LDS lets the CUs hold: each works off every so many tiles
+    const dim3 grid((unsigned)std::min(n, kCUs * (p.tile == 256 ? 1 : p.tile == 128 ? 2 : 4)));
     if (p.tile == 256)
-        hipLaunchKernelGGL((ortho_product<256, 2, 4, MODE>), dim3((unsigned)n), dim3(512), 0, s, ref, first, step);
+        hipLaunchKernelGGL((ortho_product<256, 2, 4, MODE>), grid, dim3(512), 0, s, ref, first, n, step);
     else if (p.tile == 128)
-        hipLaunchKernelGGL((ortho_product<128, 2, 2, MODE>), dim3((unsigned)n), dim3(256), 0, s, ref, first, step);
+        hipLaunchKernelGGL((ortho_product<128, 2, 2, MODE>), grid, dim3(256), 0, s, ref, first, n, step);
     else
-        hipLaunchKernelGGL((ortho_product<64, 2, 2, MODE>), dim3((unsigned)n), dim3(256), 0, s, ref, first, step);
+        hipLaunchKernelGGL((ortho_product<64, 2, 2, MODE>), grid, dim3(256), 0, s, ref, first, n, step);
     return launch_status("ortho_product");
 }
 
@@ -534,7 +552,7 @@ int check_coefs(const double* coefs, int32_t n_steps) {
         double next = 0.0, poly = 0.0;
         for (int i = 0; i <= 4096; ++i) {
             const double x = top * i / 4096, y = x * x;
-            poly = std::max(poly, std::fabs(y * (b + c * y)));
+            poly = std::max({poly, std::fabs(y * (b + c * y)), std::fabs(a + y * (b + c * y))});
             next = std::max(next, std::fabs(x * (a + y * (b + c * y))));
         }
         if (poly > 32.0 || next > 4.0)
@@ -669,9 +687,7 @@ int zero_multi_orthogonalize(const void* table, const void* d_table, const doubl
         hipLaunchKernelGGL(ortho_load, dim3((unsigned)pass.n_pieces), dim3(kBlock), 0, s, ref, pass.piece_first, eps);
         rc = launch_status("ortho_load");
         for (int k = 0; k < n_steps && rc == ZERO_OK; ++k) {
-            // the square's sums start with (b / c) A, which has to stay in float32
-            const float b = steps.b[k], c = std::fabs(steps.c[k]) > std::fabs(b) * 0x1p-40f ? steps.c[k] : 0.0f;
-            const NsStep step{steps.a[k], b, c, k & 1, k + 1 == n_steps};
+            const NsStep step{steps.a[k], steps.b[k], steps.c[k], k & 1, k + 1 == n_steps};
             rc = launch_product<kGram>(pass, ref, step, s);
             if (rc == ZERO_OK) rc = launch_product<kPoly>(pass, ref, step, s);
             if (rc == ZERO_OK) rc = launch_product<kApply>(pass, ref, step, s);
