@@ -67,8 +67,10 @@ struct ThinItem {
 };
 static_assert(sizeof(ThinItem) == sizeof(MatrixItem), "one array holds both");
 
+constexpr uint32_t kNoItem = UINT32_MAX;
+
 struct TileRef {
-    uint32_t item;
+    uint32_t item;                      // kNoItem: a block's round without a tile
     uint16_t i, j;                      // tile row (along s) and tile column
 };
 
@@ -79,8 +81,9 @@ struct OrthoPass {
     int32_t tile;
     int32_t n_items;
     int64_t first_item;
-    int64_t sym_first, n_sym;           // tiles of the symmetric products, lower triangle
-    int64_t x_first, n_x;               // tiles of the iterate
+    int64_t sym_first, n_sym;           // tiles of the symmetric products, lower triangle: rounds of sym_blocks
+    int64_t x_first, n_x;               // tiles of the iterate: rounds of x_blocks
+    int32_t sym_blocks, x_blocks;
     int64_t piece_first, n_pieces;      // pieces in which U is read (not of thin ones)
 };
 

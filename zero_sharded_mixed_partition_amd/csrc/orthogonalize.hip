@@ -248,8 +248,8 @@ __device__ __forceinline__ Source source_of(const NsRef& ref, const TileRef tile
     }
 }
 
-// The tiles of a product, block b taking tiles b, b + blocks, ...  M runs over a
-// tile's rows for kGram and kPoly and over its columns for kApply, so that a
+// The tiles of a product, block b taking tiles b, b + blocks, ... as far as there
+// are any.  M runs over a tile's rows for kGram and kPoly and over its columns for kApply, so that a
 // lane ends with four neighbours of a stored row: rows of X for kApply, of the
 // transposed tile for the others.
 //
@@ -277,6 +277,7 @@ __global__ __launch_bounds__(64 * WM * WN) void ortho_product(NsRef ref, int64_t
     }
     const uint32_t lds = lds_address(smem), mine = lds + wave * L * 1024;
     TileRef tile = tile_at(blockIdx.x);
+    if (tile.item == kNoItem) return;
     Source now = source_of<T, WM, WN, MODE>(ref, tile, step, wave), then = now;
     int n = now.stages, left = n;
     uint32_t put = 0;
@@ -342,11 +343,11 @@ __global__ __launch_bounds__(64 * WM * WN) void ortho_product(NsRef ref, int64_t
     for (int x = 0; x < UM; ++x) fm[x] = read_m(0, x);
     next = P::kStage;
     int landed = 0;                                // stages of this tile that need no wait
-    for (int64_t index = blockIdx.x; index < n_tiles; index += gridDim.x) {
+    for (int64_t index = blockIdx.x; tile.item != kNoItem; index += gridDim.x) {
         // behind the last tile its first stage is read again, into places that nothing reads any more
-        TileRef following = tile;
-        if (index + (int64_t)gridDim.x < n_tiles) {
-            following = tile_at(index + gridDim.x);
+        TileRef following{kNoItem, 0, 0};
+        if (index + (int64_t)gridDim.x < n_tiles) following = tile_at(index + gridDim.x);
+        if (following.item != kNoItem) {
             then = source_of<T, WM, WN, MODE>(ref, following, step, wave);
         } else {
             then = Source{now.m, now.n, 0, 0, INT32_MAX};
@@ -478,16 +479,6 @@ double step_cost(const std::vector<OrthoMatrix>& matrices, int tile) {
     return cost;
 }
 
-// Blocks go to the eight XCDs in turn.  A run of tiles of equal depth is dealt
-// out so that each XCD takes a part of it whose tiles share their operands in
-// one L2, and as many tiles as the others.
-void deal_out(std::vector<TileRef>& tiles, size_t first) {
-    const std::vector<TileRef> run(tiles.begin() + first, tiles.end());
-    size_t next = 0;
-    for (size_t xcd = 0; xcd < 8; ++xcd)
-        for (size_t b = first + (xcd + 8 - first % 8) % 8; b < tiles.size(); b += 8) tiles[b] = run[next++];
-}
-
 // A matrix's places in the workspace, from *at on.
 void place_item(MatrixItem* it, int64_t* at) {
     const int64_t x = (int64_t)it->sp * it->lp * 2, a = (int64_t)it->sp * it->sp * 2;
@@ -498,37 +489,72 @@ void place_item(MatrixItem* it, int64_t* at) {
     it->slots = place(at, (int64_t)it->n_slots * 8);
 }
 
+constexpr int kXCDs = 8, kCUs = 256;
+
+// Blocks of a product: as many as the LDS lets the CUs hold.
+int most_blocks(int tile) { return kCUs * (tile == 256 ? 1 : tile == 128 ? 2 : 4); }
+
 // The tiles of the symmetric products (lower triangle), or of the iterate, of
-// the items from `first` on: the deepest products first, so that short ones fill
-// the end; within a matrix four tile rows at a time, column by column.
-void add_tiles(OrthoPlan* plan, size_t first, int tile, bool symmetric) {
+// the items from `first` on, as rounds of one tile per block.  Blocks go to the
+// eight XCDs in turn.  Of the tiles of one depth each XCD takes an equal run,
+// within a matrix four tile rows at a time and column by column, so that its
+// tiles share their operands in one L2; the deepest come first, and a tile goes
+// to the block of its XCD that has the least to do (405M list: 1.35 ms for
+// X X^T, 1.50 with every 256th tile to a block).
+void add_tiles(OrthoPlan* plan, size_t first, int tile, bool symmetric, int32_t* blocks) {
     constexpr int kBand = 4;
+    const double besides = tile == 256 ? 8.0 : 10.0;         // stages that a tile costs besides its own
     const auto depth = [&](uint32_t k) { return stages_of(symmetric ? plan->items[k].l : plan->items[k].s); };
     std::vector<uint32_t> order;
     for (size_t k = first; k < plan->items.size(); ++k) order.push_back((uint32_t)k);
     std::stable_sort(order.begin(), order.end(), [&](uint32_t a, uint32_t b) { return depth(a) > depth(b); });
-    for (size_t o = 0; o < order.size();) {
-        const size_t run = plan->tiles.size();
-        const int d = depth(order[o]);
-        for (; o < order.size() && depth(order[o]) == d; ++o) {
-            const uint32_t k = order[o];
-            const int n = plan->items[k].sp / tile, nl = symmetric ? n : plan->items[k].lp / tile;
-            for (int i0 = 0; i0 < n; i0 += kBand)
-                for (int j = 0; j < (symmetric ? std::min(i0 + kBand, n) : nl); ++j)
-                    for (int i = symmetric ? std::max(i0, j) : i0; i < std::min(i0 + kBand, n); ++i)
-                        plan->tiles.push_back({k, (uint16_t)i, (uint16_t)j});
-        }
-        deal_out(plan->tiles, run);
+    std::vector<std::pair<double, std::vector<TileRef>>> runs;       // of one depth
+    int64_t all = 0;
+    for (const uint32_t k : order) {
+        const double cost = depth(k) + besides;
+        if (runs.empty() || runs.back().first != cost) runs.push_back({cost, {}});
+        std::vector<TileRef>& run = runs.back().second;
+        const int n = plan->items[k].sp / tile, nl = symmetric ? n : plan->items[k].lp / tile;
+        for (int i0 = 0; i0 < n; i0 += kBand)
+            for (int j = 0; j < (symmetric ? std::min(i0 + kBand, n) : nl); ++j)
+                for (int i = symmetric ? std::max(i0, j) : i0; i < std::min(i0 + kBand, n); ++i)
+                    run.push_back({k, (uint16_t)i, (uint16_t)j});
+        all += (int64_t)n * nl;
     }
+    *blocks = (int32_t)std::min<int64_t>(most_blocks(tile), pad_to(all, kXCDs));
+    struct Block {
+        double load;
+        int index;
+        bool operator<(const Block& o) const { return load != o.load ? load > o.load : index > o.index; }     // for a heap with the least on top
+    };
+    std::vector<std::vector<Block>> heaps(kXCDs);
+    for (int b = 0; b < *blocks; ++b) heaps[b % kXCDs].push_back({0.0, b});
+    std::vector<std::vector<TileRef>> work(*blocks);
+    size_t offset = 0;                                       // the XCD that the next run's odd tiles begin with
+    for (const auto& [cost, run] : runs) {
+        size_t next = 0;
+        for (int x = 0; x < kXCDs; ++x) {
+            const size_t xcd = (x + offset) % kXCDs, share = run.size() / kXCDs + ((size_t)x < run.size() % kXCDs);
+            for (size_t k = 0; k < share; ++k) {
+                std::vector<Block>& heap = heaps[xcd];
+                std::pop_heap(heap.begin(), heap.end());
+                work[heap.back().index].push_back(run[next++]);
+                heap.back().load += cost;
+                std::push_heap(heap.begin(), heap.end());
+            }
+        }
+        offset += run.size();
+    }
+    size_t rounds = 0;
+    for (const auto& w : work) rounds = std::max(rounds, w.size());
+    for (size_t r = 0; r < rounds; ++r)
+        for (const auto& w : work) plan->tiles.push_back(r < w.size() ? w[r] : TileRef{kNoItem, 0, 0});
 }
-
-constexpr int64_t kCUs = 256;
 
 template <int MODE>
 int launch_product(const OrthoPass& p, const NsRef& ref, const NsStep& step, hipStream_t s) {
     const int64_t first = MODE == kApply ? p.x_first : p.sym_first, n = MODE == kApply ? p.n_x : p.n_sym;
-    // as many blocks as the LDS lets the CUs hold: each works off every so many tiles
-    const dim3 grid((unsigned)std::min(n, kCUs * (p.tile == 256 ? 1 : p.tile == 128 ? 2 : 4)));
+    const dim3 grid((unsigned)(MODE == kApply ? p.x_blocks : p.sym_blocks));
     if (p.tile == 256)
         hipLaunchKernelGGL((ortho_product<256, 2, 4, MODE>), grid, dim3(512), 0, s, ref, first, n, step);
     else if (p.tile == 128)
@@ -611,10 +637,10 @@ int plan_ortho(const std::vector<OrthoMatrix>& matrices, OrthoPlan* plan) {
         pass.n_items = (int32_t)(end - done);
         done = end;
         pass.sym_first = (int64_t)plan->tiles.size();
-        add_tiles(plan, first_item, tile, true);
+        add_tiles(plan, first_item, tile, true, &pass.sym_blocks);
         pass.n_sym = (int64_t)plan->tiles.size() - pass.sym_first;
         pass.x_first = (int64_t)plan->tiles.size();
-        add_tiles(plan, first_item, tile, false);
+        add_tiles(plan, first_item, tile, false, &pass.x_blocks);
         pass.n_x = (int64_t)plan->tiles.size() - pass.x_first;
         pass.piece_first = (int64_t)plan->tiles.size();
         for (size_t k = first_item; k < plan->items.size(); ++k)
