@@ -68,9 +68,10 @@ __device__ __forceinline__ h4 lds_column(uint32_t a) {
 constexpr int kThreads = 256;
 constexpr int kChunkElements = 16384;            // of a box: 64 a thread, as eight vectors of eight
 
-// Eight consecutive elements, the first `valid` of them; whole: eight may be read.
+// Eight consecutive elements, the first `valid` of them; whole: eight may be read;
+// full: all are valid.
 template <int DT>
-__device__ __forceinline__ void ld8(const void* U, int64_t e, int valid, bool whole, float v[8]) {
+__device__ __forceinline__ void ld8(const void* U, int64_t e, int valid, bool whole, bool full, float v[8]) {
     if (whole) {
         if constexpr (DT == ZERO_F32) {
             const f32x4 a = ld_any(static_cast<const float*>(U) + e), b = ld_any(static_cast<const float*>(U) + e + 4);
@@ -84,6 +85,7 @@ __device__ __forceinline__ void ld8(const void* U, int64_t e, int valid, bool wh
 #pragma unroll
             for (int k = 0; k < 4; ++k) unpack2<DT>(w[k], v[2 * k], v[2 * k + 1]);
         }
+        if (full) return;
 #pragma unroll
         for (int k = 0; k < 8; ++k) v[k] = k < valid ? v[k] : 0.0f;
     } else {
@@ -134,17 +136,20 @@ __device__ __forceinline__ void load_box(const void* U, int s, int l, int tall, 
     // a vector may run over its row's end into the next row, but not over the matrix's
     const int64_t r_last = (r0 + ROWS < s ? r0 + ROWS : s) - 1, c_last = (c0 + kColumns < l ? c0 + kColumns : l) - 1;
     const int64_t last = tall ? c_last * s + r_last : r_last * (int64_t)l + c_last;
-    if (last + 8 <= all) {
+    if (r0 + ROWS <= s && c0 + kColumns <= l) {
+#pragma unroll
+        for (int n = 0; n < 8; ++n) ld8<DT>(U, Vector8<ROWS, BAND>(s, l, tall, r0, c0, n).at, 8, true, true, x[n]);
+    } else if (last + 8 <= all) {
 #pragma unroll
         for (int n = 0; n < 8; ++n) {
             const Vector8<ROWS, BAND> v(s, l, tall, r0, c0, n);
-            ld8<DT>(U, v.valid ? v.at : 0, v.valid, true, x[n]);
+            ld8<DT>(U, v.valid ? v.at : 0, v.valid, true, false, x[n]);
         }
     } else {
 #pragma unroll
         for (int n = 0; n < 8; ++n) {
             const Vector8<ROWS, BAND> v(s, l, tall, r0, c0, n);
-            ld8<DT>(U, v.valid ? v.at : 0, v.valid, v.valid > 0 && v.at + 8 <= all, x[n]);
+            ld8<DT>(U, v.valid ? v.at : 0, v.valid, v.valid > 0 && v.at + 8 <= all, false, x[n]);
         }
     }
 }

@@ -276,16 +276,17 @@ __device__ __forceinline__ f32x4 square_product(uint32_t a, uint32_t b, int i, i
     return sum;
 }
 
-// A tile of B for the third kernel, as its fragments: [i][k / 32][lane][8] halves
-// with the inner elements of a lane in the order 4 g .. + 3 of two tiles of 16.
+// A tile of B for the third kernel, where it is added to a I and needs no scale,
+// as its fragments: [i][k / 32][lane][8] halves with the inner elements of a lane in the order 4 g .. + 3 of two tiles of 16.
 template <int SP>
 __device__ __forceinline__ void put_fragments(_Float16* to, int i, int j, int lane, const f32x4& v) {
     const int g = lane >> 4, c = lane & 15;
     h4 h, l;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        h[e] = (_Float16)v[e];
-        l[e] = (_Float16)(v[e] - (float)h[e]);
+        const float x = v[e] * (1.0f / (1 << kLog2A));
+        h[e] = (_Float16)x;
+        l[e] = (_Float16)(x - (float)h[e]);
     }
     _Float16* at = to + (((j * (SP / 32) + i / 2) * 64 + g * 16 + c) * 8 + (i & 1) * 4);
     *reinterpret_cast<h4*>(at) = h;
@@ -427,7 +428,7 @@ __device__ __forceinline__ void store_chunk(const ZS_CONSTANT ThinItem& m, int64
 // .. + 3 of a column, which is how the next product takes it: with the inner
 // elements in the order of put_fragments nothing moves between lanes.
 template <int SP>
-__global__ __launch_bounds__(kThreads) void thin_apply(NsRef ref, int64_t first, ThinSteps steps) {
+__global__ __launch_bounds__(kThreads, 2) void thin_apply(NsRef ref, int64_t first, ThinSteps steps) {
     using H = Thin<SP>;
     constexpr int R = H::kR, kStrips = H::kLC / 64, kB = H::kB, kLoads = kB / 8 / kThreads;
     if (ref.skipped()) return;
@@ -497,13 +498,14 @@ __global__ __launch_bounds__(kThreads) void thin_apply(NsRef ref, int64_t first,
                     if (H::kTwo) xl[y][i / 2][(i & 1) * 4 + e] = (_Float16)(X[y][i][e] - (float)h);
                 }
         const float a = steps.a[step];
-        constexpr float kDown = 1.0f / (1 << kLog2A);
         const uint32_t b = lds_address(place) + lane * 16;
 #pragma unroll
         for (int i = 0; i < R; ++i) {
             f32x4 sum[kStrips];
 #pragma unroll
-            for (int y = 0; y < kStrips; ++y) sum[y] = f32x4{};
+            for (int y = 0; y < kStrips; ++y)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sum[y][e] = a * X[y][i][e];
 #pragma unroll
             for (int k = 0; k < R / 2; ++k) {
                 const h8 bh = lds_h8(b + (i * (SP / 32) + k) * 1024);
@@ -519,9 +521,7 @@ __global__ __launch_bounds__(kThreads) void thin_apply(NsRef ref, int64_t first,
                 }
             }
 #pragma unroll
-            for (int y = 0; y < kStrips; ++y)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) X[y][i][e] = fmaf(a, X[y][i][e], sum[y][e] * kDown);
+            for (int y = 0; y < kStrips; ++y) X[y][i] = sum[y];
         }
     }
     __syncthreads();
