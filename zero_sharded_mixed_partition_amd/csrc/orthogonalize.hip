@@ -145,9 +145,13 @@ __device__ __forceinline__ void load_lds(const void* base, uint32_t offset, uint
 //
 // A stage is 32 inner elements of both operands, 64 bytes a row: 16 rows for
 // each 1 KB that a wave loads at a time, straight into the LDS.  Four stages lie
-// there; two are on their way while one is multiplied, since a load that misses
-// the L2 takes longer than a stage.  One barrier a stage: behind it the next
-// stage has landed for all waves, and the last one's place is free.
+// there (five at T 64, whose stages are the shortest); all but the one that is
+// multiplied and the next are on their way, since a load that misses the L2 takes
+// longer than a stage.  (T 256, products of X: 2.70 ms with four stages, 2.69
+// with five, 3.81 with three.  T 64, one matrix of 1024 x 8192: 460 us with four
+// and four blocks a CU, 390 with five and three, 409 with six and two; 42 of 331
+// x 881: 276, 282 and 310.)  One barrier a stage: behind it the next stage has
+// landed for all waves, and the last one's place is free.
 //
 // Operands in the LDS, as the 16 x 16 x 32 MFMA takes them (lane l: row or
 // column l % 16, inner elements 8 (l / 16) .. + 7):
@@ -165,7 +169,7 @@ struct Product {
     static constexpr int kUM = T / WM / 16, kUN = T / WN / 16;       // 16 x 16 results per wave
     static constexpr int kOperand = T * kPanel * 2;                  // bytes of a stage
     static constexpr int kLoads = kOperand / 1024 / kWaves;          // per wave and operand
-    static constexpr int kStages = 4;
+    static constexpr int kStages = T == 64 ? 5 : 4;
     static constexpr int kStage = 2 * kOperand;
     static constexpr int kMirror = 2 * 16 * (T / WN) * 2;            // of a wave: 32 rows of its mirrored results
     static constexpr int kLds = kStages * kStage + kWaves * kMirror;
@@ -333,7 +337,7 @@ __global__ __launch_bounds__(64 * WM * WN) void ortho_product(NsRef ref, int64_t
         next = next == (S - 1) * P::kStage ? 0 : next + P::kStage;
     };
 
-    for (int k = 0; k < S - 1; ++k)                // no tile has fewer stages
+    for (int k = 0; k < S - 1; ++k)                // every tile has more
 #pragma unroll
         for (int q = 0; q < NL; ++q) load(q);
     wait_stage<(S - 2) * NL>();
@@ -360,7 +364,7 @@ __global__ __launch_bounds__(64 * WM * WN) void ortho_product(NsRef ref, int64_t
             if (k >= landed) wait_stage<(S - 3) * NL>();
             else __asm__ volatile("s_barrier" ::: "memory");
             multiply(std::integral_constant<int, 0>{});
-            if (k >= landed) wait_stage<(S - 3) * NL>();
+            if (k + 1 >= landed) wait_stage<(S - 3) * NL>();
             else __asm__ volatile("s_barrier" ::: "memory");
             multiply(std::integral_constant<int, 1>{});
         }
@@ -421,7 +425,7 @@ __global__ __launch_bounds__(64 * WM * WN) void ortho_product(NsRef ref, int64_t
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
                                 const float v = fmaf(step.b, (float)a[e], acc[x + z][y][e] * scale);
-                                h[e] = (_Float16)(ti == tj && im + (x + z) * 16 + e == in + y * 16 ? v + diagonal : v);
+                                h[e] = to_half(ti == tj && im + (x + z) * 16 + e == in + y * 16 ? v + diagonal : v);
                             }
                         }
                         *reinterpret_cast<h4*>(out + at(x + z, y)) = h;
@@ -451,15 +455,15 @@ __global__ __launch_bounds__(64 * WM * WN) void ortho_product(NsRef ref, int64_t
 
 // What one step of the products is taken to cost with tiles of this size, in
 // microseconds: per product the larger of one tile's chain of stages and of all
-// tiles over the CUs.  A tile costs c0 besides its stages (start, first loads,
-// stores), and a chain of stages alone in its CU is slower than several (c1
-// against c1_full).  Measured with every size (64, 128, 256) on 19 lists: one of
-// 512 x 512 takes 86, 166 and 364 us, 64 of 512 x 2048 1427, 1310 and 1267, one
-// of 4096 x 4096 2109, 1693 and 1589, 4 of 1024 x 4096 578, 558 and 840; the
-// size that this picks is within 8% of the fastest on all of them.
+// tiles over the CUs.  A tile costs c0 besides its stages, and a chain of stages
+// alone in its CU is slower than several (c1 against c1_full).  Measured with
+// tiles of 64, 128 and 256 on 19 lists: one matrix of 512 x 512 takes 92, 141 and
+// 270 us, 64 of 512 x 2048 1278, 1059 and 943, one of 4096 x 4096 2144, 1573 and
+// 1446, 4 of 1024 x 4096 550, 475 and 769; the size that this picks is within 5%
+// of the fastest on all of them.
 double step_cost(const std::vector<OrthoMatrix>& matrices, int tile) {
-    const double c0 = tile == 256 ? 21.0 : tile == 128 ? 4.8 : 0.82, first = tile == 256 ? 13.5 : tile == 128 ? 5.0 : 2.1;
-    const double c1 = tile == 256 ? 0.68 : tile == 128 ? 0.30 : 0.20, c1_full = tile == 256 ? 0.68 : tile == 128 ? 0.32 : 0.105;
+    const double c0 = tile == 256 ? 12.0 : tile == 128 ? 2.4 : 0.55, first = tile == 256 ? 12.0 : tile == 128 ? 5.0 : 2.3;
+    const double c1 = tile == 256 ? 0.68 : tile == 128 ? 0.23 : 0.19, c1_full = tile == 256 ? 0.68 : tile == 128 ? 0.28 : 0.098;
     double cost = 0.0;
     for (int product = 0; product < 3; ++product) {
         double tiles = 0.0, work = 0.0, deepest = 0.0;
@@ -492,7 +496,7 @@ void place_item(MatrixItem* it, int64_t* at) {
 constexpr int kXCDs = 8, kCUs = 256;
 
 // Blocks of a product: as many as the LDS lets the CUs hold.
-int most_blocks(int tile) { return kCUs * (tile == 256 ? 1 : tile == 128 ? 2 : 4); }
+int most_blocks(int tile) { return kCUs * (tile == 256 ? 1 : tile == 128 ? 2 : 3); }
 
 // The tiles of the symmetric products (lower triangle), or of the iterate, of
 // the items from `first` on, as rounds of one tile per block.  Blocks go to the
