@@ -341,6 +341,28 @@ def test_a_list_in_several_parts(Z):
         assert torch.equal(bits(u[k]), bits(o)), k
 
 
+@pytest.mark.parametrize("shape", [(130, 1 << 21), ((1 << 22) - 3, 5), (70, 1 << 22), (1 << 20, 300)], ids=lambda s: "x".join(map(str, s)))
+def test_long_sides(Z, shape):
+    """Up to the longest side: against the definition in float64 on the device."""
+    u = torch.empty(shape, dtype=torch.bfloat16, device="cuda")
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    for k in range(0, shape[0], 1 << 16):
+        part = u[k:k + (1 << 16)]
+        part.copy_(torch.randn(part.shape, device="cuda", generator=gen))
+    o = torch.empty_like(u)
+    orthogonalize(Z, Z.MatrixTable([u], [o]))
+    tall = shape[0] > shape[1]
+    x = (u.T if tall else u).double()
+    x /= x.norm()
+    for a, b, c in M.COEFS:
+        g = x @ x.T
+        x = (a * torch.eye(len(g), dtype=torch.float64, device="cuda") + b * g + c * (g @ g)) @ x
+    off = float(((o.T if tall else o).double() - x).norm() / x.norm())
+    # bf16's half step, at most 2^-8 of each value, and twice what the model of the
+    # roundings gives where all singular values are alike, as here (1.2e-3)
+    assert off <= 2.0 ** -8 + 2 * 1.2e-3, off
+
+
 def test_device_of_the_table(Z):
     u = torch.zeros(4, 6, dtype=torch.bfloat16, device="cuda")
     table = Z.MatrixTable([u])
@@ -352,3 +374,5 @@ def test_device_of_the_table(Z):
         Z.zero_multi_orthogonalize(table, torch.empty(256, dtype=torch.uint8, device="cuda"))
     with pytest.raises(ValueError, match="without gradients"):
         table.set_grads([u])
+    table.release_grads()
+    orthogonalize(Z, table)

@@ -64,7 +64,8 @@ def test_table_refusals():
     assert build([matrix(update=AL + 3 * STEP + 2, update_dtype=L.ZERO_F32)])[0] == L.ZERO_EALIGN
     assert build([matrix(grad=AL + 2 * STEP + 2, grad_dtype=L.ZERO_F32)])[0] == L.ZERO_EALIGN
     for bad in (dict(rows=(1 << 22) + 1), dict(cols=(1 << 22) + 1), dict(rows=1 << 22, cols=1 << 22, batch=1 << 20),
-                dict(rows=1 << 22, cols=1 << 22, batch=1 << 62)):
+                dict(rows=1 << 22, cols=1 << 22, batch=1 << 62), dict(rows=1 << 22, cols=1 << 22), dict(rows=1, cols=1, batch=1 << 25),
+                dict(rows=1 << 21, cols=1 << 20)):
         assert build([matrix(**bad)])[0] == L.ZERO_ERANGE, bad
     assert build([matrix()], capacity=10)[0] == L.ZERO_ENOSPC
     lib, s = L.lib(), ctypes.c_size_t()

@@ -17,6 +17,8 @@
 namespace zero_shard {
 namespace {
 
+// What a table describes fits any GPU's memory: its maps stay small too.
+constexpr int64_t kMostElements = int64_t(1) << 40, kMostMatrices = 1 << 24;
 constexpr int64_t kMaxGrid = (int64_t(1) << 26) - 1;
 constexpr size_t kLdsMomentum = 0, kLdsUpdate = 0;
 
@@ -111,6 +113,7 @@ __device__ __forceinline__ void momentum_task_u(const ZS_CONSTANT MatrixDesc& d,
 
 // The gradients' factor comes by value, or from d_step (a coefficient block
 // formed on the device).
+template <bool DEVICE>
 __global__ __launch_bounds__(kTaskThreads) void matrix_momentum(MuonSet set, StepCoef by_value, const StepCoef* __restrict__ d_step,
                                                                 MatrixRef t, const double* __restrict__ d_sq,
                                                                 const int32_t* __restrict__ d_ovf) {
@@ -122,7 +125,9 @@ __global__ __launch_bounds__(kTaskThreads) void matrix_momentum(MuonSet set, Ste
         const int64_t base = task * kTask - d.momentum_shift;
         if (base >= d.numel) continue;
         const MuonCoef c = set.c[d.group];
-        const StepCoef step = d_step != nullptr ? *d_step : by_value;
+        StepCoef step;
+        if constexpr (DEVICE) step = *d_step;
+        else step = by_value;
         if (d.gdt == ZERO_F16) momentum_task_u<ZERO_F16>(d, base, c, step, d_sq);
         else if (d.gdt == ZERO_BF16) momentum_task_u<ZERO_BF16>(d, base, c, step, d_sq);
         else momentum_task_u<ZERO_F32>(d, base, c, step, d_sq);
@@ -205,7 +210,7 @@ int check_matrix(const zero_matrix& m, int32_t i, int64_t* numel) {
     if (m.rows < 0 || m.cols < 0 || m.batch < 0) return fail(ZERO_EINVAL, "matrix %d: negative size", i);
     if (m.rows > ZERO_MAX_MATRIX_SIDE || m.cols > ZERO_MAX_MATRIX_SIDE)
         return fail(ZERO_ERANGE, "matrix %d: a side above %d", i, ZERO_MAX_MATRIX_SIDE);
-    if (__builtin_mul_overflow(m.rows * m.cols, m.batch, numel) || *numel > INT64_MAX / 8)
+    if (__builtin_mul_overflow(m.rows * m.cols, m.batch, numel) || *numel > kMostElements)
         return fail(ZERO_ERANGE, "matrix %d: numel too large", i);
     if (m.group < 0 || m.group >= ZERO_MAX_GROUPS)
         return fail(ZERO_EINVAL, "matrix %d: group %d outside [0, %d)", i, m.group, ZERO_MAX_GROUPS);
@@ -241,7 +246,7 @@ int build_matrix_table(const zero_matrix* matrices, int32_t n, void* table, size
     std::vector<MatrixDesc> desc;
     std::vector<OrthoMatrix> singles;
     std::vector<int64_t> momentum_tasks, master_tasks;
-    int64_t n_singles = 0;
+    int64_t n_singles = 0, n_elements = 0;
     for (int32_t i = 0; i < n; ++i) {
         const zero_matrix& m = matrices[i];
         int64_t numel = 0;
@@ -281,8 +286,9 @@ int build_matrix_table(const zero_matrix* matrices, int32_t n, void* table, size
         desc.push_back(d);
         momentum_tasks.push_back(tasks_of(numel, d.momentum_shift));
         master_tasks.push_back(tasks_of(numel, d.master_shift));
+        n_elements += numel;
         n_singles += m.batch;
-        if (n_singles > INT32_MAX) return fail(ZERO_ERANGE, "the list is too long");
+        if (n_singles > kMostMatrices || n_elements > kMostElements) return fail(ZERO_ERANGE, "the list is too long");
     }
     h.n_entries = (int32_t)desc.size();
     std::vector<AddressRange> ranges, reads;
@@ -388,8 +394,13 @@ int momentum_step(const void* table, const void* d_table, const zero_muon_params
     if (rc != ZERO_OK || h.n_entries == 0) return rc;
     const MatrixRef t{at<MatrixDesc>(d_table, h.desc_at), at<PieceRef>(d_table, h.momentum_at), h.n_momentum,
                       h.momentum_log2};
-    hipLaunchKernelGGL(matrix_momentum, task_grid(h.n_momentum, h.momentum_log2), dim3(kTaskThreads), kLdsMomentum,
-                       static_cast<hipStream_t>(hip_stream), set, c, static_cast<const StepCoef*>(d_coef), t, d_sq, d_ovf);
+    const dim3 grid = task_grid(h.n_momentum, h.momentum_log2);
+    const hipStream_t s = static_cast<hipStream_t>(hip_stream);
+    const StepCoef* d_step = static_cast<const StepCoef*>(d_coef);
+    if (d_step != nullptr)
+        hipLaunchKernelGGL(matrix_momentum<true>, grid, dim3(kTaskThreads), kLdsMomentum, s, set, c, d_step, t, d_sq, d_ovf);
+    else
+        hipLaunchKernelGGL(matrix_momentum<false>, grid, dim3(kTaskThreads), kLdsMomentum, s, set, c, d_step, t, d_sq, d_ovf);
     return launch_status("matrix_momentum");
 }
 

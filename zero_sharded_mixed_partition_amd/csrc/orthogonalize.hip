@@ -494,6 +494,7 @@ void place_item(MatrixItem* it, int64_t* at) {
 }
 
 constexpr int kXCDs = 8, kCUs = 256;
+constexpr int64_t kMostTiles = 1 << 26;      // beyond any GPU's memory
 
 // Blocks of a product: as many as the LDS lets the CUs hold.
 int most_blocks(int tile) { return kCUs * (tile == 256 ? 1 : tile == 128 ? 2 : 3); }
@@ -600,9 +601,11 @@ int plan_ortho(const std::vector<OrthoMatrix>& matrices, OrthoPlan* plan) {
     int tile = 64;
     for (const int other : {128, 256})
         if (step_cost(matrices, other) < step_cost(matrices, tile)) tile = other;
-    int64_t total = 0;
+    int64_t total = 0, n_all = 0;
     for (const OrthoMatrix& m : matrices) {
         if (std::min(m.rows, m.cols) <= kThin) continue;
+        n_all += pad_to(m.rows, tile) / tile * (pad_to(m.cols, tile) / tile);
+        if (n_all > kMostTiles) return fail(ZERO_ERANGE, "the list is too long");
         MatrixItem it{};
         it.in = m.in;
         it.out = m.out;
@@ -615,7 +618,6 @@ int plan_ortho(const std::vector<OrthoMatrix>& matrices, OrthoPlan* plan) {
         it.odt = m.odt;
         it.log2_scale = log2_scale(it.l);
         const int64_t n_slots = pad_to(it.s, kPieceRows) / kPieceRows * (pad_to(it.l, kPieceColumns) / kPieceColumns);
-        if (n_slots > INT32_MAX) return fail(ZERO_ERANGE, "a matrix of %d x %d is too large", it.s, it.l);
         it.n_slots = (int32_t)n_slots;
         place_item(&it, &total);
         mine.push_back(it);
@@ -652,7 +654,6 @@ int plan_ortho(const std::vector<OrthoMatrix>& matrices, OrthoPlan* plan) {
                 for (int j = 0; j < (int)(pad_to(plan->items[k].lp, kPieceColumns) / kPieceColumns); ++j)
                     plan->tiles.push_back({(uint32_t)k, (uint16_t)i, (uint16_t)j});
         pass.n_pieces = (int64_t)plan->tiles.size() - pass.piece_first;
-        if (std::max({pass.n_x, pass.n_sym, pass.n_pieces}) > INT32_MAX) return fail(ZERO_ERANGE, "the list is too long");
         plan->passes.push_back(pass);
     }
     return plan_thin(matrices, plan);

@@ -98,6 +98,11 @@ class MatrixTable(TensorTable):
                 raise ValueError(f"grads[{i}]: shape {tuple(g.shape)}, {shape} expected")
         super().set_grads(grads)
 
+    def release_grads(self) -> None:
+        """TensorTable.release_grads; nothing where the table has no gradients."""
+        if self._has_grads:
+            super().release_grads()
+
     def _describe(self, shaped) -> None:
         self._c = (_L.zero_matrix * max(1, self.n_tensors))()
         self._index = shaped[0].get_device() if shaped and hasattr(shaped[0], "get_device") else -1
