@@ -113,7 +113,7 @@ def test_lists_batches_and_places_do_not_matter(Z):
 @pytest.mark.parametrize("shape", [(5, 9), (64, 64), (200, 130), (300, 513), (1100, 1030)], ids=lambda s: "x".join(map(str, s)))
 def test_sizes_of_values(Z, shape):
     """Scaling U by a power of two changes nothing, up to the ends of the types;
-    zero gives zero; a norm below eps divides by eps."""
+    zero gives zero, whatever eps; a norm below eps divides by eps."""
     x = draw(shape, 3, size=1.0)
     base = None
     for e in (0, 40, -40, 100, -100):
@@ -125,7 +125,7 @@ def test_sizes_of_values(Z, shape):
             check(o, u, "bf16", eps=0.0)
         assert torch.equal(bits(o), bits(base)), e
     u, _ = place(np.zeros(shape), "f32")
-    for eps in (0.0, 1e-7):
+    for eps in (0.0, 1e-7, 1e-320, 1e300):
         o = torch.full(shape, 7.0, dtype=torch.float16, device="cuda")
         orthogonalize(Z, Z.MatrixTable([u], [o]), eps=eps)
         assert not o.any()

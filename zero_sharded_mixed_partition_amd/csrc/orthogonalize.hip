@@ -138,7 +138,7 @@ __device__ __forceinline__ void load_lds(const void* base, uint32_t offset, uint
     __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
                      :
                      : "s"(lds), "v"(offset), "s"(base)
-                     : "memory");
+                     : "memory", "m0");
 }
 
 // A wave's share of a T x T tile of a product, WM x WN waves.
@@ -682,6 +682,8 @@ int zero_multi_orthogonalize(const void* table, const void* d_table, const doubl
     if (rc == ZERO_OK) rc = check_coefs(coefs, n_steps);
     if (rc != ZERO_OK) return rc;
     if (!(eps >= 0.0) || !std::isfinite(eps)) return fail(ZERO_EINVAL, "eps must be finite and >= 0");
+    // below the least norm that is not zero eps decides nothing, and 1 / eps might not be finite
+    if (eps < 0x1p-149) eps = 0.0;
     if ((uintptr_t)d_global_overflow & 3u) return fail(ZERO_EALIGN, "d_global_overflow misaligned");
     if (h.n_entries == 0) return ZERO_OK;
     if (d_workspace == nullptr) return fail(ZERO_EINVAL, "d_workspace is NULL");
