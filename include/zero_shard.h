@@ -748,7 +748,8 @@ int zero_multi_adam_step_coef(const void* table, const void* d_table, const void
  *  scale       finite factor of the learning rate for this matrix
  *  group       index into the step's hyperparameters, [0, ZERO_MAX_GROUPS)
  * Matrices are row-major without gaps, and pointers need only be aligned to
- * their elements.  A matrix may be empty.  Sides reach ZERO_MAX_MATRIX_SIDE.
+ * their elements.  A matrix may be empty.  Sides reach ZERO_MAX_MATRIX_SIDE, a
+ * list 2^24 matrices and 2^40 elements.
  * A call needs the buffers that it names below on every matrix that has
  * elements; the others may be NULL.  Gradients may share memory with one
  * another; no other buffer may overlap another one of the list.  A matrix has to
@@ -756,8 +757,8 @@ int zero_multi_adam_step_coef(const void* table, const void* d_table, const void
  * first.
  *
  * zero_matrix_table_build (host only): as zero_multi_table_build, the table of
- *   such a list.  About 16 bytes per 8192 elements, 100 per matrix and 16 per
- *   tile of the products.
+ *   such a list.  About 16 bytes per 8192 elements, 180 per matrix and 8 per
+ *   tile of the products (64 to 256 rows and columns).
  * zero_multi_momentum_step (momentum, grad, update): per element, in float32,
  *     g = (1 - mu) * (grad * s);  m = fma(mu, m, g);  u = nesterov ? fma(mu, m, g) : m
  *   with s the factor of zero_shard_adam_step (the inverse loss scale times the
@@ -770,17 +771,24 @@ int zero_multi_adam_step_coef(const void* table, const void* d_table, const void
  *     X = U / max(|U|, eps);  n_steps times  X = a X + (b X X^T + c X X^T X X^T) X
  *   with (a, b, c) = coefs[3 k .. 3 k + 2] at step k; ortho = X.  (For X with
  *   more rows than columns X X^T ... X is formed as X ... X^T X, which is equal.)
- *   eps = 0 leaves a zero matrix zero.  X and the products are rounded to fp16
- *   between steps, sums are float32: about 1.2e-3 off in all (relative,
- *   Frobenius) with five steps of (3.4445, -4.7750, 2.0315) where singular values
- *   are spread as those of a random matrix, more where they differ by
- *   thousands.  A matrix that holds an inf or a NaN becomes NaN.  Coefficients
- *   have to keep singular values of [0, 1] within 4, and |b x + c x^2| of their
- *   squares within 32 (ZERO_ERANGE).  1 <= n_steps <= ZERO_MAX_ORTHO_STEPS.
+ *   eps = 0 leaves a zero matrix zero.  A matrix that holds an inf or a NaN
+ *   becomes NaN.  Where the short side exceeds 128, X, X X^T and the polynomial
+ *   are rounded to fp16 between products; up to 128, X stays in float32, X X^T is
+ *   carried on through the steps with 22 bits, and the polynomial has 11 bits (22
+ *   up to 64).  Sums are float32.  Besides its own rounding the result of five steps
+ *   of (3.4445, -4.7750, 2.0315) is off (relative, Frobenius) by about 1e-4 with a
+ *   short side up to 64 and 1.2e-3 above it for random matrices, by up to 1e-3 and
+ *   1.7e-3 where a strong low-rank part is added (2.5e-3 seen), and by 4e-3 for
+ *   1024 singular values that fall as 1, 1/2, 1/3, ...
+ *   Coefficients have to keep singular values of [0, 1] within 4, and
+ *   |b x + c x^2| and |a + b x + c x^2| of their squares x within 32
+ *   (ZERO_ERANGE).  1 <= n_steps <= ZERO_MAX_ORTHO_STEPS.
  *   Workspace: zero_multi_orthogonalize_workspace_bytes(table) bytes, 256-byte
- *   aligned, clobbered: about 4 bytes an element, and 4 for each of a short
- *   side's square, of the list or of a part of it of 4 GiB.  Calls, and graphs
- *   recorded with them, that may run at the same time need a workspace each.
+ *   aligned, clobbered.  A matrix takes about 4 bytes an element and 4 for each of
+ *   its short side's square; with a short side of at most 32, 64 or 128, 0.13, 0.5
+ *   or 1 MB and its parts, at most 2 MB.  A list that would take more than 4 GiB
+ *   is worked off in parts.  Calls, and graphs recorded with them, that may run at
+ *   the same time need a workspace each.
  * zero_multi_muon_update (master, ortho; param_out): per element, in float32,
  *     p = fma(p, 1 - lr * weight_decay, -((lr * scale) * o));  param = round(p)
  * With d_global_overflow given and nonzero when the kernels run, a call writes
