@@ -6,17 +6,29 @@
 // transposed, which its first load and last store do.
 //
 // What is rounded.  The iterate X and the two symmetric s x s matrices A and
-// B = b A + c A A are held in fp16 between the products, each times a power of
-// two that keeps typical entries far from fp16's small end (X: about sqrt(l),
-// A and B: 2^10); every sum is float32, |U|_F float64.  fp16 instead of bf16
-// because the iteration multiplies what is lost: on 1024 x 1024 matrices of
+// Q = a I + b A + c A A are held in fp16 between the products, each times a
+// power of two that keeps typical entries far from fp16's small end (X: about
+// sqrt(l), A and Q: 2^10); every sum is float32, |U|_F float64.  fp16 instead of
+// bf16 because the iteration multiplies what is lost: on 1024 x 1024 matrices of
 // noise plus a low-rank part the result is 1.2e-3 off (relative, Frobenius)
 // with fp16 in these places and 1e-2 with bf16, at the same MFMA rate.
 //
-// Products.  All three run through one MFMA kernel in square tiles of T x T
-// over a padded copy in the workspace, so no load is bounded and padding stays
-// zero.  X X^T and A A are symmetric: only tiles on and below the diagonal are
-// formed, and stored twice.
+// Products.  A step is three, X X^T, A A and Q X, in square tiles of T x T over
+// a padded copy in the workspace, so no load is bounded and padding stays zero.
+// X X^T and A A are symmetric: only tiles on and below the diagonal are formed,
+// and stored twice.  T is 64, 128 or 256 for a whole list (step_cost); what a
+// matrix becomes does not depend on it.  A product is one launch, the blocks
+// that fit the CUs, which work off lists of tiles.
+//
+// What bounds it.  192 matrices of 405M elements (96 of 1024 x 1024, 96 of 1024
+// x 2752), us of a step: X X^T 1343, A A 902, Q X 2708, in tiles of 256; with 2 m
+// n k for a product, half of it for the symmetric ones, 1.1 to 1.3e15 a second,
+// where the loops between a tile's first loads and its stores run at 1.5e15,
+// about what a large matrix product of a library reaches.  The MFMAs are busy 77%
+// of the time at 1.7 GHz, to which the power limit takes the clock from 2.4: more
+// waves, deeper stages and the larger MFMA gain nothing, 32 x 32 x 16 loses 4%.
+// HBM is not what bounds: Q X reads and writes 6.0 GB in 2.7 ms.  Small lists are
+// bound by their 2 + 3 n_steps launches of 4 to 6 us, one after the other.
 #include <hip/hip_runtime.h>
 
 #include <cmath>
@@ -50,7 +62,8 @@ __device__ __forceinline__ void load_piece(const ZS_CONSTANT MatrixItem& m, int 
     load_box<kPieceRows, D>(m.udt, m.in, m.s, m.l, m.tall, r0, c0, x);
 }
 
-// One piece's sum of squares into its slot.
+// One piece's sum of squares into its slot.  A read of U: 405M elements of bf16,
+// 810 MB, take 127 us, 6.4 TB/s.
 __global__ __launch_bounds__(kBlock) void ortho_squares(NsRef ref, int64_t first) {
     if (ref.skipped()) return;
     __shared__ double s_sq[kWaves];
@@ -88,7 +101,10 @@ __device__ __forceinline__ double norm_factor(const ZS_CONSTANT MatrixItem& m, c
     return by > 0.0 ? ldexp(1.0, m.log2_scale) / by : 0.0;
 }
 
-// A piece of X = U * factor, with its padding.
+// A piece of X = U * factor, with its padding.  A read and a write: 405M elements
+// take 333 us, 4.9 TB/s.  Each block forms the norm again from the slots, 176 of
+// them for 1024 x 2752, behind its loads; a launch of its own would take 4 us.
+// Bands of 8 rows at a time, so that a wave's stores fill whole rows of a panel.
 __global__ __launch_bounds__(kBlock) void ortho_load(NsRef ref, int64_t first, double eps) {
     if (ref.skipped()) return;
     __shared__ double s_sq[kWaves];
@@ -138,20 +154,22 @@ __device__ __forceinline__ void load_lds(const void* base, uint32_t offset, uint
     __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
                      :
                      : "s"(lds), "v"(offset), "s"(base)
-                     : "memory", "m0");
+                     : "memory");
 }
 
 // A wave's share of a T x T tile of a product, WM x WN waves.
 //
 // A stage is 32 inner elements of both operands, 64 bytes a row: 16 rows for
 // each 1 KB that a wave loads at a time, straight into the LDS.  Four stages lie
-// there (five at T 64, whose stages are the shortest); all but the one that is
-// multiplied and the next are on their way, since a load that misses the L2 takes
-// longer than a stage.  (T 256, products of X: 2.70 ms with four stages, 2.69
-// with five, 3.81 with three.  T 64, one matrix of 1024 x 8192: 460 us with four
-// and four blocks a CU, 390 with five and three, 409 with six and two; 42 of 331
-// x 881: 276, 282 and 310.)  One barrier a stage: behind it the next stage has
-// landed for all waves, and the last one's place is free.
+// there; all but the one that is multiplied and the next are on their way, since
+// a load that misses the L2 takes longer than a stage.  (T 256, products of X:
+// 2.70 ms with four stages, 2.69 with five, 3.81 with three.)  One barrier a
+// stage: behind it the next stage has landed for all waves, and the last one's
+// place is free.  At T 64 a stage is four MFMAs a wave, less than its barrier:
+// there one barrier serves two stages, of which six lie in the LDS, and three
+// blocks fit a CU.  (One matrix of 512 x 512, of 1024 x 8192, four of 1024 x
+// 1024: 87, 352 and 208 us; with five stages and a barrier each 92, 384 and 218,
+// with five and a barrier for two 98 and more, with eight and two blocks a CU 89.)
 //
 // Operands in the LDS, as the 16 x 16 x 32 MFMA takes them (lane l: row or
 // column l % 16, inner elements 8 (l / 16) .. + 7):
@@ -169,9 +187,11 @@ struct Product {
     static constexpr int kUM = T / WM / 16, kUN = T / WN / 16;       // 16 x 16 results per wave
     static constexpr int kOperand = T * kPanel * 2;                  // bytes of a stage
     static constexpr int kLoads = kOperand / 1024 / kWaves;          // per wave and operand
-    static constexpr int kStages = T == 64 ? 5 : 4;
+    static constexpr bool kPairs = T == 64;                          // one barrier for two stages
+    static constexpr int kStages = kPairs ? 6 : 4;
     static constexpr int kStage = 2 * kOperand;
-    static constexpr int kMirror = 2 * 16 * (T / WN) * 2;            // of a wave: 32 rows of its mirrored results
+    static constexpr int kMirrorRows = T == 64 ? 16 : 32;            // 16: three blocks fit a CU
+    static constexpr int kMirror = kMirrorRows * (T / WN) * 2;       // of a wave: so many rows of its mirrored results
     static constexpr int kLds = kStages * kStage + kWaves * kMirror;
     static_assert(kLoads >= 1 && kLds <= 160 * 1024, "stages do not fit the LDS");
 
@@ -348,7 +368,7 @@ __global__ __launch_bounds__(64 * WM * WN) void ortho_product(NsRef ref, int64_t
     next = P::kStage;
     int landed = 0;                                // stages of this tile that need no wait
     for (int64_t index = blockIdx.x; tile.item != kNoItem; index += gridDim.x) {
-        // behind the last tile its first stage is read again, into places that nothing reads any more
+        // behind the last tile one of its stages is read again, into places that nothing reads any more
         TileRef following{kNoItem, 0, 0};
         if (index + (int64_t)gridDim.x < n_tiles) following = tile_at(index + gridDim.x);
         if (following.item != kNoItem) {
@@ -361,12 +381,21 @@ __global__ __launch_bounds__(64 * WM * WN) void ortho_product(NsRef ref, int64_t
 #pragma unroll
             for (int y = 0; y < UN; ++y) acc[x][y] = f32x4{};
         for (int k = 0; k < n; k += 2) {
-            if (k >= landed) wait_stage<(S - 3) * NL>();
-            else __asm__ volatile("s_barrier" ::: "memory");
-            multiply(std::integral_constant<int, 0>{});
-            if (k + 1 >= landed) wait_stage<(S - 3) * NL>();
-            else __asm__ volatile("s_barrier" ::: "memory");
-            multiply(std::integral_constant<int, 1>{});
+            if constexpr (P::kPairs) {
+                // this wave's reads of stage k are done too: its place is filled behind this barrier
+                __asm__ volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+                if (k + 1 >= landed) wait_stage<(S - 4) * NL>();
+                else __asm__ volatile("s_barrier" ::: "memory");
+                multiply(std::integral_constant<int, 0>{});
+                multiply(std::integral_constant<int, 1>{});
+            } else {
+                if (k >= landed) wait_stage<(S - 3) * NL>();
+                else __asm__ volatile("s_barrier" ::: "memory");
+                multiply(std::integral_constant<int, 0>{});
+                if (k + 1 >= landed) wait_stage<(S - 3) * NL>();
+                else __asm__ volatile("s_barrier" ::: "memory");
+                multiply(std::integral_constant<int, 1>{});
+            }
         }
         // What is on its way has had a stage's time: with it landed, the stores below
         // are the oldest that a later wait waits for.
@@ -410,9 +439,9 @@ __global__ __launch_bounds__(64 * WM * WN) void ortho_product(NsRef ref, int64_t
             _Float16* out = reinterpret_cast<_Float16*>(ref.ws + (MODE == kGram ? m.a : m.b));
             char* mirror_at = smem + S * P::kStage + wave * P::kMirror;
 #pragma unroll
-            for (int x = 0; x < UM; x += 2) {
+            for (int x = 0; x < UM; x += P::kMirrorRows / 16) {
 #pragma unroll
-                for (int z = 0; z < 2; ++z)
+                for (int z = 0; z < P::kMirrorRows / 16; ++z)
 #pragma unroll
                     for (int y = 0; y < UN; ++y) {
                         const int r = z * 16 + (lane >> 4) * 4, c = y * 16 + (lane & 15);
@@ -432,14 +461,14 @@ __global__ __launch_bounds__(64 * WM * WN) void ortho_product(NsRef ref, int64_t
                         if (ti == tj) continue;
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            *reinterpret_cast<_Float16*>(mirror_at + ((c / kPanel) * 32 + r + e) * 64 + mirror_piece(r, c) + (c & 7) * 2) = h[e];
+                            *reinterpret_cast<_Float16*>(mirror_at + ((c / kPanel) * P::kMirrorRows + r + e) * 64 + mirror_piece(r, c) + (c & 7) * 2) = h[e];
                     }
                 if (ti == tj) continue;
                 __asm__ volatile("s_waitcnt lgkmcnt(0)" ::: "memory");     // a wave reads what it wrote
 #pragma unroll
                 for (int k = 0; k < P::kMirror / 1024; ++k) {
-                    const int piece = k * 64 + lane, r = piece / 4 % 32, c = piece / 128 * kPanel + (piece & 3) * 8;
-                    const h8 h = *reinterpret_cast<const h8*>(mirror_at + ((c / kPanel) * 32 + r) * 64 + mirror_piece(r, c));
+                    const int piece = k * 64 + lane, r = piece / 4 % P::kMirrorRows, c = piece / (4 * P::kMirrorRows) * kPanel + (piece & 3) * 8;
+                    const h8 h = *reinterpret_cast<const h8*>(mirror_at + ((c / kPanel) * P::kMirrorRows + r) * 64 + mirror_piece(r, c));
                     *reinterpret_cast<h8*>(out + panel_at((int64_t)ti * T + wm + x * 16 + r, (int64_t)tj * T + wn + c, sp)) = h;
                 }
                 __asm__ volatile("s_waitcnt lgkmcnt(0)" ::: "memory");     // before the next 32 rows
@@ -457,13 +486,13 @@ __global__ __launch_bounds__(64 * WM * WN) void ortho_product(NsRef ref, int64_t
 // microseconds: per product the larger of one tile's chain of stages and of all
 // tiles over the CUs.  A tile costs c0 besides its stages, and a chain of stages
 // alone in its CU is slower than several (c1 against c1_full).  Measured with
-// tiles of 64, 128 and 256 on 19 lists: one matrix of 512 x 512 takes 92, 141 and
-// 270 us, 64 of 512 x 2048 1278, 1059 and 943, one of 4096 x 4096 2144, 1573 and
-// 1446, 4 of 1024 x 4096 550, 475 and 769; the size that this picks is within 5%
+// tiles of 64, 128 and 256 on 24 lists: one matrix of 512 x 512 takes 87, 142 and
+// 273 us, 64 of 512 x 2048 1292, 1063 and 941, one of 4096 x 4096 2067, 1541 and
+// 1434, 4 of 1024 x 1024 208, 224 and 428; the size that this picks is within 5%
 // of the fastest on all of them.
 double step_cost(const std::vector<OrthoMatrix>& matrices, int tile) {
     const double c0 = tile == 256 ? 12.0 : tile == 128 ? 2.4 : 0.55, first = tile == 256 ? 12.0 : tile == 128 ? 5.0 : 2.3;
-    const double c1 = tile == 256 ? 0.68 : tile == 128 ? 0.23 : 0.19, c1_full = tile == 256 ? 0.68 : tile == 128 ? 0.28 : 0.098;
+    const double c1 = tile == 256 ? 0.68 : tile == 128 ? 0.23 : 0.17, c1_full = tile == 256 ? 0.68 : tile == 128 ? 0.28 : 0.098;
     double cost = 0.0;
     for (int product = 0; product < 3; ++product) {
         double tiles = 0.0, work = 0.0, deepest = 0.0;
