@@ -160,6 +160,25 @@ def test_steps_and_coefficients(Z, n):
         check(o, u, "bf16", coefs=coefs)
 
 
+@pytest.mark.parametrize("n", [7, 12, 32])
+@pytest.mark.parametrize("shape", [(2, 2), (16, 16), (30, 300), (64, 64), (500, 50), (128, 128), (128, 2000), (200, 210)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_many_steps(Z, shape, n):
+    """Nothing that a step leaves grows in the next ones: five of the usual steps,
+    then ones that converge; all of them the usual ones."""
+    after = (1.875, -1.25, 0.375)
+    for k, (kind, ut) in enumerate((("noise", "bf16"), ("spread", "f16"))):
+        u, _ = place(draw(shape, 40 + k, kind, 1.0), ut)
+        for coefs in (M.COEFS[:5] + (after,) * (n - 5), M.COEFS[:1] * n):
+            o = torch.empty(shape, dtype=torch.float16, device="cuda")
+            orthogonalize(Z, Z.MatrixTable([u], [o]), coefs=coefs)
+            if coefs[-1] == after:
+                check(o, u, "f16", coefs=coefs)
+            else:                                            # no limit, but a band: [0.68, 1.21]
+                s = torch.linalg.svdvals(o.cpu().double())
+                assert 0.66 < float(s[-1]) <= float(s[0]) < 1.23, s
+
+
 def test_one_step_that_keeps_x(Z):
     """(1, 0, 0) returns U over its norm: X's rounding and the result's remain."""
     u, _ = place(draw((150, 90), 6), "f32")
