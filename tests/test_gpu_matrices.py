@@ -179,6 +179,19 @@ def test_many_steps(Z, shape, n):
                 assert 0.66 < float(s[-1]) <= float(s[0]) < 1.23, s
 
 
+@pytest.mark.parametrize("n", [5, 7, 12])
+@pytest.mark.parametrize("shape", [(4, 4), (16, 16), (30, 300), (300, 60), (128, 300), (200, 210)], ids=lambda s: "x".join(map(str, s)))
+def test_rank_three(Z, shape, n):
+    """Most singular values are exactly 0: what rounding leaves in their place may
+    not grow beyond what the model of the roundings gives."""
+    rng = np.random.default_rng(7)
+    u, _ = place(rng.integers(-3, 4, (shape[0], 3)) @ rng.integers(-3, 4, (3, shape[1])).astype(float), "bf16")
+    o = torch.empty(shape, dtype=torch.float16, device="cuda")
+    orthogonalize(Z, Z.MatrixTable([u], [o]), coefs=M.COEFS[:1] * n)
+    check(o, u, "f16", coefs=M.COEFS[:1] * n)
+    assert float(torch.linalg.svdvals(o.cpu().double())[0]) < 1.23
+
+
 def test_one_step_that_keeps_x(Z):
     """(1, 0, 0) returns U over its norm: X's rounding and the result's remain."""
     u, _ = place(draw((150, 90), 6), "f32")

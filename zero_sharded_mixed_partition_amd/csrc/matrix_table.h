@@ -55,15 +55,15 @@ struct ThinItem {
     void* out;
     int64_t parts;                      // workspace: partial X X^T, float [n_parts][tiles of the lower triangle][256]
     int64_t exponents;                  // workspace: each part's exponent, int32 [n_parts]
-    int64_t q;                          // workspace: the steps' polynomials, half, sp * sp a step (twice that for sp <= 64)
+    int64_t p;                          // workspace: the polynomial of a run of steps, half, two of [sp][sp]
     int64_t factor;                     // workspace: 1 / max(|U|, eps), double
-    int64_t chunks_per_part;
+    int64_t x;                          // workspace: what a run that is not the last leaves, half, laid out as U
     int32_t n_parts;
     int32_t s, l, sp, n_chunks;
     int32_t udt, odt;
     int32_t tall;
     int32_t log2_scale;
-    int32_t reserved;
+    int32_t chunks_per_part;
 };
 static_assert(sizeof(ThinItem) == sizeof(MatrixItem), "one array holds both");
 

@@ -9,11 +9,15 @@ namespace zero_shard {
 // n_steps steps on the matrices of a pass with a short side of at most kThin
 // (orthogonalize_thin.hip).
 struct NsRef;
-struct ThinSteps {
+struct OrthoSteps {
     float a[ZERO_MAX_ORTHO_STEPS], b[ZERO_MAX_ORTHO_STEPS], c[ZERO_MAX_ORTHO_STEPS];
     int32_t n;
+    uint32_t begins;                             // bit k: a run of thin matrices' steps begins with step k (the first has none)
 };
-int launch_thin(const OrthoPass& pass, const NsRef& ref, const ThinSteps& steps, double eps, hipStream_t stream);
+constexpr double kMostPoly = 32.0;               // of a step's polynomials, on the singular values that reach it
+constexpr double kMostRun = 1024.0;              // of the product of a run's
+constexpr double kMostCarried = 256.0;           // ... without its last
+int launch_thin(const OrthoPass& pass, const NsRef& ref, const OrthoSteps& steps, double eps, hipStream_t stream);
 // The passes, work lists and workspace of those matrices, appended to plan.
 int plan_thin(const std::vector<OrthoMatrix>& matrices, OrthoPlan* plan);
 

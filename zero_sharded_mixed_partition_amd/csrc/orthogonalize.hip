@@ -601,24 +601,36 @@ int launch_product(const OrthoPass& p, const NsRef& ref, const NsStep& step, hip
 // The singular values start in [0, 1].  What each step makes of the largest
 // interval they can be in has to stay within what fp16 holds of X, A and B at
 // their scales, with room for single entries.
-int check_coefs(const double* coefs, int32_t n_steps) {
+int check_coefs(const double* coefs, int32_t n_steps, OrthoSteps* steps) {
     if (coefs == nullptr) return fail(ZERO_EINVAL, "coefs is NULL");
     if (n_steps < 1 || n_steps > ZERO_MAX_ORTHO_STEPS)
         return fail(ZERO_EINVAL, "n_steps must lie in [1, %d] (got %d)", ZERO_MAX_ORTHO_STEPS, n_steps);
-    double top = 1.0;
+    double top = 1.0, run = 1.0;
+    *steps = OrthoSteps{};
+    steps->n = n_steps;
     for (int k = 0; k < n_steps; ++k) {
         const double a = coefs[3 * k], b = coefs[3 * k + 1], c = coefs[3 * k + 2];
         if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c)) return fail(ZERO_EINVAL, "coefs must be finite");
-        double next = 0.0, poly = 0.0;
+        double next = 0.0, poly = 0.0, factor = 0.0;
         for (int i = 0; i <= 4096; ++i) {
             const double x = top * i / 4096, y = x * x;
-            poly = std::max({poly, std::fabs(y * (b + c * y)), std::fabs(a + y * (b + c * y))});
+            poly = std::max(poly, std::fabs(y * (b + c * y)));
+            factor = std::max(factor, std::fabs(a + y * (b + c * y)));
             next = std::max(next, std::fabs(x * (a + y * (b + c * y))));
         }
-        if (poly > 32.0 || next > 4.0)
+        poly = std::max(poly, factor);
+        if (poly > kMostPoly || next > 4.0)
             return fail(ZERO_ERANGE, "step %d takes singular values of [0, 1] to %g (at most 4), its polynomial to %g (at most 32)",
                         k, next, poly);
         top = next;
+        if (run > kMostCarried || run * factor > kMostRun) {
+            steps->begins |= 1u << k;
+            run = 1.0;
+        }
+        run *= factor;
+        steps->a[k] = (float)a;
+        steps->b[k] = (float)b;
+        steps->c[k] = (float)c;
     }
     return ZERO_OK;
 }
@@ -708,7 +720,8 @@ int zero_multi_orthogonalize(const void* table, const void* d_table, const doubl
     clear_error();
     MatrixHeader h;
     int rc = read_matrix_table(table, d_table, kCanOrtho, "the orthogonalisation (update, ortho)", &h);
-    if (rc == ZERO_OK) rc = check_coefs(coefs, n_steps);
+    OrthoSteps steps;
+    if (rc == ZERO_OK) rc = check_coefs(coefs, n_steps, &steps);
     if (rc != ZERO_OK) return rc;
     if (!(eps >= 0.0) || !std::isfinite(eps)) return fail(ZERO_EINVAL, "eps must be finite and >= 0");
     // below the least norm that is not zero eps decides nothing, and 1 / eps might not be finite
@@ -729,13 +742,6 @@ int zero_multi_orthogonalize(const void* table, const void* d_table, const doubl
     const NsRef ref{at<MatrixItem>(d_table, h.items_at), at<TileRef>(d_table, h.tiles_at), static_cast<char*>(d_workspace),
                     d_global_overflow};
     const OrthoPass* passes = at<OrthoPass>(table, h.passes_at);
-    ThinSteps steps{};
-    steps.n = n_steps;
-    for (int k = 0; k < n_steps; ++k) {
-        steps.a[k] = (float)coefs[3 * k];
-        steps.b[k] = (float)coefs[3 * k + 1];
-        steps.c[k] = (float)coefs[3 * k + 2];
-    }
     for (int p = 0; p < h.n_passes; ++p) {
         const OrthoPass& pass = passes[p];
         if (pass.tile <= 0) {

@@ -31,6 +31,13 @@
 namespace zero_shard {
 namespace {
 
+// The steps of one run.
+struct ThinSteps {
+    float a[ZERO_MAX_ORTHO_STEPS], b[ZERO_MAX_ORTHO_STEPS], c[ZERO_MAX_ORTHO_STEPS];
+    int32_t n;
+};
+
+constexpr int kLog2P = 4;                        // a run's polynomial is held times 2^4: at most 2^14
 
 template <int SP>
 struct Thin {
@@ -39,8 +46,10 @@ struct Thin {
     static constexpr int kLC = kChunkElements / SP;           // columns of a chunk
     static constexpr int kWaves2 = SP == 128 ? 12 : SP == 64 ? 5 : 3;   // of the second kernel: tiles divide evenly
     static constexpr int kOwn = kTiles / kWaves2;
-    static constexpr bool kTwo = SP <= 64;                    // X and B as two fp16 in their product
-    static constexpr int kB = SP * SP * (kTwo ? 2 : 1);       // halves of a step's B
+    static constexpr int kP = 2 * SP * SP;                    // halves of a run's polynomial
+    // in the second kernel's LDS a place of its own for it, or A's
+    static constexpr bool kOwnP = SP <= 64;
+    static constexpr int kSquares = kOwnP ? 3 : 2;
     static constexpr int kStageLd = kLC + 4;                  // floats a row: four rows apart meet other banks
 };
 
@@ -51,9 +60,18 @@ __device__ __forceinline__ int pair_index(int i, int j) { return i * (i + 1) / 2
 template <int SP>
 using ChunkVector = Vector8<SP, SP>;
 
+// Of U, or of what a run of steps has left in the workspace.
+struct ThinSource {
+    const void* at;
+    int dt;
+
+    __device__ __forceinline__ ThinSource(const NsRef& ref, const ZS_CONSTANT ThinItem& m, bool again)
+        : at(again ? ref.ws + m.x : static_cast<const char*>(m.in)), dt(again ? (int)ZERO_F16 : m.udt) {}
+};
+
 template <int SP>
-__device__ __forceinline__ void load_chunk(const ZS_CONSTANT ThinItem& m, int64_t first, float x[8][8]) {
-    load_box<SP, SP>(m.udt, m.in, m.s, m.l, m.tall, 0, first, x);
+__device__ __forceinline__ void load_chunk(const ZS_CONSTANT ThinItem& m, const ThinSource& from, int64_t first, float x[8][8]) {
+    load_box<SP, SP>(from.dt, from.at, m.s, m.l, m.tall, 0, first, x);
 }
 
 // ---------------------------------------------------------------- first kernel: parts of U U^T
@@ -131,7 +149,7 @@ __device__ __forceinline__ void chunk_products(f32x4* acc, uint32_t hi, uint32_t
 
 // One part of an item: chunks_per_part chunks, summed in order.
 template <int SP>
-__global__ __launch_bounds__(kThreads, 2) void thin_gram(NsRef ref, int64_t first) {
+__global__ __launch_bounds__(kThreads, 2) void thin_gram(NsRef ref, int64_t first, bool again) {
     using H = Thin<SP>;
     if (ref.skipped()) return;
     __shared__ __attribute__((aligned(1024))) char smem[2 * kChunkElements * 2];
@@ -140,17 +158,19 @@ __global__ __launch_bounds__(kThreads, 2) void thin_gram(NsRef ref, int64_t firs
     const ZS_CONSTANT ThinItem& m = ((const ZS_CONSTANT ThinItem*)ref.items)[t.item];
     const int part = t.i, lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t hi = lds_address(smem), lo = hi + kChunkElements * 2;
-    const bool two = m.udt == ZERO_F32, tall = m.tall != 0;
+    const ThinSource from(ref, m, again);
+    const bool two = from.dt == ZERO_F32, tall = m.tall != 0;
     constexpr int kOwn = SP == 128 ? 12 : H::kTiles;
     f32x4 acc[kOwn];
 #pragma unroll
     for (int k = 0; k < kOwn; ++k) acc[k] = f32x4{};
     int run = INT_MIN / 4;                       // exponent that the sums are scaled by
     bool bad = false;
-    const int64_t c_end = (part + 1) * m.chunks_per_part < m.n_chunks ? (part + 1) * m.chunks_per_part : m.n_chunks;
+    const int64_t c_first = (int64_t)part * m.chunks_per_part;
+    const int64_t c_end = c_first + m.chunks_per_part < m.n_chunks ? c_first + m.chunks_per_part : m.n_chunks;
     float x[8][8];
-    load_chunk<SP>(m, part * m.chunks_per_part * H::kLC, x);
-    for (int64_t chunk = part * m.chunks_per_part; chunk < c_end; ++chunk) {
+    load_chunk<SP>(m, from, c_first * H::kLC, x);
+    for (int64_t chunk = c_first; chunk < c_end; ++chunk) {
         uint32_t top = 0;
 #pragma unroll
         for (int n = 0; n < 8; ++n)
@@ -196,7 +216,7 @@ __global__ __launch_bounds__(kThreads, 2) void thin_gram(NsRef ref, int64_t firs
             *reinterpret_cast<h8*>(smem + at) = h;
             if (two) *reinterpret_cast<h8*>(smem + kChunkElements * 2 + at) = g;
         }
-        if (chunk + 1 < c_end) load_chunk<SP>(m, (chunk + 1) * H::kLC, x);      // on its way during the products
+        if (chunk + 1 < c_end) load_chunk<SP>(m, from, (chunk + 1) * H::kLC, x);      // on its way during the products
         __syncthreads();
         if (two) chunk_products<SP, true>(acc, hi, lo, tall, wave, lane);
         else chunk_products<SP, false>(acc, hi, lo, tall, wave, lane);
@@ -285,42 +305,42 @@ __device__ __forceinline__ f32x4 square_product(uint32_t a, uint32_t b, int i, i
     return sum;
 }
 
-// A tile of B for the third kernel, where it is added to a I and needs no scale,
-// as its fragments: [i][k / 32][lane][8] halves with the inner elements of a lane in the order 4 g .. + 3 of two tiles of 16.
+// A tile of a run's polynomial for the third kernel, as its fragments:
+// [i][k / 32][lane][8] halves with the inner elements of a lane in the order
+// 4 g .. + 3 of two tiles of 16.
 template <int SP>
 __device__ __forceinline__ void put_fragments(_Float16* to, int i, int j, int lane, const f32x4& v) {
     const int g = lane >> 4, c = lane & 15;
     h4 h, l;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        const float x = v[e] * (1.0f / (1 << kLog2A));
-        h[e] = (_Float16)x;
-        l[e] = (_Float16)(x - (float)h[e]);
+        h[e] = (_Float16)v[e];
+        l[e] = (_Float16)(v[e] - (float)h[e]);
     }
     _Float16* at = to + (((j * (SP / 32) + i / 2) * 64 + g * 16 + c) * 8 + (i & 1) * 4);
     if (i != j) {
         *reinterpret_cast<h4*>(at) = h;
-        if (Thin<SP>::kTwo) *reinterpret_cast<h4*>(at + SP * SP) = l;
+        *reinterpret_cast<h4*>(at + SP * SP) = l;
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         if (i == j && 4 * g + e < c) continue;
         _Float16* mirror = to + (((i * (SP / 32) + j / 2) * 64 + (c >> 2) * 16 + 4 * g + e) * 8 + (j & 1) * 4 + (c & 3));
         mirror[0] = h[e];
-        if (Thin<SP>::kTwo) mirror[SP * SP] = l[e];
+        mirror[SP * SP] = l[e];
         if (i == j) {
             at[e] = h[e];
-            if (Thin<SP>::kTwo) at[SP * SP + e] = l[e];
+            at[SP * SP + e] = l[e];
         }
     }
 }
 
 template <int SP>
-__global__ __launch_bounds__(64 * Thin<SP>::kWaves2) void thin_steps(NsRef ref, int64_t first_item, ThinSteps steps, double eps) {
+__global__ __launch_bounds__(64 * Thin<SP>::kWaves2) void thin_steps(NsRef ref, int64_t first_item, ThinSteps steps, double eps, bool again) {
     using H = Thin<SP>;
     constexpr int kOwn = H::kOwn;
     if (ref.skipped()) return;
-    __shared__ __attribute__((aligned(1024))) char smem[4 * SP * SP * 2];     // A and B, two fp16 each
+    __shared__ __attribute__((aligned(1024))) char smem[H::kSquares * 2 * SP * SP * 2];     // A, B and P, two fp16 each
     __shared__ double s_diag[SP];
     const ZS_CONSTANT ThinItem& m = ((const ZS_CONSTANT ThinItem*)ref.items)[first_item + blockIdx.x];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -362,7 +382,8 @@ __global__ __launch_bounds__(64 * Thin<SP>::kWaves2) void thin_steps(NsRef ref, 
     for (int off = (SP < 64 ? SP : 64) / 2; off > 0; off >>= 1) trace += __shfl_xor(trace, off, 64);
     const int up = top < INT_MIN / 8 || bad ? 0 : top;
     const double norm = ldexp(sqrt(trace), up);
-    const double by = norm > eps ? norm : eps;
+    // what a run has left is X times a power of two
+    const double by = again ? ldexp(1.0, m.log2_scale) : norm > eps ? norm : eps;
     const double factor = bad ? NAN : by > 0.0 ? 1.0 / by : 0.0;
     if (threadIdx.x == 0) *reinterpret_cast<double*>(ref.ws + m.factor) = factor;
     const double unit = by > 0.0 ? ldexp(1.0, up) / by : 0.0;
@@ -374,49 +395,70 @@ __global__ __launch_bounds__(64 * Thin<SP>::kWaves2) void thin_steps(NsRef ref, 
         put_square<SP>(smem, ti[k], tj[k], lane, A[k]);
     }
     __syncthreads();
-    const uint32_t a = lds_address(smem), b = a + 2 * SP * SP * 2;
-    char* const b_at = smem + 2 * SP * SP * 2;
+    const uint32_t a = lds_address(smem), b = a + 2 * SP * SP * 2, p = H::kOwnP ? b + 2 * SP * SP * 2 : a;
+    char* const b_at = smem + (b - a);
+    char* const p_at = smem + (p - a);
     constexpr float kDown = 1.0f / (1 << kLog2A);
+    f32x4 P[kOwn];
     for (int step = 0; step < steps.n; ++step) {
-        _Float16* q = reinterpret_cast<_Float16*>(ref.ws + m.q) + (int64_t)step * H::kB;
+        const bool last = step + 1 == steps.n;
+        const float sa = steps.a[step];
 #pragma unroll
         for (int k = 0; k < kOwn; ++k) {
             const f32x4 square = square_product<SP>(a, a, ti[k], tj[k], lane);
             f32x4 B;
 #pragma unroll
             for (int e = 0; e < 4; ++e) B[e] = fmaf(steps.b[step], A[k][e], steps.c[step] * (square[e] * kDown));
-            put_fragments<SP>(q, ti[k], tj[k], lane, B);
-            put_square<SP>(b_at, ti[k], tj[k], lane, B);
-        }
-        if (step + 1 == steps.n) break;
-        // twice A <- a A + B A
+            if (step > 0 || !last) put_square<SP>(b_at, ti[k], tj[k], lane, B);
+            if (step == 0) {
 #pragma unroll
-        for (int twice = 0; twice < 2; ++twice) {
-            __syncthreads();
-            f32x4 next[kOwn];
-#pragma unroll
-            for (int k = 0; k < kOwn; ++k) {
-                const f32x4 v = square_product<SP>(b, a, ti[k], tj[k], lane);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) next[k][e] = fmaf(steps.a[step], A[k][e], v[e] * kDown);
-            }
-            __syncthreads();
-#pragma unroll
-            for (int k = 0; k < kOwn; ++k) {
-                A[k] = next[k];
-                put_square<SP>(smem, ti[k], tj[k], lane, A[k]);
+                for (int e = 0; e < 4; ++e)
+                    P[k][e] = (float)(1 << kLog2P) * (B[e] * kDown + (ti[k] == tj[k] && 4 * (lane >> 4) + e == (lane & 15) ? sa : 0.0f));
+            } else if (H::kOwnP) {
+                put_square<SP>(p_at, ti[k], tj[k], lane, P[k]);
             }
         }
+        const auto times_b = [&](f32x4* v, uint32_t by) {         // v <- a v + B v, of which `by` is the LDS's copy
+#pragma unroll
+            for (int k = 0; k < kOwn; ++k) {
+                const f32x4 w = square_product<SP>(b, by, ti[k], tj[k], lane);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[k][e] = fmaf(sa, v[k][e], w[e] * kDown);
+            }
+        };
+        const auto put = [&](char* to, const f32x4* v) {
+#pragma unroll
+            for (int k = 0; k < kOwn; ++k) put_square<SP>(to, ti[k], tj[k], lane, v[k]);
+        };
+        __syncthreads();
+        if (!last) times_b(A, a);
+        if (step > 0) {
+            if (!H::kOwnP) {
+                __syncthreads();
+                put(p_at, P);
+                __syncthreads();
+            }
+            times_b(P, p);
+        }
+        if (last) break;
+        __syncthreads();
+        put(smem, A);
+        __syncthreads();
+        times_b(A, a);
+        __syncthreads();
+        put(smem, A);
         __syncthreads();
     }
+#pragma unroll
+    for (int k = 0; k < kOwn; ++k) put_fragments<SP>(reinterpret_cast<_Float16*>(ref.ws + m.p), ti[k], tj[k], lane, P[k]);
 }
 
 // ---------------------------------------------------------------- third kernel: X through all steps
 
 template <int SP, int ODT>
-__device__ __forceinline__ void store_chunk(const ZS_CONSTANT ThinItem& m, int64_t first, const float* stage, float back) {
+__device__ __forceinline__ void store_chunk(const ZS_CONSTANT ThinItem& m, void* to, int64_t first, const float* stage, float back) {
     using H = Thin<SP>;
-    uint16_t* out = static_cast<uint16_t*>(m.out);
+    uint16_t* out = static_cast<uint16_t*>(to);
 #pragma unroll
     for (int n = 0; n < 8; ++n) {
         const ChunkVector<SP> v(m.s, m.l, m.tall, 0, first, n);
@@ -442,12 +484,12 @@ __device__ __forceinline__ void store_chunk(const ZS_CONSTANT ThinItem& m, int64
 // .. + 3 of a column, which is how the next product takes it: with the inner
 // elements in the order of put_fragments nothing moves between lanes.
 template <int SP>
-__global__ __launch_bounds__(kThreads, 2) void thin_apply(NsRef ref, int64_t first, ThinSteps steps) {
+__global__ __launch_bounds__(kThreads, 2) void thin_apply(NsRef ref, int64_t first, bool again, bool last) {
     using H = Thin<SP>;
-    constexpr int R = H::kR, kStrips = H::kLC / 64, kB = H::kB, kLoads = kB / 8 / kThreads;
+    constexpr int R = H::kR, kStrips = H::kLC / 64, kP = H::kP, kLoads = kP / 8 / kThreads;
     if (ref.skipped()) return;
     __shared__ __attribute__((aligned(1024))) char smem[SP * H::kStageLd * 4];
-    static_assert(kB * 4 <= SP * H::kStageLd * 4 && kLoads * 8 * kThreads == kB, "two steps' B take the stage's place");
+    static_assert(kP * 2 <= SP * H::kStageLd * 4 && kLoads * 8 * kThreads == kP, "a polynomial takes the stage's place");
     const ZS_CONSTANT TileRef& t = ref.tile(first + blockIdx.x);
     const ZS_CONSTANT ThinItem& m = ((const ZS_CONSTANT ThinItem*)ref.items)[t.item];
     const int64_t column = (int64_t)t.i * H::kLC;
@@ -455,7 +497,7 @@ __global__ __launch_bounds__(kThreads, 2) void thin_apply(NsRef ref, int64_t fir
     float* stage = reinterpret_cast<float*>(smem);
     {
         float x[8][8];
-        load_chunk<SP>(m, column, x);
+        load_chunk<SP>(m, ThinSource(ref, m, again), column, x);
         // x * factor as x * 2^e * f, f in [0.5, 1): neither the factor nor a product leaves float32
         int e;
         const float f = (float)frexp(*reinterpret_cast<const double*>(ref.ws + m.factor), &e);
@@ -475,7 +517,7 @@ __global__ __launch_bounds__(kThreads, 2) void thin_apply(NsRef ref, int64_t fir
             }
         }
     }
-    const u32x4* q = reinterpret_cast<const u32x4*>(ref.ws + m.q);
+    const u32x4* q = reinterpret_cast<const u32x4*>(ref.ws + m.p);
     u32x4 ahead[kLoads];
 #pragma unroll
     for (int k = 0; k < kLoads; ++k) ahead[k] = q[k * kThreads + threadIdx.x];
@@ -488,55 +530,41 @@ __global__ __launch_bounds__(kThreads, 2) void thin_apply(NsRef ref, int64_t fir
         for (int i = 0; i < R; ++i)
 #pragma unroll
             for (int e = 0; e < 4; ++e) X[y][i][e] = stage[(i * 16 + row + e) * H::kStageLd + own + y * 16];
+    const uint32_t p = lds_address(smem) + lane * 16;
     __syncthreads();                                          // the stage has been read
-    for (int step = 0; step < steps.n; ++step) {
-        // in turn in two places: where this one goes was last read before the last barrier
-        char* const place = smem + (step & 1) * kB * 2;
 #pragma unroll
-        for (int k = 0; k < kLoads; ++k) reinterpret_cast<u32x4*>(place)[k * kThreads + threadIdx.x] = ahead[k];
-        if (step + 1 < steps.n) {
-            q += kB / 8;
+    for (int k = 0; k < kLoads; ++k) reinterpret_cast<u32x4*>(smem)[k * kThreads + threadIdx.x] = ahead[k];
+    __syncthreads();
+    h8 xh[kStrips][R / 2], xl[kStrips][R / 2];
 #pragma unroll
-            for (int k = 0; k < kLoads; ++k) ahead[k] = q[k * kThreads + threadIdx.x];
+    for (int y = 0; y < kStrips; ++y)
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const _Float16 h = (_Float16)X[y][i][e];
+                xh[y][i / 2][(i & 1) * 4 + e] = h;
+                xl[y][i / 2][(i & 1) * 4 + e] = (_Float16)(X[y][i][e] - (float)h);
+            }
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        f32x4 sum[kStrips];
+#pragma unroll
+        for (int y = 0; y < kStrips; ++y) sum[y] = f32x4{};
+#pragma unroll
+        for (int k = 0; k < R / 2; ++k) {
+            const h8 ph = lds_h8(p + (i * (SP / 32) + k) * 1024), pl = lds_h8(p + SP * SP * 2 + (i * (SP / 32) + k) * 1024);
+#pragma unroll
+            for (int y = 0; y < kStrips; ++y) {
+                sum[y] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ph, xh[y][k], sum[y], 0, 0, 0);
+                sum[y] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ph, xl[y][k], sum[y], 0, 0, 0);
+                sum[y] = __builtin_amdgcn_mfma_f32_16x16x32_f16(pl, xh[y][k], sum[y], 0, 0, 0);
+            }
         }
-        __syncthreads();
-        h8 xh[kStrips][R / 2], xl[kStrips][R / 2];
 #pragma unroll
         for (int y = 0; y < kStrips; ++y)
 #pragma unroll
-            for (int i = 0; i < R; ++i)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const _Float16 h = (_Float16)X[y][i][e];
-                    xh[y][i / 2][(i & 1) * 4 + e] = h;
-                    if (H::kTwo) xl[y][i / 2][(i & 1) * 4 + e] = (_Float16)(X[y][i][e] - (float)h);
-                }
-        const float a = steps.a[step];
-        const uint32_t b = lds_address(place) + lane * 16;
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-            f32x4 sum[kStrips];
-#pragma unroll
-            for (int y = 0; y < kStrips; ++y)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) sum[y][e] = a * X[y][i][e];
-#pragma unroll
-            for (int k = 0; k < R / 2; ++k) {
-                const h8 bh = lds_h8(b + (i * (SP / 32) + k) * 1024);
-#pragma unroll
-                for (int y = 0; y < kStrips; ++y) sum[y] = __builtin_amdgcn_mfma_f32_16x16x32_f16(bh, xh[y][k], sum[y], 0, 0, 0);
-                if (H::kTwo) {
-                    const h8 bl = lds_h8(b + SP * SP * 2 + (i * (SP / 32) + k) * 1024);
-#pragma unroll
-                    for (int y = 0; y < kStrips; ++y) {
-                        sum[y] = __builtin_amdgcn_mfma_f32_16x16x32_f16(bh, xl[y][k], sum[y], 0, 0, 0);
-                        sum[y] = __builtin_amdgcn_mfma_f32_16x16x32_f16(bl, xh[y][k], sum[y], 0, 0, 0);
-                    }
-                }
-            }
-#pragma unroll
-            for (int y = 0; y < kStrips; ++y) X[y][i] = sum[y];
-        }
+            for (int e = 0; e < 4; ++e) X[y][i][e] = sum[y][e] * (1.0f / (1 << kLog2P));
     }
     __syncthreads();
 #pragma unroll
@@ -546,39 +574,55 @@ __global__ __launch_bounds__(kThreads, 2) void thin_apply(NsRef ref, int64_t fir
 #pragma unroll
             for (int e = 0; e < 4; ++e) stage[(i * 16 + row + e) * H::kStageLd + own + y * 16] = X[y][i][e];
     __syncthreads();
-    const float back = ldexpf(1.0f, -m.log2_scale);
-    if (m.odt == ZERO_F16) store_chunk<SP, ZERO_F16>(m, column, stage, back);
-    else store_chunk<SP, ZERO_BF16>(m, column, stage, back);
+    const float back = last ? ldexpf(1.0f, -m.log2_scale) : 1.0f;
+    if (!last) store_chunk<SP, ZERO_F16>(m, ref.ws + m.x, column, stage, back);
+    else if (m.odt == ZERO_F16) store_chunk<SP, ZERO_F16>(m, m.out, column, stage, back);
+    else store_chunk<SP, ZERO_BF16>(m, m.out, column, stage, back);
 }
 
 // ---------------------------------------------------------------- host side
 
 int padded(int64_t s) { return s <= 32 ? 32 : s <= 64 ? 64 : 128; }
 
+// One run of steps; again: not the first, last: the last.
 template <int SP>
-int launch_thin_sp(const OrthoPass& p, const NsRef& ref, const ThinSteps& steps, double eps, hipStream_t s) {
-    hipLaunchKernelGGL(thin_gram<SP>, dim3((unsigned)p.n_sym), dim3(kThreads), 0, s, ref, p.sym_first);
+int launch_run(const OrthoPass& p, const NsRef& ref, const ThinSteps& steps, double eps, bool again, bool last, hipStream_t s) {
+    hipLaunchKernelGGL(thin_gram<SP>, dim3((unsigned)p.n_sym), dim3(kThreads), 0, s, ref, p.sym_first, again);
     int rc = launch_status("thin_gram");
     if (rc != ZERO_OK) return rc;
-    hipLaunchKernelGGL(thin_steps<SP>, dim3((unsigned)p.n_items), dim3(64 * Thin<SP>::kWaves2), 0, s, ref, p.first_item, steps, eps);
+    hipLaunchKernelGGL(thin_steps<SP>, dim3((unsigned)p.n_items), dim3(64 * Thin<SP>::kWaves2), 0, s, ref, p.first_item, steps, eps, again);
     rc = launch_status("thin_steps");
     if (rc != ZERO_OK) return rc;
-    hipLaunchKernelGGL(thin_apply<SP>, dim3((unsigned)p.n_x), dim3(kThreads), 0, s, ref, p.x_first, steps);
+    hipLaunchKernelGGL(thin_apply<SP>, dim3((unsigned)p.n_x), dim3(kThreads), 0, s, ref, p.x_first, again, last);
     return launch_status("thin_apply");
 }
 
 }  // namespace
 
-int launch_thin(const OrthoPass& pass, const NsRef& ref, const ThinSteps& steps, double eps, hipStream_t stream) {
-    if (pass.tile == -128) return launch_thin_sp<128>(pass, ref, steps, eps, stream);
-    if (pass.tile == -64) return launch_thin_sp<64>(pass, ref, steps, eps, stream);
-    return launch_thin_sp<32>(pass, ref, steps, eps, stream);
+int launch_thin(const OrthoPass& pass, const NsRef& ref, const OrthoSteps& steps, double eps, hipStream_t stream) {
+    int rc = ZERO_OK;
+    for (int k = 0; k < steps.n && rc == ZERO_OK;) {
+        ThinSteps run{};
+        const int begin = k;
+        do {
+            run.a[run.n] = steps.a[k];
+            run.b[run.n] = steps.b[k];
+            run.c[run.n] = steps.c[k];
+            ++run.n;
+            ++k;
+        } while (k < steps.n && !(steps.begins >> k & 1));
+        const bool again = begin > 0, last = k == steps.n;
+        rc = pass.tile == -128  ? launch_run<128>(pass, ref, run, eps, again, last, stream)
+             : pass.tile == -64 ? launch_run<64>(pass, ref, run, eps, again, last, stream)
+                                : launch_run<32>(pass, ref, run, eps, again, last, stream);
+    }
+    return rc;
 }
 
 int plan_thin(const std::vector<OrthoMatrix>& matrices, OrthoPlan* plan) {
     for (const int sp : {128, 64, 32}) {
         const int tiles = sp / 16 * (sp / 16 + 1) / 2;
-        const int64_t b_bytes = 2 * (sp == 128 ? Thin<128>::kB : sp == 64 ? Thin<64>::kB : Thin<32>::kB);
+        const int64_t p_bytes = 2 * 2 * sp * sp;
         OrthoPass pass{};
         int64_t at = 0;
         size_t first = plan->items.size();
@@ -619,15 +663,17 @@ int plan_thin(const std::vector<OrthoMatrix>& matrices, OrthoPlan* plan) {
             // at least sp / 32 chunks a part, and no more than 2 MB of parts: one
             // workgroup sums them
             const int64_t most = (int64_t(2) << 20) / (tiles * 1024);
-            it.chunks_per_part = std::max<int64_t>(sp / 32, (it.n_chunks + most - 1) / most);
+            it.chunks_per_part = (int32_t)std::max<int64_t>(sp / 32, (it.n_chunks + most - 1) / most);
             it.n_parts = (int32_t)((it.n_chunks + it.chunks_per_part - 1) / it.chunks_per_part);
+            const int64_t x_bytes = s * l * 2;
             const int64_t need = pad_to((int64_t)it.n_parts * tiles * 1024, 256) + pad_to((int64_t)it.n_parts * 4, 256) +
-                                 ZERO_MAX_ORTHO_STEPS * b_bytes + 256;
-            if (at + need > kPassBytes || plan->items.size() - first >= 1 << 20) finish();
+                                 p_bytes + 256 + pad_to(x_bytes, 256);
+            if ((at > 0 && at + need > kPassBytes) || plan->items.size() - first >= 1 << 20) finish();
             it.parts = place(&at, (int64_t)it.n_parts * tiles * 1024);
             it.exponents = place(&at, (int64_t)it.n_parts * 4);
-            it.q = place(&at, ZERO_MAX_ORTHO_STEPS * b_bytes);
+            it.p = place(&at, p_bytes);
             it.factor = place(&at, sizeof(double));
+            it.x = place(&at, x_bytes);
             MatrixItem slot;
             std::memcpy(&slot, &it, sizeof(it));
             plan->items.push_back(slot);
