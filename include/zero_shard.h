@@ -773,20 +773,22 @@ int zero_multi_adam_step_coef(const void* table, const void* d_table, const void
  *   more rows than columns X X^T ... X is formed as X ... X^T X, which is equal.)
  *   eps = 0 leaves a zero matrix zero.  A matrix that holds an inf or a NaN
  *   becomes NaN.  Where the short side exceeds 128, X, X X^T and the polynomial
- *   are rounded to fp16 between products; up to 128, X stays in float32, X X^T is
- *   carried on through the steps with 22 bits, and the polynomial has 11 bits (22
- *   up to 64).  Sums are float32.  Besides its own rounding the result of five steps
- *   of (3.4445, -4.7750, 2.0315) is off (relative, Frobenius) by about 1e-4 with a
- *   short side up to 64 and 1.2e-3 above it for random matrices, by up to 1e-3 and
- *   1.7e-3 where a strong low-rank part is added (2.5e-3 seen), and by 4e-3 for
- *   1024 singular values that fall as 1, 1/2, 1/3, ...
+ *   are rounded to fp16 between products.  Up to 128 they have 22 bits, and X is
+ *   rounded to fp16 only between runs of steps: a run ends where the product of
+ *   the largest |a + b x + c x^2| could exceed 1024 (256 before its last step);
+ *   five steps of (3.4445, -4.7750, 2.0315) are one.  Sums are float32.  Besides
+ *   its own rounding the result of these five is off (relative, Frobenius) by 1e-6
+ *   to 1e-4 with a short side up to 128; above it by about 1.2e-3 for random
+ *   matrices, 1.7e-3 where a strong low-rank part is added, and 4e-3 for 1024
+ *   singular values that fall as 1, 1/2, 1/3, ...  A singular value that rounding
+ *   puts in the place of a zero grows by a each step, as any other.
  *   Coefficients have to keep singular values of [0, 1] within 4, and
  *   |b x + c x^2| and |a + b x + c x^2| of their squares x within 32
  *   (ZERO_ERANGE).  1 <= n_steps <= ZERO_MAX_ORTHO_STEPS.
  *   Workspace: zero_multi_orthogonalize_workspace_bytes(table) bytes, 256-byte
  *   aligned, clobbered.  A matrix takes about 4 bytes an element and 4 for each of
- *   its short side's square; with a short side of at most 32, 64 or 128, 0.13, 0.5
- *   or 1 MB and its parts, at most 2 MB.  A list that would take more than 4 GiB
+ *   its short side's square; with a short side of at most 128, 2 bytes an element
+ *   and at most 2 MB.  A list that would take more than 4 GiB
  *   is worked off in parts.  Calls, and graphs recorded with them, that may run at
  *   the same time need a workspace each.
  * zero_multi_muon_update (master, ortho; param_out): per element, in float32,

@@ -2,23 +2,34 @@
 // adapters, single heads, small layers.
 //
 // Every step multiplies X from the left by a polynomial of A = X X^T, and A of
-// the next step follows from A alone: with Q = a I + B, B = b A + c A A (all of
+// the next step follows from A alone: with B = b A + c A A and Q = a I + B (all of
 // them symmetric, and functions of the first A, so they commute)
-//     X' = Q X,   A' = X' X'^T = Q A Q.
-// So U is read once for its A, which is s x s, all steps' B are formed from that
-// by one workgroup, and U is read again, multiplied by the steps' Q in turn
-// while it stays in registers, and stored.  Three launches, whatever the number
-// of steps, and 6 to 8 bytes an element; the tiled products take 17 launches and
-// 50 bytes.
+//     X' = Q X,   A' = X' X'^T = Q Q A.
+// So U is read once for its A, which is s x s; one workgroup per matrix carries A
+// and P, the product of the steps' Q, through the steps; and U is read again,
+// multiplied by P, and stored.  Three launches whatever the number of steps and 6
+// to 8 bytes an element; the tiled products take 17 launches and 50 bytes, and
+// multiply X five times as often.
+//
+// A run of steps ends where P could exceed 2^10, or Q Q .. of all but its last
+// step 2^16: what rounding leaves of A's zero singular values, 1e-7 of the
+// largest, positive or negative, would grow into something.  The next run starts
+// from X, in fp16.  Five steps of (3.4445, -4.7750, 2.0315) are one run.
 //
 // What is rounded.  A small singular value's square is far below A's largest
-// entries, and the steps multiply it by up to 11.8 each: A, Q A and B are held
-// as two fp16 each (22 bits, times 2^10), their products as three MFMAs of the
-// four (the lower halves' own is below 2^-22), sums in float32.  U enters A with
-// 11 bits or what it has of them, float32 as two fp16.  X stays in float32; in B
-// X both factors are two fp16 for s <= 64, and one for larger s, which costs the
-// result 1e-3 and saves two thirds of the products.  fp16's range: each chunk
-// of U is scaled by a power of two of its own, which follows it to the sum.
+// entries, and the steps multiply it by up to 11.8 each: A, Q A, B and P are held
+// as two fp16 each (22 bits, times 2^10, P 2^4), and so is X where it is
+// multiplied; products are three MFMAs of the four (the lower halves' own is
+// below 2^-22), sums float32.  U enters A with 11 bits or what it has of them,
+// float32 as two fp16.  fp16's range: each chunk of U is scaled by a power of two
+// of its own, which follows it to the sum.  A run's result is 1e-6 to 1e-4 off.
+//
+// What bounds it.  64 matrices of 128 x 4096, bf16, 67 MB in and out: 31 us for A
+// (2.2 TB/s; each block waits for its chunk, multiplies, and waits again), 50 for
+// the steps (64 of 256 CUs; products through the LDS one after the other, each
+// between barriers), 52 for P X, 2.6 TB/s (26 GF of 2 s s l three times over, which
+// at the rate of a large product are 16 us, beside 21 us for its bytes, on two
+// blocks a CU).  64 of 16 x 4096 and 64 of 4096 x 16, 17 MB: 20, 11 and 24 us.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -147,7 +158,8 @@ __device__ __forceinline__ void chunk_products(f32x4* acc, uint32_t hi, uint32_t
     }
 }
 
-// One part of an item: chunks_per_part chunks, summed in order.
+// One part of an item: chunks_per_part chunks, summed in order; the next chunk's
+// loads are on their way during a chunk's products.
 template <int SP>
 __global__ __launch_bounds__(kThreads, 2) void thin_gram(NsRef ref, int64_t first, bool again) {
     using H = Thin<SP>;
@@ -288,21 +300,34 @@ __device__ __forceinline__ void put_square(char* at, int i, int j, int lane, con
     }
 }
 
-// The tile (i, j) of the product of two symmetric matrices that commute.
-template <int SP>
-__device__ __forceinline__ f32x4 square_product(uint32_t a, uint32_t b, int i, int j, int lane) {
+// A wave's tiles (ti, tj) of the product of two symmetric matrices that commute.
+// They follow each other along the rows of the triangle, so that all but the
+// first always share their row, whose pieces are read once; alike: the first too.
+template <int SP, int N, bool ALIKE>
+__device__ __forceinline__ void square_products(uint32_t a, uint32_t b, const int* ti, const int* tj, int lane, f32x4* sum) {
     constexpr int kLo = SP * SP * 2;
-    f32x4 sum{};
-    const int ri = 16 * i + (lane & 15), rj = 16 * j + (lane & 15);
+#pragma unroll
+    for (int n = 0; n < N; ++n) sum[n] = f32x4{};
 #pragma unroll
     for (int kk = 0; kk < SP / 32; ++kk) {
-        const uint32_t pa = a + square_piece<SP>(ri, kk * 4 + (lane >> 4)), pb = b + square_piece<SP>(rj, kk * 4 + (lane >> 4));
-        const h8 ah = lds_h8(pa), al = lds_h8(pa + kLo), bh = lds_h8(pb), bl = lds_h8(pb + kLo);
-        sum = __builtin_amdgcn_mfma_f32_16x16x32_f16(ah, bh, sum, 0, 0, 0);
-        sum = __builtin_amdgcn_mfma_f32_16x16x32_f16(ah, bl, sum, 0, 0, 0);
-        sum = __builtin_amdgcn_mfma_f32_16x16x32_f16(al, bh, sum, 0, 0, 0);
+        const auto piece = [&](uint32_t from, int i) { return from + square_piece<SP>(16 * i + (lane & 15), kk * 4 + (lane >> 4)); };
+        const uint32_t last = piece(a, ti[N - 1]);
+        const h8 h = lds_h8(last), l = lds_h8(last + kLo);
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            h8 ah = h, al = l;
+            if (!ALIKE && n == 0) {
+                const uint32_t own = piece(a, ti[0]);
+                ah = lds_h8(own);
+                al = lds_h8(own + kLo);
+            }
+            const uint32_t pb = piece(b, tj[n]);
+            const h8 bh = lds_h8(pb), bl = lds_h8(pb + kLo);
+            sum[n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ah, bh, sum[n], 0, 0, 0);
+            sum[n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ah, bl, sum[n], 0, 0, 0);
+            sum[n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(al, bh, sum[n], 0, 0, 0);
+        }
     }
-    return sum;
 }
 
 // A tile of a run's polynomial for the third kernel, as its fragments:
@@ -399,16 +424,21 @@ __global__ __launch_bounds__(64 * Thin<SP>::kWaves2) void thin_steps(NsRef ref, 
     char* const b_at = smem + (b - a);
     char* const p_at = smem + (p - a);
     constexpr float kDown = 1.0f / (1 << kLog2A);
+    const auto products = [&](uint32_t of, uint32_t by, f32x4* sum) {
+        if (ti[0] == ti[kOwn - 1]) square_products<SP, kOwn, true>(of, by, ti, tj, lane, sum);
+        else square_products<SP, kOwn, false>(of, by, ti, tj, lane, sum);
+    };
     f32x4 P[kOwn];
     for (int step = 0; step < steps.n; ++step) {
         const bool last = step + 1 == steps.n;
         const float sa = steps.a[step];
+        f32x4 w[kOwn];
+        products(a, a, w);
 #pragma unroll
         for (int k = 0; k < kOwn; ++k) {
-            const f32x4 square = square_product<SP>(a, a, ti[k], tj[k], lane);
             f32x4 B;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) B[e] = fmaf(steps.b[step], A[k][e], steps.c[step] * (square[e] * kDown));
+            for (int e = 0; e < 4; ++e) B[e] = fmaf(steps.b[step], A[k][e], steps.c[step] * (w[k][e] * kDown));
             if (step > 0 || !last) put_square<SP>(b_at, ti[k], tj[k], lane, B);
             if (step == 0) {
 #pragma unroll
@@ -419,12 +449,11 @@ __global__ __launch_bounds__(64 * Thin<SP>::kWaves2) void thin_steps(NsRef ref, 
             }
         }
         const auto times_b = [&](f32x4* v, uint32_t by) {         // v <- a v + B v, of which `by` is the LDS's copy
+            products(b, by, w);
 #pragma unroll
-            for (int k = 0; k < kOwn; ++k) {
-                const f32x4 w = square_product<SP>(b, by, ti[k], tj[k], lane);
+            for (int k = 0; k < kOwn; ++k)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) v[k][e] = fmaf(sa, v[k][e], w[e] * kDown);
-            }
+                for (int e = 0; e < 4; ++e) v[k][e] = fmaf(sa, v[k][e], w[k][e] * kDown);
         };
         const auto put = [&](char* to, const f32x4* v) {
 #pragma unroll
@@ -453,7 +482,7 @@ __global__ __launch_bounds__(64 * Thin<SP>::kWaves2) void thin_steps(NsRef ref, 
     for (int k = 0; k < kOwn; ++k) put_fragments<SP>(reinterpret_cast<_Float16*>(ref.ws + m.p), ti[k], tj[k], lane, P[k]);
 }
 
-// ---------------------------------------------------------------- third kernel: X through all steps
+// ---------------------------------------------------------------- third kernel: P X
 
 template <int SP, int ODT>
 __device__ __forceinline__ void store_chunk(const ZS_CONSTANT ThinItem& m, void* to, int64_t first, const float* stage, float back) {
