@@ -20,14 +20,14 @@
 // matrix becomes does not depend on it.  A product is one launch, the blocks
 // that fit the CUs, which work off lists of tiles.
 //
-// What bounds it.  192 matrices of 405M elements (96 of 1024 x 1024, 96 of 1024
-// x 2752), us of a step: X X^T 1343, A A 902, Q X 2708, in tiles of 256; with 2 m
-// n k for a product, half of it for the symmetric ones, 1.1 to 1.3e15 a second,
+// What bounds it.  14 matrices of 405M elements (8 of 4096 x 4096, 6 of 4096 x
+// 11008), us of a step: X X^T 1383, A A 909, Q X 2853, in tiles of 256; with 2 m n
+// k for a product, half of it for the symmetric ones, 1.06 to 1.2e15 a second,
 // where the loops between a tile's first loads and its stores run at 1.5e15,
-// about what a large matrix product of a library reaches.  The MFMAs are busy 77%
-// of the time at 1.7 GHz, to which the power limit takes the clock from 2.4: more
-// waves, deeper stages and the larger MFMA gain nothing, 32 x 32 x 16 loses 4%.
-// HBM is not what bounds: Q X reads and writes 6.0 GB in 2.7 ms.  Small lists are
+// about what a large matrix product of a library reaches.  The MFMAs are busy 62
+// to 77% of the time at 1.7 GHz, to which the power limit takes the clock from 2.4:
+// more waves, deeper stages and the larger MFMA gain nothing, 32 x 32 x 16 loses 4%.
+// HBM is not what bounds: Q X reads and writes 6.1 GB in 2.9 ms.  Small lists are
 // bound by their 2 + 3 n_steps launches of 4 to 6 us, one after the other.
 #include <hip/hip_runtime.h>
 
@@ -102,8 +102,8 @@ __device__ __forceinline__ double norm_factor(const ZS_CONSTANT MatrixItem& m, c
 }
 
 // A piece of X = U * factor, with its padding.  A read and a write: 405M elements
-// take 333 us, 4.9 TB/s.  Each block forms the norm again from the slots, 176 of
-// them for 1024 x 2752, behind its loads; a launch of its own would take 4 us.
+// take 334 us, 4.9 TB/s.  Each block forms the norm again from the slots, 2752 of
+// them for 4096 x 11008, behind its loads; a launch of its own would take 4 us.
 // Bands of 8 rows at a time, so that a wave's stores fill whole rows of a panel.
 __global__ __launch_bounds__(kBlock) void ortho_load(NsRef ref, int64_t first, double eps) {
     if (ref.skipped()) return;
