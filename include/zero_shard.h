@@ -782,8 +782,9 @@ int zero_multi_adam_step_coef(const void* table, const void* d_table, const void
  *   matrices, 1.7e-3 where a strong low-rank part is added, and 4e-3 for 1024
  *   singular values that fall as 1, 1/2, 1/3, ...  A singular value that rounding
  *   puts in the place of a zero grows by a each step, as any other.
- *   Coefficients have to keep singular values of [0, 1] within 4, and
- *   |b x + c x^2| and |a + b x + c x^2| of their squares x within 32
+ *   Coefficients have to keep singular values of [0, 1] within 4 and the largest
+ *   that they can be above 1/16, and |b x + c x^2| and |a + b x + c x^2| of their
+ *   squares x within 32
  *   (ZERO_ERANGE).  1 <= n_steps <= ZERO_MAX_ORTHO_STEPS.
  *   Workspace: zero_multi_orthogonalize_workspace_bytes(table) bytes, 256-byte
  *   aligned, clobbered.  A matrix takes about 4 bytes an element and 4 for each of

@@ -164,6 +164,10 @@ def test_coefficients_that_leave_fp16_are_refused():
         assert status(*steps) == L.ZERO_ENOSPC, steps
     for steps in (((5.0, 0.0, 0.0),), ((2.0, 0.0, 0.0),) * 3, ((1.0, 33.0, -33.0),), ((1.0, 40.0, -40.0),)):
         assert status(*steps) == L.ZERO_ERANGE, steps
+    # and those that leave nothing at fp16's small end
+    assert status(*((0.9, 0.0, 0.0),) * 26) == L.ZERO_ENOSPC
+    for steps in (((0.9, 0.0, 0.0),) * 27, ((0.0, 0.0, 0.0),), ((0.06, 0.0, 0.0),)):
+        assert status(*steps) == L.ZERO_ERANGE, steps
     for bad in (math.nan, math.inf):
         assert status((bad, 0.0, 0.0)) == L.ZERO_EINVAL
 

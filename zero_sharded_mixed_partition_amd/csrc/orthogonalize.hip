@@ -600,7 +600,7 @@ int launch_product(const OrthoPass& p, const NsRef& ref, const NsStep& step, hip
 
 // The singular values start in [0, 1].  What each step makes of the largest
 // interval they can be in has to stay within what fp16 holds of X, A and B at
-// their scales, with room for single entries.
+// their scales, with room for single entries, and well above its small end.
 int check_coefs(const double* coefs, int32_t n_steps, OrthoSteps* steps) {
     if (coefs == nullptr) return fail(ZERO_EINVAL, "coefs is NULL");
     if (n_steps < 1 || n_steps > ZERO_MAX_ORTHO_STEPS)
@@ -619,8 +619,8 @@ int check_coefs(const double* coefs, int32_t n_steps, OrthoSteps* steps) {
             next = std::max(next, std::fabs(x * (a + y * (b + c * y))));
         }
         poly = std::max(poly, factor);
-        if (poly > kMostPoly || next > 4.0)
-            return fail(ZERO_ERANGE, "step %d takes singular values of [0, 1] to %g (at most 4), its polynomial to %g (at most 32)",
+        if (poly > kMostPoly || next > 4.0 || next < 0.0625)
+            return fail(ZERO_ERANGE, "step %d takes singular values of [0, 1] to %g (1/16 to 4), its polynomial to %g (at most 32)",
                         k, next, poly);
         top = next;
         if (run > kMostCarried || run * factor > kMostRun) {
