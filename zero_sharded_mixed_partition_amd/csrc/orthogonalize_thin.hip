@@ -25,7 +25,7 @@
 // of its own, which follows it to the sum.  A run's result is 1e-6 to 1e-4 off.
 //
 // What bounds it.  64 matrices of 128 x 4096, bf16, 67 MB in and out: 31 us for A
-// (2.2 TB/s; each block waits for its chunk, multiplies, and waits again), 50 for
+// (2.2 TB/s; each block waits for its chunk, multiplies, and waits again), 46 for
 // the steps (64 of 256 CUs; products through the LDS one after the other, each
 // between barriers), 52 for P X, 2.6 TB/s (26 GF of 2 s s l three times over, which
 // at the rate of a large product are 16 us, beside 21 us for its bytes, on two
@@ -35,6 +35,7 @@
 #include <algorithm>
 #include <climits>
 #include <cmath>
+#include <type_traits>
 #include <vector>
 
 #include "orthogonalize.h"
@@ -266,6 +267,26 @@ __device__ __forceinline__ uint32_t square_piece(int r, int piece) {
     return r * (SP * 2) + ((piece ^ order) << 4);
 }
 
+// Of four lanes in a row, lane t gets element t of each: a tile's mirror image
+// then leaves in 8-byte pieces (2 bytes at a time the steps of 64 x 128 x 4096
+// take 49.9 us, so 46.4).
+__device__ __forceinline__ h4 quad_transpose(h4 v, int lane) {
+    typedef int i2 __attribute__((ext_vector_type(2)));
+    const i2 w = __builtin_bit_cast(i2, v);
+    const bool upper = lane & 2;
+    const auto from = [&](auto quad) {               // all four lanes' copy of one lane's pair that holds element t
+        constexpr int kQuad = decltype(quad)::value;
+        const int a = __builtin_amdgcn_update_dpp(0, w[0], kQuad, 0xF, 0xF, true);
+        const int b = __builtin_amdgcn_update_dpp(0, w[1], kQuad, 0xF, 0xF, true);
+        return upper ? b : a;
+    };
+    const int u0 = from(std::integral_constant<int, 0x00>{}), u1 = from(std::integral_constant<int, 0x55>{});
+    const int u2 = from(std::integral_constant<int, 0xAA>{}), u3 = from(std::integral_constant<int, 0xFF>{});
+    const uint32_t halves = lane & 1 ? 0x07060302u : 0x05040100u;
+    const i2 out = {(int)__builtin_amdgcn_perm((uint32_t)u1, (uint32_t)u0, halves), (int)__builtin_amdgcn_perm((uint32_t)u3, (uint32_t)u2, halves)};
+    return __builtin_bit_cast(h4, out);
+}
+
 // A tile's values (rows 16 i + 4 g + e, column 16 j + c) into a symmetric
 // matrix of two fp16: hi at `at`, lo behind it.  Of a tile on the diagonal only
 // the values below it are taken: a matrix carried through the steps has to stay
@@ -286,17 +307,19 @@ __device__ __forceinline__ void put_square(char* at, int i, int j, int lane, con
     if (i != j) {
         *reinterpret_cast<h4*>(row) = h;
         *reinterpret_cast<h4*>(row + kLo) = l;
+        char* mirror = at + square_piece<SP>(16 * i + 4 * g + (c & 3), 2 * j + (c >> 3)) + (c & 4) * 2;
+        *reinterpret_cast<h4*>(mirror) = quad_transpose(h, lane);
+        *reinterpret_cast<h4*>(mirror + kLo) = quad_transpose(l, lane);
+        return;
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        if (i == j && 4 * g + e < c) continue;
+        if (4 * g + e < c) continue;
         char* to = at + square_piece<SP>(16 * i + 4 * g + e, 2 * j + (c >> 3)) + (c & 7) * 2;
         *reinterpret_cast<_Float16*>(to) = h[e];
         *reinterpret_cast<_Float16*>(to + kLo) = l[e];
-        if (i == j) {
-            *reinterpret_cast<_Float16*>(row + 2 * e) = h[e];
-            *reinterpret_cast<_Float16*>(row + kLo + 2 * e) = l[e];
-        }
+        *reinterpret_cast<_Float16*>(row + 2 * e) = h[e];
+        *reinterpret_cast<_Float16*>(row + kLo + 2 * e) = l[e];
     }
 }
 
