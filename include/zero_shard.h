@@ -789,7 +789,7 @@ int zero_multi_adam_step_coef(const void* table, const void* d_table, const void
  *   Workspace: zero_multi_orthogonalize_workspace_bytes(table) bytes, 256-byte
  *   aligned, clobbered.  A matrix takes about 4 bytes an element and 4 for each of
  *   its short side's square; with a short side of at most 128, 2 bytes an element
- *   and at most 2 MB.  A list that would take more than 4 GiB
+ *   and some 2 MB at most.  A list that would take more than 4 GiB
  *   is worked off in parts.  Calls, and graphs recorded with them, that may run at
  *   the same time need a workspace each.
  * zero_multi_muon_update (master, ortho; param_out): per element, in float32,

@@ -192,6 +192,36 @@ def test_rank_three(Z, shape, n):
     assert float(torch.linalg.svdvals(o.cpu().double())[0]) < 1.23
 
 
+def test_many_steps_in_place_and_recorded(Z):
+    """Steps that take several runs, in the update's place, in batches and in a
+    graph: as out of place and alone."""
+    shapes = [(3, 20, 300), (4, 500, 40), (2, 128, 260), (90, 90), (150, 140)]
+    coefs = M.COEFS[:1] * 12
+    us = [place(draw(s, 60 + k, "spread"), "f16")[0] for k, s in enumerate(shapes)]
+    alone = []
+    for u in us:
+        for m in u.reshape(-1, *u.shape[-2:]):
+            o = torch.empty(m.shape, dtype=torch.float16, device="cuda")
+            orthogonalize(Z, Z.MatrixTable([m.clone()], [o]), coefs=coefs)
+            alone.append(o)
+    table, kept = Z.MatrixTable(us), [u.clone() for u in us]
+    ws = workspace(Z, table)
+    Z.zero_multi_orthogonalize(table, ws, coefs)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    for k in range(3):
+        got = [m for u in us for m in u.reshape(-1, *u.shape[-2:])]
+        assert all(torch.equal(bits(x), bits(y)) for x, y in zip(got, alone)), k
+        for u, x in zip(us, kept):
+            u.copy_(x)
+        if k == 0:
+            with torch.cuda.graph(graph):
+                Z.zero_multi_orthogonalize(table, ws, coefs)
+        ws.fill_(255)
+        graph.replay()
+        torch.cuda.synchronize()
+
+
 def test_one_step_that_keeps_x(Z):
     """(1, 0, 0) returns U over its norm: X's rounding and the result's remain."""
     u, _ = place(draw((150, 90), 6), "f32")
