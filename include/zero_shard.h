@@ -780,12 +780,12 @@ int zero_multi_adam_step_coef(const void* table, const void* d_table, const void
  *   its own rounding the result of these five is off (relative, Frobenius) by 1e-6
  *   to 1e-4 with a short side up to 128; above it by about 1.2e-3 for random
  *   matrices, 1.7e-3 where a strong low-rank part is added, and 4e-3 for 1024
- *   singular values that fall as 1, 1/2, 1/3, ...  A singular value that rounding
- *   puts in the place of a zero grows by a each step, as any other.
+ *   singular values that fall as 1, 1/2, 1/3, ...  (With |U| below eps / 1000 X
+ *   begins at fp16's small end there and loses digits.)  A singular value that
+ *   rounding puts in the place of a zero grows by a each step, as any other.
  *   Coefficients have to keep singular values of [0, 1] within 4 and the largest
  *   that they can be above 1/16, and |b x + c x^2| and |a + b x + c x^2| of their
- *   squares x within 32
- *   (ZERO_ERANGE).  1 <= n_steps <= ZERO_MAX_ORTHO_STEPS.
+ *   squares x within 32 (ZERO_ERANGE).  1 <= n_steps <= ZERO_MAX_ORTHO_STEPS.
  *   Workspace: zero_multi_orthogonalize_workspace_bytes(table) bytes, 256-byte
  *   aligned, clobbered.  A matrix takes about 4 bytes an element and 4 for each of
  *   its short side's square; with a short side of at most 128, 2 bytes an element

@@ -366,20 +366,22 @@ __device__ __forceinline__ void put_fragments(_Float16* to, int i, int j, int la
         l[e] = (_Float16)(v[e] - (float)h[e]);
     }
     _Float16* at = to + (((j * (SP / 32) + i / 2) * 64 + g * 16 + c) * 8 + (i & 1) * 4);
+    _Float16* mirror = to + (((i * (SP / 32) + j / 2) * 64 + (c >> 2) * 16 + 4 * g) * 8 + (j & 1) * 4);
     if (i != j) {
         *reinterpret_cast<h4*>(at) = h;
         *reinterpret_cast<h4*>(at + SP * SP) = l;
+        mirror += (c & 3) * 8;
+        *reinterpret_cast<h4*>(mirror) = quad_transpose(h, lane);
+        *reinterpret_cast<h4*>(mirror + SP * SP) = quad_transpose(l, lane);
+        return;
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        if (i == j && 4 * g + e < c) continue;
-        _Float16* mirror = to + (((i * (SP / 32) + j / 2) * 64 + (c >> 2) * 16 + 4 * g + e) * 8 + (j & 1) * 4 + (c & 3));
-        mirror[0] = h[e];
-        mirror[SP * SP] = l[e];
-        if (i == j) {
-            at[e] = h[e];
-            at[SP * SP + e] = l[e];
-        }
+        if (4 * g + e < c) continue;
+        mirror[8 * e + (c & 3)] = h[e];
+        mirror[8 * e + (c & 3) + SP * SP] = l[e];
+        at[e] = h[e];
+        at[SP * SP + e] = l[e];
     }
 }
 
