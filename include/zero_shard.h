@@ -773,16 +773,25 @@ int zero_multi_adam_step_coef(const void* table, const void* d_table, const void
  *   more rows than columns X X^T ... X is formed as X ... X^T X, which is equal.)
  *   eps = 0 leaves a zero matrix zero.  A matrix that holds an inf or a NaN
  *   becomes NaN.  Where the short side exceeds 128, X, X X^T and the polynomial
- *   are rounded to fp16 between products.  Up to 128 they have 22 bits, and X is
- *   rounded to fp16 only between runs of steps: a run ends where the product of
- *   the largest |a + b x + c x^2| could exceed 1024 (256 before its last step);
- *   five steps of (3.4445, -4.7750, 2.0315) are one.  Sums are float32.  Besides
- *   its own rounding the result of these five is off (relative, Frobenius) by 1e-6
- *   to 1e-4 with a short side up to 128; above it by about 1.2e-3 for random
- *   matrices, 1.7e-3 where a strong low-rank part is added, and 4e-3 for 1024
- *   singular values that fall as 1, 1/2, 1/3, ...  (With |U| below eps / 1000 X
- *   begins at fp16's small end there and loses digits.)  A singular value that
- *   rounding puts in the place of a zero grows by a each step, as any other.
+ *   are rounded to fp16 between products; X begins as U times a power of two, so
+ *   that fp16 and bf16 updates are not rounded there, and fp32 ones are.  Up to 128
+ *   they have 22 bits, and X is rounded to fp16 only between runs of steps: a run
+ *   ends where the product of the largest |a + b x + c x^2| could exceed 1024 (256
+ *   before its last step); five steps of (3.4445, -4.7750, 2.0315) are one.  Sums
+ *   are float32.  (With |U| below eps / 1000 X begins at fp16's small end there and
+ *   loses digits.)
+ *   How far the result of these five is off, besides its own rounding (relative,
+ *   Frobenius), for random matrices and for singular values that fall:
+ *                                random   1/k      1/k^2    rank 16  rank 3
+ *     short side up to 128       1e-5     1e-4     7e-4     6e-5     2e-4
+ *     above, update fp16, bf16   1.2e-3   2.5e-3   7.5e-3   3.3e-2   5e-2
+ *     above, update fp32         1.3e-3   4.2e-3   2.1e-2   3.4e-2   5e-2
+ *   What rounding leaves in the place of a zero or small singular value grows by a
+ *   each step, as any other: about 2^-12 of X after the first step by a^4 = 141 to
+ *   the end of five.  Seven steps, above 128: 2e-3 for random matrices, 4e-2 for
+ *   1/k^2 (fp32 1.2e-1), 4e-1 for rank 16.  Between the matrix's own singular
+ *   directions such results are within 1e-2 all the same, and all singular values
+ *   stay in the steps' band.
  *   Coefficients have to keep singular values of [0, 1] within 4 and the largest
  *   that they can be above 1/16, and |b x + c x^2| and |a + b x + c x^2| of their
  *   squares x within 32 (ZERO_ERANGE).  1 <= n_steps <= ZERO_MAX_ORTHO_STEPS.

@@ -40,7 +40,7 @@ struct MatrixItem {
     void* out;
     int64_t x0, x1;                     // workspace: the iterate and the next one, half [sp][lp]
     int64_t a, b;                       // workspace: X X^T and the polynomial, half [sp][sp]
-    int64_t slots;                      // workspace: partial sums of squares, double [n_slots]
+    int64_t slots;                      // workspace: partial sums of squares, double [n_slots], and start_factor
     int32_t n_slots;
     int32_t s, l, sp, lp;
     int32_t udt, odt;

@@ -67,13 +67,15 @@ __device__ __forceinline__ h4 lds_column(uint32_t a) {
     return __builtin_bit_cast(h4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4*)(uintptr_t)a));
 }
 
-// The float32 value rounded to fp16.  Opaque to the compiler, which otherwise may
-// or may not round the operation before it straight to fp16, and so make results
-// depend on the tile size.
-__device__ __forceinline__ _Float16 to_half(float x) {
+// The value as float32 has it.  Opaque to the compiler, which otherwise may or may
+// not round the operation before it straight to 16 bits, and so make results depend
+// on the tile size.
+__device__ __forceinline__ float as_float(float x) {
     __asm__("" : "+v"(x));
-    return (_Float16)x;
+    return x;
 }
+
+__device__ __forceinline__ _Float16 to_half(float x) { return (_Float16)as_float(x); }
 
 // ---------------------------------------------------------------- boxes of U
 

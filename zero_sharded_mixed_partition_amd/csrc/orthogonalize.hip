@@ -10,8 +10,12 @@
 // power of two that keeps typical entries far from fp16's small end (X: about
 // sqrt(l), A and Q: 2^10); every sum is float32, |U|_F float64.  fp16 instead of
 // bf16 because the iteration multiplies what is lost: on 1024 x 1024 matrices of
-// noise plus a low-rank part the result is 1.2e-3 off (relative, Frobenius)
-// with fp16 in these places and 1e-2 with bf16, at the same MFMA rate.
+// noise plus a low-rank part the result is 1.1e-3 off (relative, Frobenius)
+// with fp16 in these places and 1e-2 with bf16, at the same MFMA rate.  What
+// decides where singular values fall is X's rounding after the early steps: what
+// it leaves in a zero's place grows by a = 3.4 a step.  1024 x 1024, fp16 U: 2.3e-3
+// for 1 / k, 7.5e-3 for 1 / k^2, 3.2e-2 for rank 16, where a model with X in two
+// fp16 (three times the products of X, twice its memory) gives 3e-4.
 //
 // Products.  A step is three, X X^T, A A and Q X, in square tiles of T x T over
 // a padded copy in the workspace, so no load is bounded and padding stays zero.
@@ -85,9 +89,9 @@ __global__ __launch_bounds__(kBlock) void ortho_squares(NsRef ref, int64_t first
         reinterpret_cast<double*>(ref.ws + m.slots)[(int64_t)t.i * ((m.l + kPieceColumns - 1) / kPieceColumns) + t.j] = acc;
 }
 
-// The factor 2^log2_scale / max(|U|_F, eps); NaN if U is not finite, so that all of the result is.
-__device__ __forceinline__ double norm_factor(const ZS_CONSTANT MatrixItem& m, const char* ws, double eps, double* s_sq,
-                                              uint32_t* s_bad) {
+// max(|U|_F, eps), and NaN if U is not finite.
+__device__ __forceinline__ double divisor(const ZS_CONSTANT MatrixItem& m, const char* ws, double eps, double* s_sq,
+                                          uint32_t* s_bad) {
     const double* slots = reinterpret_cast<const double*>(ws + m.slots);
     double acc = 0.0;
     for (int k = threadIdx.x; k < m.n_slots; k += kBlock) acc += slots[k];
@@ -96,12 +100,21 @@ __device__ __forceinline__ double norm_factor(const ZS_CONSTANT MatrixItem& m, c
     if (threadIdx.x == 0) s_sq[0] = acc;
     __syncthreads();
     const double norm = sqrt(s_sq[0]);
-    if (!(norm < INFINITY)) return NAN;
-    const double by = norm > eps ? norm : eps;
-    return by > 0.0 ? ldexp(1.0, m.log2_scale) / by : 0.0;
+    return !(norm < INFINITY) ? NAN : norm > eps ? norm : eps;
 }
 
-// A piece of X = U * factor, with its padding.  A read and a write: 405M elements
+// What is left of X's factor where the iterate is U times a power of two, in (1, 2].
+__device__ __forceinline__ double* start_factor(const NsRef& ref, const ZS_CONSTANT MatrixItem& m) {
+    return reinterpret_cast<double*>(ref.ws + m.slots) + m.n_slots;
+}
+
+// A piece of U times a power of two, 2^log2_scale / max(|U|, eps) to within 2,
+// with its padding: a 16-bit U is not rounded by it (but for bf16 elements below
+// 2^-14 of the typical one), and the first step's sums take the rest of the factor.
+// With all of it here U would be rounded to fp16 once more, and what that leaves in
+// a zero singular value's place grows by a in every step: 512 x 512, 1 / k^2, 2.0e-2
+// instead of 7.3e-3 off.
+// A read and a write: 405M elements
 // take 334 us, 4.9 TB/s.  Each block forms the norm again from the slots, 2752 of
 // them for 4096 x 11008, behind its loads; a launch of its own would take 4 us.
 // Bands of 8 rows at a time, so that a wave's stores fill whole rows of a panel.
@@ -122,15 +135,19 @@ __global__ __launch_bounds__(kBlock) void ortho_load(NsRef ref, int64_t first, d
 #pragma unroll
             for (int k = 0; k < 8; ++k) x[n][k] = 0.0f;
     }
-    int e;
-    const float f = (float)frexp(norm_factor(m, ref.ws, eps, s_sq, s_bad), &e);
+    const double by = divisor(m, ref.ws, eps, s_sq, s_bad);
+    const float keep = by < INFINITY ? 1.0f : NAN;           // of a U that is not finite, all of X is NaN
+    int up = 0;
+    const double fraction = by > 0.0 && by < INFINITY ? frexp(by, &up) : 1.0;
+    if (t.i == 0 && t.j == 0 && threadIdx.x == 0) *start_factor(ref, m) = 1.0 / fraction;
+    const int e = m.log2_scale - up;
     _Float16* X = reinterpret_cast<_Float16*>(ref.ws + m.x0);
 #pragma unroll
     for (int n = 0; n < 8; ++n) {
         const Vector8<kPieceRows, 8> v(m.s, m.l, m.tall, r0, c0, n);
         h8 h;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) h[k] = k < v.valid ? (_Float16)scaled(x[n][k], f, e) : (_Float16)0;
+        for (int k = 0; k < 8; ++k) h[k] = k < v.valid ? (_Float16)(ldexpf(x[n][k], e) * keep) : (_Float16)0;
         if (m.tall) {
 #pragma unroll
             for (int k = 0; k < 8; ++k) block[v.r + k][v.c] = h[k];
@@ -222,7 +239,7 @@ __device__ __host__ __forceinline__ int stages_of(int depth) { return (depth + 2
 struct NsStep {
     float a, b, c;
     int32_t odd;                                   // the iterate is in x1
-    int32_t last;
+    int32_t first, last;
 };
 
 // Four neighbours of a row of X into the caller's matrix.
@@ -376,6 +393,8 @@ __global__ __launch_bounds__(64 * WM * WN) void ortho_product(NsRef ref, int64_t
         } else {
             then = Source{now.m, now.n, 0, 0, INT32_MAX};
         }
+        float rest = 1.0f;                         // read here: its latency passes behind the stages
+        if (MODE != kPoly && step.first) rest = (float)*(const ZS_CONSTANT double*)start_factor(ref, ref.item(tile.item));
 #pragma unroll
         for (int x = 0; x < UM; ++x)
 #pragma unroll
@@ -411,7 +430,7 @@ __global__ __launch_bounds__(64 * WM * WN) void ortho_product(NsRef ref, int64_t
                                            : panel_at((int64_t)tj * T + in, (int64_t)ti * T + im, sp);
         const auto at = [&](int x, int y) { return at0 + (x >> 1) * sp * kPanel + (x & 1) * 16 + y * 16 * kPanel; };
         if constexpr (MODE == kApply) {
-            const float scale = step.last ? ldexpf(1.0f, -kLog2A - m.log2_scale) : ldexpf(1.0f, -kLog2A);
+            const float scale = ldexpf(rest, step.last ? -kLog2A - m.log2_scale : -kLog2A);
             _Float16* out = reinterpret_cast<_Float16*>(ref.ws + (step.odd ? m.x0 : m.x1));
 #pragma unroll
             for (int x = 0; x < UM; ++x)
@@ -419,7 +438,7 @@ __global__ __launch_bounds__(64 * WM * WN) void ortho_product(NsRef ref, int64_t
                 for (int y = 0; y < UN; ++y) {
                     float v[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) v[e] = acc[x][y][e] * scale;
+                    for (int e = 0; e < 4; ++e) v[e] = as_float(acc[x][y][e] * scale);
                     if (!step.last) {
                         *reinterpret_cast<h4*>(out + at(x, y)) = h4{(_Float16)v[0], (_Float16)v[1], (_Float16)v[2], (_Float16)v[3]};
                         continue;
@@ -433,7 +452,7 @@ __global__ __launch_bounds__(64 * WM * WN) void ortho_product(NsRef ref, int64_t
             // (c, r .. r + 3) is what a lane holds of the symmetric result; its mirror
             // (r .. r + 3, c) goes through the LDS, 32 rows at a time, to leave in
             // whole rows of a panel
-            const float scale = MODE == kGram ? ldexpf(1.0f, kLog2A - 2 * m.log2_scale) : step.c * ldexpf(1.0f, -kLog2A);
+            const float scale = MODE == kGram ? ldexpf(rest * rest, kLog2A - 2 * m.log2_scale) : step.c * ldexpf(1.0f, -kLog2A);
             const float diagonal = step.a * (1 << kLog2A);
             const _Float16* old = reinterpret_cast<const _Float16*>(ref.ws + m.a);
             _Float16* out = reinterpret_cast<_Float16*>(ref.ws + (MODE == kGram ? m.a : m.b));
@@ -448,7 +467,7 @@ __global__ __launch_bounds__(64 * WM * WN) void ortho_product(NsRef ref, int64_t
                         h4 h;
                         if constexpr (MODE == kGram) {
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) h[e] = (_Float16)(acc[x + z][y][e] * scale);
+                            for (int e = 0; e < 4; ++e) h[e] = to_half(acc[x + z][y][e] * scale);
                         } else {
                             const h4 a = *reinterpret_cast<const h4*>(old + at(x + z, y));
 #pragma unroll
@@ -519,7 +538,7 @@ void place_item(MatrixItem* it, int64_t* at) {
     it->x1 = place(at, x);
     it->a = place(at, a);
     it->b = place(at, a);
-    it->slots = place(at, (int64_t)it->n_slots * 8);
+    it->slots = place(at, (int64_t)(it->n_slots + 1) * 8);
 }
 
 constexpr int kXCDs = 8, kCUs = 256;
@@ -755,7 +774,7 @@ int zero_multi_orthogonalize(const void* table, const void* d_table, const doubl
         hipLaunchKernelGGL(ortho_load, dim3((unsigned)pass.n_pieces), dim3(kBlock), 0, s, ref, pass.piece_first, eps);
         rc = launch_status("ortho_load");
         for (int k = 0; k < n_steps && rc == ZERO_OK; ++k) {
-            const NsStep step{steps.a[k], steps.b[k], steps.c[k], k & 1, k + 1 == n_steps};
+            const NsStep step{steps.a[k], steps.b[k], steps.c[k], k & 1, k == 0, k + 1 == n_steps};
             rc = launch_product<kGram>(pass, ref, step, s);
             if (rc == ZERO_OK) rc = launch_product<kPoly>(pass, ref, step, s);
             if (rc == ZERO_OK) rc = launch_product<kApply>(pass, ref, step, s);
