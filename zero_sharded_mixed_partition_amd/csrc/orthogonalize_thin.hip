@@ -33,12 +33,12 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
-#include <climits>
 #include <cmath>
 #include <type_traits>
 #include <vector>
 
 #include "orthogonalize.h"
+#include "part_exponent.h"
 
 namespace zero_shard {
 namespace {
@@ -177,7 +177,7 @@ __global__ __launch_bounds__(kThreads, 2) void thin_gram(NsRef ref, int64_t firs
     f32x4 acc[kOwn];
 #pragma unroll
     for (int k = 0; k < kOwn; ++k) acc[k] = f32x4{};
-    int run = INT_MIN / 4;                       // exponent that the sums are scaled by
+    int run = kAllZero;                          // exponent that the sums are scaled by
     bool bad = false;
     const int64_t c_first = (int64_t)part * m.chunks_per_part;
     const int64_t c_end = c_first + m.chunks_per_part < m.n_chunks ? c_first + m.chunks_per_part : m.n_chunks;
@@ -205,7 +205,7 @@ __global__ __launch_bounds__(kThreads, 2) void thin_gram(NsRef ref, int64_t firs
             // the largest element lands in [2^14, 2^15)
             const int e = (int)ilogbf(__uint_as_float(top)) - 14;
             if (e > run) {
-                const int down = run < INT_MIN / 8 ? 0 : 2 * (run - e);
+                const int down = part_shift(run, e);
 #pragma unroll
                 for (int k = 0; k < kOwn; ++k)
 #pragma unroll
@@ -213,7 +213,7 @@ __global__ __launch_bounds__(kThreads, 2) void thin_gram(NsRef ref, int64_t firs
                 run = e;
             }
         }
-        const int shift = run < INT_MIN / 8 ? 0 : -run;
+        const int shift = has_exponent(run) ? -run : 0;
 #pragma unroll
         for (int n = 0; n < 8; ++n) {
             h8 h, g;
@@ -254,7 +254,7 @@ __global__ __launch_bounds__(kThreads, 2) void thin_gram(NsRef ref, int64_t firs
             reinterpret_cast<f32x4*>(out)[k] = sum;
         }
     }
-    if (threadIdx.x == 0) reinterpret_cast<int32_t*>(ref.ws + m.exponents)[part] = bad ? INT_MAX : run;
+    if (threadIdx.x == 0) reinterpret_cast<int32_t*>(ref.ws + m.exponents)[part] = bad ? kNotFinite : run;
 }
 
 // ---------------------------------------------------------------- second kernel: the steps' polynomials
@@ -395,9 +395,9 @@ __global__ __launch_bounds__(64 * Thin<SP>::kWaves2) void thin_steps(NsRef ref, 
     const ZS_CONSTANT ThinItem& m = ((const ZS_CONSTANT ThinItem*)ref.items)[first_item + blockIdx.x];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int32_t* exponents = reinterpret_cast<const int32_t*>(ref.ws + m.exponents);
-    int top = INT_MIN;
+    int top = kAllZero;
     for (int p = 0; p < m.n_parts; ++p) top = exponents[p] > top ? exponents[p] : top;
-    const bool bad = top == INT_MAX;
+    const bool bad = top == kNotFinite;
     int ti[kOwn], tj[kOwn];
     f32x4 A[kOwn];
 #pragma unroll
@@ -412,12 +412,12 @@ __global__ __launch_bounds__(64 * Thin<SP>::kWaves2) void thin_steps(NsRef ref, 
 #pragma unroll 8
     for (int p = 0; p < m.n_parts; ++p) {
         const f32x4* part = reinterpret_cast<const f32x4*>(ref.ws + m.parts) + (int64_t)p * H::kTiles * 64;
-        const int down = exponents[p] < INT_MIN / 8 ? 0 : 2 * (exponents[p] - top);
+        const int down = part_shift(exponents[p], top);
 #pragma unroll
         for (int k = 0; k < kOwn; ++k) {
             const f32x4 v = part[(wave * kOwn + k) * 64 + lane];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) A[k][e] += ldexpf(v[e], bad ? 0 : down);
+            for (int e = 0; e < 4; ++e) A[k][e] += ldexpf(v[e], down);
         }
     }
     // |U|^2 = the trace
@@ -430,7 +430,7 @@ __global__ __launch_bounds__(64 * Thin<SP>::kWaves2) void thin_steps(NsRef ref, 
     __syncthreads();
     double trace = s_diag[lane % SP] + (SP == 128 ? s_diag[lane + 64] : 0.0);
     for (int off = (SP < 64 ? SP : 64) / 2; off > 0; off >>= 1) trace += __shfl_xor(trace, off, 64);
-    const int up = top < INT_MIN / 8 || bad ? 0 : top;
+    const int up = !has_exponent(top) || bad ? 0 : top;
     const double norm = ldexp(sqrt(trace), up);
     // what a run has left is X times a power of two
     const double by = again ? ldexp(1.0, m.log2_scale) : norm > eps ? norm : eps;
