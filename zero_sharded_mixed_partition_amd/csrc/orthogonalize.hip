@@ -617,6 +617,34 @@ int launch_product(const OrthoPass& p, const NsRef& ref, const NsStep& step, hip
     return launch_status("ortho_product");
 }
 
+// The largest of what a step makes of singular values x in [0, top]: |x (a + b y +
+// c y^2)| with y = x^2, |b y + c y^2| and |a + b y + c y^2|, from their values at the
+// ends and where their derivatives vanish.
+struct StepRange {
+    double next, poly, factor;
+};
+
+StepRange step_range(double a, double b, double c, double top) {
+    StepRange m{0.0, 0.0, std::fabs(a)};
+    const double end = top * top;
+    const auto at = [&](double y) {
+        if (!(y > 0.0 && y <= end)) return;
+        const double p = y * (b + c * y);
+        m.poly = std::max(m.poly, std::fabs(p));
+        m.factor = std::max(m.factor, std::fabs(a + p));
+        m.next = std::max(m.next, std::sqrt(y) * std::fabs(a + p));
+    };
+    at(end);
+    at(-0.5 * b / c);                            // b + 2 c y = 0
+    const double d = 9.0 * b * b - 20.0 * a * c; // a + 3 b y + 5 c y^2 = 0
+    if (d >= 0.0) {
+        const double q = -0.5 * (3.0 * b + std::copysign(std::sqrt(d), b));
+        at(q / (5.0 * c));
+        at(a / q);
+    }
+    return m;
+}
+
 // The singular values start in [0, 1].  What each step makes of the largest
 // interval they can be in has to stay within what fp16 holds of X, A and B at
 // their scales, with room for single entries, and well above its small end.
@@ -630,23 +658,17 @@ int check_coefs(const double* coefs, int32_t n_steps, OrthoSteps* steps) {
     for (int k = 0; k < n_steps; ++k) {
         const double a = coefs[3 * k], b = coefs[3 * k + 1], c = coefs[3 * k + 2];
         if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c)) return fail(ZERO_EINVAL, "coefs must be finite");
-        double next = 0.0, poly = 0.0, factor = 0.0;
-        for (int i = 0; i <= 4096; ++i) {
-            const double x = top * i / 4096, y = x * x;
-            poly = std::max(poly, std::fabs(y * (b + c * y)));
-            factor = std::max(factor, std::fabs(a + y * (b + c * y)));
-            next = std::max(next, std::fabs(x * (a + y * (b + c * y))));
-        }
-        poly = std::max(poly, factor);
-        if (poly > kMostPoly || next > 4.0 || next < 0.0625)
+        const StepRange m = step_range(a, b, c, top);
+        const double poly = std::max(m.poly, m.factor);
+        if (!(poly <= kMostPoly && m.next <= 4.0 && m.next >= 0.0625))
             return fail(ZERO_ERANGE, "step %d takes singular values of [0, 1] to %g (1/16 to 4), its polynomial to %g (at most 32)",
-                        k, next, poly);
-        top = next;
-        if (run > kMostCarried || run * factor > kMostRun) {
+                        k, m.next, poly);
+        top = m.next;
+        if (run > kMostCarried || run * m.factor > kMostRun) {
             steps->begins |= 1u << k;
             run = 1.0;
         }
-        run *= factor;
+        run *= m.factor;
         steps->a[k] = (float)a;
         steps->b[k] = (float)b;
         steps->c[k] = (float)c;
