@@ -6,8 +6,10 @@ scaler).  save() writes them as one .npy file each and one JSON file in a
 directory; load() restores them into a ShardAdam built over the same shard
 size.  ShardAdam8 saves its 8-bit moments as they are (codes and scales), and
 the seed of their rounding; MultiAdam saves its tensors in list order, and the
-group of each: a list of other tensors or with other groups is refused.  Because
-every step is deterministic, k steps, save, load and k more steps give the same
+group of each: a list of other tensors or with other groups is refused.  MultiMuon
+also saves what its steps are made of besides the hyperparameters (coefs, eps, each
+matrix's factor of the learning rate, the type of its updates): others are refused.
+Because every step is deterministic, k steps, save, load and k more steps give the same
 bits as 2k uninterrupted steps.
 """
 import copy
@@ -35,6 +37,8 @@ def state_dict(opt) -> dict:
         d["seed"] = opt.seed                           # keys the rounding of 8-bit moments
     if hasattr(opt, "groups"):
         d["groups"] = list(opt.groups)                 # one per tensor of a list
+    if hasattr(opt, "checkpoint_settings"):
+        d["settings"] = opt.checkpoint_settings()
     return d
 
 
@@ -54,6 +58,11 @@ def load_state_dict(opt, d: dict) -> None:
     if have is not None and list(have) != want:
         raise ValueError(f"{len(have)} tensors in the checkpoint, {len(want)} expected" if len(have) != len(want) else
                          "the checkpoint's tensors belong to other groups")
+    if d.get("settings") is not None:
+        mine = opt.checkpoint_settings() if hasattr(opt, "checkpoint_settings") else {}
+        for k, x in d["settings"].items():
+            if mine.get(k) != x:
+                raise ValueError(f"the checkpoint was written with other {k}: {x}, not {mine.get(k)}")
     for k, dst in arrays.items():
         dst.copy_(torch.from_numpy(np.ascontiguousarray(d[k])).view(dst.shape))
     opt.t = int(d["t"])
@@ -79,7 +88,7 @@ def save(opt, directory: str) -> None:
     d = state_dict(opt)
     for k in opt.checkpoint_arrays():
         np.save(os.path.join(directory, f"{k}.npy"), d[k])
-    meta = {k: d[k] for k in ("t", "skipped", "scaler", "hyper", "seed", "groups") if k in d}
+    meta = {k: d[k] for k in ("t", "skipped", "scaler", "hyper", "seed", "groups", "settings") if k in d}
     with open(os.path.join(directory, "scalars.json"), "w") as f:
         json.dump(meta, f, indent=1)
 

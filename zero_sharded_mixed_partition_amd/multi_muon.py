@@ -85,11 +85,12 @@ class MultiMuon:
             for a, b in zip(ms, momentums):
                 a.copy_(b)
         updates = [x.view(shape) for x, shape in zip(_slices(dev, update_dtype, sizes), shapes)]
-        scales = [muon_scale(shape, adjust) for shape in shapes]
-        self.table = MatrixTable(updates, None, ms, list(grads), masters, params_out, scales=scales, groups=self.groups)
+        self.scales, self.update_dtype = [muon_scale(shape, adjust) for shape in shapes], update_dtype
+        self.table = MatrixTable(updates, None, ms, list(grads), masters, params_out, scales=self.scales,
+                                 groups=self.groups)
         self.norm_table = TensorTable.of_grads(grads)
         self.masters, self.momentums, self.updates = list(masters), ms, updates
-        self.coefs, self.eps = tuple(tuple(x) for x in coefs), float(eps)
+        self.coefs, self.eps = tuple(tuple(float(c) for c in x) for x in coefs), float(eps)
         self.scaler = scaler if scaler is not None else LossScaler.static(1.0)
         self.t = applied_steps
         self.workspace = torch.empty(max(1, zero_multi_orthogonalize_workspace_bytes(self.table)), dtype=torch.uint8, device=dev)
@@ -106,6 +107,11 @@ class MultiMuon:
     def checkpoint_arrays(self) -> dict:
         return {f"{name}_{i}": x for name, col in (("master", self.masters), ("momentum", self.momentums))
                 for i, x in enumerate(col)}
+
+    def checkpoint_settings(self) -> dict:
+        """What a resumed list has to agree in, as JSON holds it."""
+        return dict(coefs=[list(x) for x in self.coefs], eps=self.eps, scales=list(self.scales),
+                    update_dtype=str(self.update_dtype).replace("torch.", ""))
 
     def _hypers(self):
         return [MuonHyper(**{k: v for k, v in h.items() if k != "max_grad_norm"}) for h in self.hyper]
