@@ -167,6 +167,8 @@ __global__ __launch_bounds__(kBlock) void ortho_load(NsRef ref, int64_t first, d
 // ---------------------------------------------------------------- products
 
 // 16 bytes per lane from base + offset straight into the LDS: lane l's at lds + 16 l.
+// m0 is not in the list of what it clobbers, where the compiler would ignore it: each
+// load sets its own, and a test of the generated code sees that nothing else uses it.
 __device__ __forceinline__ void load_lds(const void* base, uint32_t offset, uint32_t lds) {
     __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
                      :
