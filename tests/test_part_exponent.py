@@ -28,7 +28,7 @@ def test_shifts_do_not_overflow(tmp_path):
         if e > top:
             continue                               # top is the largest of them
         want = 2 * (e - top) if e in FINITE and top in FINITE else 0
-        checks.append(f"static_assert(part_shift({e}, {top}) == {want}, \"\");")
+        checks.append(f"static_assert(({top} == kNotFinite ? 0 : part_shift({e}, {top})) == {want}, \"\");")
     ok, why = compiles(tmp_path, *checks)
     assert ok, why
 
@@ -45,3 +45,4 @@ def test_the_kernels_use_it():
     from zero_sharded_mixed_partition_amd import build as B
     text = open(os.path.join(B.CSRC, "orthogonalize_thin.hip")).read()
     assert "INT_MAX" not in text and "INT_MIN" not in text and text.count("part_shift(") == 2
+    assert "bad = top == kNotFinite" in text and "bad ? 0 : part_shift(exponents[p], top)" in text

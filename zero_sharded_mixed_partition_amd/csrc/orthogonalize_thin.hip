@@ -412,7 +412,7 @@ __global__ __launch_bounds__(64 * Thin<SP>::kWaves2) void thin_steps(NsRef ref, 
 #pragma unroll 8
     for (int p = 0; p < m.n_parts; ++p) {
         const f32x4* part = reinterpret_cast<const f32x4*>(ref.ws + m.parts) + (int64_t)p * H::kTiles * 64;
-        const int down = part_shift(exponents[p], top);
+        const int down = bad ? 0 : part_shift(exponents[p], top);
 #pragma unroll
         for (int k = 0; k < kOwn; ++k) {
             const f32x4 v = part[(wave * kOwn + k) * 64 + lane];

@@ -11,7 +11,7 @@ constexpr int kNotFinite = INT_MAX;              // an inf or a NaN
 constexpr bool has_exponent(int e) { return e >= INT_MIN / 8; }
 
 // The power of two that takes a part's sums to the scale of the parts' largest
-// exponent; 0 where nothing is to be scaled.
-constexpr int part_shift(int e, int top) { return top == kNotFinite || !has_exponent(e) ? 0 : 2 * (e - top); }
+// exponent; 0 for a part of zeros.  Not to be formed where the largest is kNotFinite.
+constexpr int part_shift(int e, int top) { return has_exponent(e) ? 2 * (e - top) : 0; }
 
 }  // namespace zero_shard
