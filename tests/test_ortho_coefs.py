@@ -73,3 +73,11 @@ def test_extreme_coefficients(refused):
                  (0.0, 1e308, 1e-308), (1e-300, 1e-300, 1e-300)):
         assert refused(step), step
     assert not refused((1.0, 1e-320, -1e-320)) and not refused((1.0, 0.0, -1e-300)) and not refused((-1.0, -0.0, 0.0))
+
+
+@pytest.mark.parametrize("kind", [list, tuple, iter, lambda x: (s for s in x)])
+def test_the_binding_counts_each_step(kind):
+    """Also of steps that can be gone through only once: three of two numbers are not two of three."""
+    import zero_sharded_mixed_partition_amd as Z
+    with pytest.raises(ValueError, match="three numbers"):
+        Z.zero_multi_orthogonalize(None, None, coefs=kind([(1.5, -0.5)] * 3))

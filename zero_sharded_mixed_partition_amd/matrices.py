@@ -173,12 +173,13 @@ def zero_multi_orthogonalize(table: MatrixTable, workspace, coefs=ORTHO_COEFS, e
     """Enqueue the orthogonalisation of every matrix of the list: orthos <- X
     after the steps X <- a X + (b X X^T + c (X X^T)^2) X for the (a, b, c) of
     coefs, from X = update / max(its Frobenius norm, eps)."""
-    flat = [float(x) for step in coefs for x in step]
-    if any(len(step) != 3 for step in coefs):
+    steps = [tuple(float(x) for x in step) for step in coefs]
+    if any(len(step) != 3 for step in steps):
         raise ValueError("coefs: three numbers per step expected")
+    flat = [x for step in steps for x in step]
     dev = _current_device()
     _L.check(_L.lib().zero_multi_orthogonalize(*table._ptrs(dev, stream), (ctypes.c_double * max(1, len(flat)))(*flat),
-                                               len(flat) // 3, float(eps),
+                                               len(steps), float(eps),
                                                _buf(global_overflow, torch.int32, 4, "global_overflow", dev),
                                                _buf(workspace, None, 0, "workspace", dev),
                                                workspace.numel() * workspace.element_size(), _stream(stream, dev)),
