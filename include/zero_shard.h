@@ -783,7 +783,7 @@ int zero_multi_adam_step_coef(const void* table, const void* d_table, const void
  *   How far the result of these five is off, besides its own rounding (relative,
  *   Frobenius), for random matrices and for singular values that fall:
  *                                random   1/k      1/k^2    rank 16  rank 3
- *     short side up to 128       1e-5     1e-4     7e-4     6e-5     2e-4
+ *     short side up to 128       2e-5     1e-4     7e-4     6e-5     2e-4
  *     above, update fp16, bf16   1.2e-3   2.5e-3   7.5e-3   3.3e-2   5e-2
  *     above, update fp32         1.3e-3   4.2e-3   2.1e-2   3.4e-2   5e-2
  *   What rounding leaves in the place of a zero or small singular value grows by a

@@ -52,6 +52,21 @@ def test_five_steps(Z, shape, kind, update):
     check(u, got, "f16", M.COEFS)
 
 
+# the header's figures for five steps and short sides above 128: 16-bit updates, fp32
+STATED = {"noise": (1.2e-3, 1.3e-3), "k1": (2.5e-3, 4.2e-3), "k2": (7.5e-3, 2.1e-2), "rank16": (3.3e-2, 3.4e-2), "rank3": (5e-2, 5e-2)}
+
+
+@pytest.mark.parametrize("kind", sorted(STATED))
+@pytest.mark.parametrize("shape", [(200, 210), (512, 512), (520, 1000), (2048, 1024)], ids=ident)
+def test_the_header_says_how_far(Z, shape, kind):
+    """A tenth for matrices other than those measured, and the result's own rounding."""
+    for k, update in ((0, "f16"), (0, "bf16"), (1, "f32")):
+        u, got = result(Z, S.draw(kind, shape, 7), update, "f16", M.COEFS)
+        ref = M.exact(u)
+        norm = float(np.linalg.norm(ref))
+        assert float(np.linalg.norm(got - ref)) <= 1.1 * (STATED[kind][k] * norm + S.stored(ref, "f16")), update
+
+
 @pytest.mark.parametrize("kind", ["noise", "k2", "rank16"])
 @pytest.mark.parametrize("shape", [(64, 300), (200, 210), (512, 512)], ids=ident)
 def test_bf16(Z, shape, kind):
