@@ -25,13 +25,13 @@
 // that fit the CUs, which work off lists of tiles.
 //
 // What bounds it.  14 matrices of 405M elements (8 of 4096 x 4096, 6 of 4096 x
-// 11008), us of a step: X X^T 1383, A A 909, Q X 2853, in tiles of 256; with 2 m n
-// k for a product, half of it for the symmetric ones, 1.06 to 1.2e15 a second,
+// 11008), us of a step: X X^T 1460, A A 978, Q X 2916, in tiles of 256; with 2 m n
+// k for a product, half of it for the symmetric ones, 0.98 to 1.14e15 a second,
 // where the loops between a tile's first loads and its stores run at 1.5e15,
-// about what a large matrix product of a library reaches.  The MFMAs are busy 62
-// to 77% of the time at 1.7 GHz, to which the power limit takes the clock from 2.4:
+// about what a large matrix product of a library reaches.  The MFMAs are busy 58
+// to 69% of the time at 1.7 GHz, to which the power limit takes the clock from 2.4:
 // more waves, deeper stages and the larger MFMA gain nothing, 32 x 32 x 16 loses 4%.
-// HBM is not what bounds: Q X reads and writes 6.1 GB in 2.9 ms.  Small lists are
+// HBM is not what bounds: Q X reads and writes 6.2 GB in 2.9 ms.  Small lists are
 // bound by their 2 + 3 n_steps launches of 4 to 6 us, one after the other.
 #include <hip/hip_runtime.h>
 
@@ -67,7 +67,7 @@ __device__ __forceinline__ void load_piece(const ZS_CONSTANT MatrixItem& m, int 
 }
 
 // One piece's sum of squares into its slot.  A read of U: 405M elements of bf16,
-// 810 MB, take 127 us, 6.4 TB/s.
+// 810 MB, take 129 us, 6.3 TB/s.
 __global__ __launch_bounds__(kBlock) void ortho_squares(NsRef ref, int64_t first) {
     if (ref.skipped()) return;
     __shared__ double s_sq[kWaves];
@@ -114,10 +114,10 @@ __device__ __forceinline__ double* start_factor(const NsRef& ref, const ZS_CONST
 // With all of it here U would be rounded to fp16 once more, and what that leaves in
 // a zero singular value's place grows by a in every step: 512 x 512, 1 / k^2, 2.0e-2
 // instead of 7.3e-3 off.
-// A read and a write: 405M elements
-// take 334 us, 4.9 TB/s.  Each block forms the norm again from the slots, 2752 of
-// them for 4096 x 11008, behind its loads; a launch of its own would take 4 us.
-// Bands of 8 rows at a time, so that a wave's stores fill whole rows of a panel.
+// A read and a write: 405M elements take 336 to 358 us, 4.5 to 4.8 TB/s.  Each block
+// forms the norm again from the slots, 2752 of them for 4096 x 11008, behind its
+// loads; a launch of its own would take 4 us.  Bands of 8 rows at a time, so that a
+// wave's stores fill whole rows of a panel.
 __global__ __launch_bounds__(kBlock) void ortho_load(NsRef ref, int64_t first, double eps) {
     if (ref.skipped()) return;
     __shared__ double s_sq[kWaves];
